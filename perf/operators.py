@@ -116,11 +116,15 @@ def _sizes(case):
 
 def _hash(seed, count, device):
     """The stochastic rounding's 32 random bits of state element i (in 64-bit integers)."""
-    low = 0xFFFFFFFF
+    whole, low = (1 << 64) - 1, 0xFFFFFFFF
+    z = seed + 0x9E3779B97F4A7C15 & whole
+    z = (z ^ z >> 30) * 0xBF58476D1CE4E5B9 & whole
+    z = (z ^ z >> 27) * 0x94D049BB133111EB & whole
+    z ^= z >> 31
     i = torch.arange(count, device=device, dtype=torch.int64)
-    x = ((i & low) ^ ((i >> 32) * 0x9E3779B1 & low)) + (seed & low) & low
+    x = (i & low) ^ ((z & low) + (i >> 32) * 0x9E3779B1 & low)
     x = (x ^ x >> 16) * 0x7FEB352D & low
-    x = (x ^ x >> 15) ^ (seed >> 32 & low)
+    x = (x ^ x >> 15) ^ z >> 32
     x = x * 0x846CA68B & low
     return x ^ x >> 16
 
@@ -295,9 +299,9 @@ def _plain_adamw(s):
     else:               # the codes are decided in 64 bits: a value next to a border takes the same side everywhere
         g = s["g"].double()
         c8, ms, vs = s["m"].double(), s["ms"].double(), s["vs"].double()
-        m = (c8 * c8.abs()).view(-1, BLOCK) * (ms / 127.0 ** 2).view(-1, 1)
+        m = (c8 * c8.abs()).view(-1, BLOCK) * (ms * (1.0 / 127.0 ** 2)).view(-1, 1)
         m = a["beta1"] * m.view(-1) + (1.0 - a["beta1"]) * g
-        v = s["v"].double().pow(4).view(-1, BLOCK) * (vs / 255.0 ** 4).view(-1, 1)
+        v = s["v"].double().pow(4).view(-1, BLOCK) * (vs * (1.0 / 255.0 ** 4)).view(-1, 1)
         v = a["beta2"] * v.view(-1) + (1.0 - a["beta2"]) * g * g
         um, uv = _offsets(_hash(s["step"], m.numel(), m.device))
         cm, ms = _encode(m.abs(), 2, 127.0, um)
@@ -307,8 +311,8 @@ def _plain_adamw(s):
         s["v"].copy_(cv.view(-1))
         s["ms"].copy_(ms.view(-1))
         s["vs"].copy_(vs.view(-1))
-        out = [(cm * cm.abs() * (ms.double() / 127.0 ** 2)).float().view(-1),
-               (cv.pow(4) * (vs.double() / 255.0 ** 4)).float().view(-1)]
+        out = [(cm * cm.abs() * (ms.double() * (1.0 / 127.0 ** 2))).float().view(-1),
+               (cv.pow(4) * (vs.double() * (1.0 / 255.0 ** 4))).float().view(-1)]
         m, v = m.float(), v.float()
     p = p * (1.0 - a["lr"] * a["weight_decay"]) - a["lr"] * (m / bc1) / ((v / bc2).sqrt() + a["eps"])
     s["p"].copy_(p)
