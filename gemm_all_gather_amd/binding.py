@@ -74,6 +74,49 @@ class GemmOptions(ctypes.Structure):
     _fields_ = [("b_layout", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)]
 
 
+AG_ACT_NONE, AG_ACT_RELU, AG_ACT_GELU, AG_ACT_GELU_TANH, AG_ACT_SILU = range(5)
+ACTS = {"none": AG_ACT_NONE, "relu": AG_ACT_RELU, "gelu": AG_ACT_GELU, "gelu_tanh": AG_ACT_GELU_TANH,
+        "silu": AG_ACT_SILU}
+AG_ADAMW_BLOCK = 256
+
+
+def _fields(ctype, names):
+    return [(name, ctype) for name in names.split()]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "x w bias residual y z") +
+                _fields(ctypes.c_int64, "ldx ldw ldr ldy ldz M N K") +
+                _fields(ctypes.c_int32, "dtype act") + [("reserved", ctypes.c_int32 * 6)])
+
+
+class LinearBackwardArgs(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "dy z x w dx dw db") +
+                _fields(ctypes.c_int64, "lddy ldz ldx ldw lddx lddw M N K") +
+                _fields(ctypes.c_int32, "dtype act dw_dtype accumulate") + [("reserved", ctypes.c_int32 * 4)])
+
+
+class ProductPlan(ctypes.Structure):
+    _fields_ = _fields(ctypes.c_int32, "variant tile_m tile_n tile_k splits n_programs packed reserved")
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = ([("product", ProductPlan), ("product_dw", ProductPlan)] +
+                _fields(ctypes.c_uint64, "workspace_bytes bytes_read bytes_written") +
+                [("flops", ctypes.c_double)] + _fields(ctypes.c_int32, "launches reserved"))
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "param grad exp_avg exp_avg_sq exp_avg_scale exp_avg_sq_scale master") +
+                [("n", ctypes.c_int64)])
+
+
+class AdamwHyper(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_double, "lr beta1 beta2 eps weight_decay grad_scale") +
+                [("step", ctypes.c_int64)] + _fields(ctypes.c_void_p, "dev_step dev_lr dev_grad_scale") +
+                [("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)])
+
+
 def _options(dest_group=0, schedule=0, tile_order=0) -> CopyOptions:
     o = CopyOptions()
     o.dest_group = dest_group
@@ -129,6 +172,14 @@ _SIGNATURES = {
     "ag_plan_gemm_all_gather_ex": [ctypes.POINTER(Geometry), _c_int, _c_int, _c_int, _c_u64, _c_i64, _c_u64,
                                    _c_i64, _c_size, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int,
                                    ctypes.POINTER(GemmOptions), ctypes.POINTER(Plan)],
+    "ag_linear": [ctypes.POINTER(LinearArgs), _vp, _c_size, _vp],
+    "ag_plan_linear": [ctypes.POINTER(LinearArgs), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _vp, _c_size, _vp],
+    "ag_plan_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_adamw_create": [ctypes.POINTER(AdamwTensor), _c_i64, _c_int, _c_int, _c_int, _HEAP_PP],
+    "ag_adamw_destroy": [_vp],
+    "ag_adamw_step": [_vp, ctypes.POINTER(AdamwHyper), _vp],
+    "ag_adamw_read_states": [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp],
 }
 
 
@@ -391,3 +442,134 @@ def gemm_all_gather_ex(heap: Heap, W, rank_start, rank_stride, A, lda, B, ldb, o
     _check(lib().ag_gemm_all_gather_ex(heap.handle, W, rank_start, rank_stride, _ptr(A), lda, _ptr(B), ldb,
                                        out_offset, M_local, N, K, _dtype(dtype), tile_m, tile_n, tile_k, n_programs,
                                        ctypes.byref(o), _stream(stream)), "ag_gemm_all_gather_ex")
+
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else act
+
+
+def _workspace(workspace):
+    """Address and bytes of a workspace: a tensor, or None."""
+    if workspace is None:
+        return 0, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _linear_args(M, N, K, dtype, act, x, w, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz) -> LinearArgs:
+    return LinearArgs(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z), ldx, ldw, ldr, ldy, ldz, M, N, K,
+                      _dtype(dtype), _act(act))
+
+
+def plan_linear(x, w, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0, ldy=0,
+                ldz=0, num_cus=0) -> LinearPlan:
+    p = LinearPlan()
+    a = _linear_args(M, N, K, dtype, act, x, w, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    _check(lib().ag_plan_linear(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_linear")
+    return p
+
+
+def linear(x, w, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0, ldy=0, ldz=0,
+           workspace=None, stream=None) -> None:
+    """y = act(x w^T + bias) + residual; z, if given, receives the pre-activation (ag_linear)."""
+    a = _linear_args(M, N, K, dtype, act, x, w, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_linear(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear")
+
+
+def _backward_args(M, N, K, dtype, act, dy, x, w, z, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw, dw_dtype,
+                   accumulate) -> LinearBackwardArgs:
+    return LinearBackwardArgs(_ptr(dy), _ptr(z), _ptr(x), _ptr(w), _ptr(dx), _ptr(dw), _ptr(db), lddy, ldz, ldx, ldw,
+                              lddx, lddw, M, N, K, _dtype(dtype), _act(act),
+                              _dtype(dtype if dw_dtype is None else dw_dtype), int(accumulate))
+
+
+def plan_linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=None, db=None, lddy=0, ldx=0, ldw=0,
+                         ldz=0, lddx=0, lddw=0, dw_dtype=None, accumulate=False, num_cus=0) -> LinearPlan:
+    p = LinearPlan()
+    a = _backward_args(M, N, K, dtype, act, dy, x, w, z, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw, dw_dtype,
+                       accumulate)
+    _check(lib().ag_plan_linear_backward(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_linear_backward")
+    return p
+
+
+def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=None, db=None, lddy=0, ldx=0, ldw=0,
+                    ldz=0, lddx=0, lddw=0, dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
+    """The gradients dx, dw and db that are given, from dy and the stored pre-activation z (ag_linear_backward)."""
+    a = _backward_args(M, N, K, dtype, act, dy, x, w, z, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw, dw_dtype,
+                       accumulate)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_linear_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_backward")
+
+
+class AdamW:
+    """ag_adamw: a device table of tensors, made once; ``step`` updates all of them in one launch.
+
+    Lists of device tensors of equal lengths, each contiguous; 8-bit states are int8 and uint8 tensors with their
+    fp32 block maxima in exp_avg_scales and exp_avg_sq_scales.  The tensors are kept alive here and must keep
+    their addresses (clear gradients in place).
+    """
+
+    def __init__(self, params, grads, exp_avgs, exp_avg_sqs, masters=None, exp_avg_scales=None,
+                 exp_avg_sq_scales=None):
+        import torch
+        lists = [params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, masters]
+        params = list(params)
+        count = len(params)
+        state8 = count > 0 and exp_avgs[0].dtype == torch.int8
+        wanted = [None, None, torch.int8 if state8 else torch.float32, torch.uint8 if state8 else torch.float32,
+                  torch.float32, torch.float32, torch.float32]
+        for part, dtype in zip(lists, wanted):
+            if part is None:
+                continue
+            if len(part) != count:
+                raise ValueError("the lists of tensors differ in length")
+            for t, p in zip(part, params):
+                need = -(-p.numel() // AG_ADAMW_BLOCK) if part is exp_avg_scales or part is exp_avg_sq_scales \
+                    else p.numel()
+                if not t.is_contiguous() or t.numel() != need or t.dtype != (dtype or part[0].dtype):
+                    raise ValueError(f"a tensor is not contiguous, not of {need} elements or not {dtype or part[0].dtype}")
+        table = (AdamwTensor * max(1, count))()
+        for i, p in enumerate(params):
+            table[i] = AdamwTensor(*(_ptr(part[i]) if part is not None else 0 for part in lists), p.numel())
+        h = ctypes.c_void_p()
+        _check(lib().ag_adamw_create(table, count, _dtype(params[0].dtype) if count else AG_F32,
+                                     _dtype(grads[0].dtype) if count else AG_F32, 8 if state8 else 32,
+                                     ctypes.byref(h)), "ag_adamw_create")
+        self._h = h
+        self._keepalive = lists
+        self._count = count
+
+    def destroy(self) -> None:
+        if self._h is not None and self._h.value:
+            lib().ag_adamw_destroy(self._h)
+        self._h = None
+
+    close = destroy
+
+    def __del__(self):
+        try:
+            if getattr(self, "_h", None) is not None and _lib is not None:
+                _lib.ag_adamw_destroy(self._h)
+                self._h = None
+        except Exception:
+            pass
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        if self._h is None:
+            raise RuntimeError("optimizer handle already destroyed")
+        return self._h
+
+    def step(self, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0, seed=None,
+             dev_step=None, dev_lr=None, dev_grad_scale=None, stream=None) -> None:
+        """One AdamW step; a seed (8-bit states) turns stochastic rounding on (ag_adamw_step)."""
+        y = AdamwHyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step, _ptr(dev_step), _ptr(dev_lr),
+                       _ptr(dev_grad_scale), 0 if seed is None else seed, 0 if seed is None else 1)
+        _check(lib().ag_adamw_step(self.handle, ctypes.byref(y), _stream(stream)), "ag_adamw_step")
+
+    def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:
+        """The fp32 values of 8-bit states, into two lists of fp32 tensors (ag_adamw_read_states)."""
+        m, v = ((_vp * max(1, self._count))(*(_ptr(t) for t in part)) for part in (exp_avgs, exp_avg_sqs))
+        if len(exp_avgs) != self._count or len(exp_avg_sqs) != self._count:
+            raise ValueError("the lists of tensors differ in length")
+        _check(lib().ag_adamw_read_states(self.handle, m, v, _stream(stream)), "ag_adamw_read_states")

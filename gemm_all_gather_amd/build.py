@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libag.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["ag_host.cpp", "ag_copy.hip", "ag_gemm.hip", "ag_util.hip"]
+SOURCES = ["ag_host.cpp", "ag_copy.hip", "ag_gemm.hip", "ag_util.hip", "ag_linear_host.cpp", "ag_linear.hip",
+           "ag_adamw_host.cpp", "ag_adamw.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

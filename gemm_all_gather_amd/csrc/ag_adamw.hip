@@ -1,0 +1,374 @@
+// AdamW over many tensors in one launch (gfx950).
+//
+// A workgroup takes one chunk of one tensor, found through a device table made with the handle.  A
+// lane holds 8 consecutive elements, so that 32 lanes hold one block of 8-bit states.  Every element is
+// read once and written once; the kernel is bound by HBM.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ag.h"
+#include "ag_adamw.h"
+
+namespace ag {
+namespace {
+
+static_assert(AG_ADAMW_BLOCK == 256, "32 lanes of 8 elements");
+static_assert(kAdamwChunk % (256 * 8) == 0, "whole passes of a workgroup");
+
+// Vectors of 8 elements at any alignment of the element (global accesses need none on gfx950).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) Any16f { u32x4 v; };
+struct __attribute__((packed, aligned(1))) Any8 { u32x2 v; };
+
+template <int DT> struct Type;      // ag_dtype_t
+template <> struct Type<AG_F32> {
+    using T = float;
+    static __device__ __forceinline__ void load(float (&x)[8], const float* p)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 t = reinterpret_cast<const Any16f*>(p + 4 * h)->v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * h + e] = __uint_as_float(t[e]);
+        }
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&x)[8])
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = __float_as_uint(x[4 * h + e]);
+            reinterpret_cast<Any16f*>(p + 4 * h)->v = t;
+        }
+    }
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <bool BF16> struct Half {
+    using T = uint16_t;
+    static __device__ __forceinline__ float get(uint16_t v)
+    {
+        if constexpr (BF16) return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
+        else return static_cast<float>(__builtin_bit_cast(_Float16, v));
+    }
+    static __device__ __forceinline__ uint16_t put(float v)    // to nearest, ties to even
+    {
+        if constexpr (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+        else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    }
+    static __device__ __forceinline__ void load(float (&x)[8], const uint16_t* p)
+    {
+        const u32x4 t = reinterpret_cast<const Any16*>(p)->v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = get(static_cast<uint16_t>(t[e / 2] >> (16 * (e & 1))));
+    }
+    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[8])
+    {
+        u32x4 t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            t[e] = static_cast<uint32_t>(put(x[2 * e])) | (static_cast<uint32_t>(put(x[2 * e + 1])) << 16);
+        reinterpret_cast<Any16*>(p)->v = t;
+    }
+};
+template <> struct Type<AG_F16> : Half<false> {};
+template <> struct Type<AG_BF16> : Half<true> {};
+
+template <int DT>
+__device__ __forceinline__ void load8(float (&x)[8], const void* base, int64_t at, int n)
+{
+    const typename Type<DT>::T* p = static_cast<const typename Type<DT>::T*>(base) + at;
+    if (n >= 8) {
+        Type<DT>::load(x, p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = e < n ? Type<DT>::get(p[e]) : 0.f;
+    }
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[8], int n)
+{
+    typename Type<DT>::T* p = static_cast<typename Type<DT>::T*>(base) + at;
+    if (n >= 8) {
+        Type<DT>::store(p, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = Type<DT>::put(x[e]);
+    }
+}
+__device__ __forceinline__ uint64_t load_codes(const void* base, int64_t at, int n)
+{
+    const uint8_t* p = static_cast<const uint8_t*>(base) + at;
+    if (n >= 8) return __builtin_bit_cast(uint64_t, reinterpret_cast<const Any8*>(p)->v);
+    uint64_t c = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n) c |= static_cast<uint64_t>(p[e]) << (8 * e);
+    return c;
+}
+__device__ __forceinline__ void store_codes(void* base, int64_t at, uint64_t c, int n)
+{
+    uint8_t* p = static_cast<uint8_t*>(base) + at;
+    if (n >= 8) {
+        reinterpret_cast<Any8*>(p)->v = __builtin_bit_cast(u32x2, c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = static_cast<uint8_t>(c >> (8 * e));
+    }
+}
+
+// The step's scalars: the host's, or made anew from what device scalars hold.
+__device__ __forceinline__ AdamwScalars scalars(const AdamwArgs& a)
+{
+    if (!a.dev_step && !a.dev_lr && !a.dev_grad_scale) return a.scalars;   // uniform
+    double lr = a.lr, gs = a.grad_scale, bias1 = a.bias1, bias2 = a.bias2;
+    AdamwScalars s = a.scalars;
+    if (a.dev_step) {
+        const int64_t step = *a.dev_step;
+        s.seed = adamw_mix_seed(a.seed + static_cast<uint64_t>(step));
+        bias1 = 1.0 - pow(a.beta1, static_cast<double>(step));
+        bias2 = 1.0 - pow(a.beta2, static_cast<double>(step));
+    }
+    if (a.dev_lr) lr = *a.dev_lr;
+    if (a.dev_grad_scale) gs *= *a.dev_grad_scale;
+    s.decay = static_cast<float>(1.0 - lr * a.weight_decay);
+    s.rate = static_cast<float>(lr / bias1);
+    s.inv_bias2 = static_cast<float>(1.0 / bias2);
+    s.grad_scale = static_cast<float>(gs);
+    return s;
+}
+
+__device__ __forceinline__ float update(float p, float m, float v, const AdamwScalars& s)
+{
+    return p * s.decay - s.rate * m / (sqrtf(v * s.inv_bias2) + s.eps);
+}
+
+// 32 random bits of the state element at place i (counted over all tensors' blocks): multiply and xor-shift
+// rounds.  The seed comes in mixed (adamw_mix_seed), half before and half between the rounds, so that seeds that
+// count up give unrelated bits at every place.
+__device__ __forceinline__ uint32_t random_bits(uint64_t mixed_seed, uint64_t i)
+{
+    uint32_t x = static_cast<uint32_t>(i) ^ (static_cast<uint32_t>(mixed_seed) + static_cast<uint32_t>(i >> 32) * 0x9E3779B1u);
+    x = (x ^ (x >> 16)) * 0x7FEB352Du;
+    x = (x ^ (x >> 15)) ^ static_cast<uint32_t>(mixed_seed >> 32);
+    x = x * 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+// The code floor(t + u), t = top * r^(1/POWER), of r = value / maximum in [0, 1], u in (0, 1) a multiple of 2^-17.
+// t is found in fp32 (error below 6e-5).  Where t + u lies within 2.5e-4 of a whole number, which side
+// it is on is decided in fp64 by comparing r top^POWER with (k - u)^POWER: the code is that of exact
+// arithmetic on r, so it depends on no instruction's last bit.
+template <int POWER>
+__device__ __forceinline__ int encode(double r, float u)
+{
+    constexpr float top = POWER == 2 ? 127.f : 255.f;
+    float t = __builtin_amdgcn_sqrtf(static_cast<float>(r));
+    if (POWER == 4) t = __builtin_amdgcn_sqrtf(t);
+    const float x = t * top + u;
+    float k = floorf(x);
+    const float near = rintf(x);
+    if (fabsf(x - near) < 2.5e-4f) {
+        const double b = static_cast<double>(near) - static_cast<double>(u);
+        const double b2 = b * b;
+        const bool reached = b <= 0.0 || (POWER == 2 ? r * (127.0 * 127.0) >= b2 : r * (255.0 * 255.0 * 255.0 * 255.0) >= b2 * b2);
+        k = reached ? near : near - 1.f;
+    }
+    return static_cast<int>(fminf(k, top));
+}
+
+// Largest of the 32 lanes of a block.  Bit patterns of non-negative floats compare as integers, and a NaN's is above all.
+__device__ __forceinline__ uint32_t block_max(uint32_t v)
+{
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d, 64));
+        v = v > o ? v : o;
+    }
+    return v;
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+constexpr double kCodeM = 1.0 / (127.0 * 127.0), kCodeV = 1.0 / (255.0 * 255.0 * 255.0 * 255.0);
+
+// beta x + y, each operation rounded to fp64 by itself.  A block's maximum often lies exactly between two
+// fp32 numbers (0.9 S + 0.1 g of short significands); its side, and with it the codes' scale, is then the
+// rounding's, and a fused operation's would differ from what the same formula gives elsewhere.
+__device__ __forceinline__ double blend(double beta, double x, double y)
+{
+#pragma clang fp contract(off)
+    const double bx = beta * x;
+    return bx + y;
+}
+
+template <int P, int G, bool MASTER, bool S8>
+__global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
+{
+    const AdamwChunk c = a.chunks[blockIdx.x];
+    const AdamwEntry t = a.entries[c.tensor];
+    const AdamwScalars s = scalars(a);
+#pragma unroll
+    for (int pass = 0; pass < kAdamwChunk / 2048; ++pass) {
+        const int64_t at = static_cast<int64_t>(c.chunk) * kAdamwChunk + pass * 2048 + threadIdx.x * 8;
+        // lanes past the end take part in their block's maximum with zeros
+        const int64_t left = t.n - at;
+        const int n = static_cast<int>(left < 0 ? 0 : left > 8 ? 8 : left);
+        if (!S8 && n == 0) return;
+        float p[8], g[8];
+        load8<G>(g, t.grad, n ? at : 0, n);
+        if constexpr (MASTER) load8<AG_F32>(p, t.master, n ? at : 0, n);
+        else load8<P>(p, t.param, n ? at : 0, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= s.grad_scale;
+
+        if constexpr (!S8) {
+            float m[8], v[8];
+            load8<AG_F32>(m, t.exp_avg, at, n);
+            load8<AG_F32>(v, t.exp_avg_sq, at, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                m[e] = s.b1 * m[e] + s.one_minus_b1 * g[e];
+                v[e] = s.b2 * v[e] + s.one_minus_b2 * g[e] * g[e];
+                p[e] = update(p[e], m[e], v[e], s);
+            }
+            store8<AG_F32>(t.exp_avg, at, m, n);
+            store8<AG_F32>(t.exp_avg_sq, at, v, n);
+        } else {
+            const int64_t block = at / AG_ADAMW_BLOCK;
+            const bool block_live = block * AG_ADAMW_BLOCK < t.n;
+            const uint64_t mc = load_codes(t.exp_avg, n ? at : 0, n), vc = load_codes(t.exp_avg_sq, n ? at : 0, n);
+            const double ms = block_live ? t.exp_avg_scale[block] * kCodeM : 0.0;
+            const double vs = block_live ? t.exp_avg_sq_scale[block] * kCodeV : 0.0;
+            double m[8], v[8];
+            uint32_t mmax = 0, vmax = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int cm = static_cast<int8_t>(mc >> (8 * e));
+                const uint32_t cv = static_cast<uint32_t>(vc >> (8 * e)) & 0xffu;
+                m[e] = blend(a.beta1, static_cast<double>(cm * abs(cm)) * ms, a.one_minus_beta1 * g[e]);
+                v[e] = blend(a.beta2, static_cast<double>(cv * cv * cv * cv) * vs, a.one_minus_beta2 * g[e] * g[e]);
+                const uint32_t mb = __builtin_bit_cast(uint32_t, static_cast<float>(m[e])) & 0x7fffffffu;
+                const uint32_t vb = __builtin_bit_cast(uint32_t, static_cast<float>(v[e])) & 0x7fffffffu;
+                mmax = mmax > mb ? mmax : mb;
+                vmax = vmax > vb ? vmax : vb;
+                p[e] = update(p[e], static_cast<float>(m[e]), static_cast<float>(v[e]), s);
+            }
+            mmax = block_max(mmax);
+            vmax = block_max(vmax);
+            // a block that holds an infinity or a NaN reads back as NaN: all codes 0, the maximum NaN
+            const bool mfine = mmax < kInfBits, vfine = vmax < kInfBits;
+            const float mS = mfine ? __builtin_bit_cast(float, mmax) : __builtin_nanf("");
+            const float vS = vfine ? __builtin_bit_cast(float, vmax) : __builtin_nanf("");
+            const double mi = mfine && mmax != 0 ? 1.0 / static_cast<double>(mS) : 0.0;
+            const double vi = vfine && vmax != 0 ? 1.0 / static_cast<double>(vS) : 0.0;
+            uint64_t mo = 0, vo = 0;
+            const uint64_t place = (static_cast<uint64_t>(t.first_block) * AG_ADAMW_BLOCK) + static_cast<uint64_t>(at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float um = 0.5f, uv = 0.5f;
+                if (a.stochastic) {   // uniform
+                    const uint32_t bits = random_bits(s.seed, place + e);
+                    um = static_cast<float>(2 * (bits & 0xffffu) + 1) * (1.f / 131072.f);
+                    uv = static_cast<float>(2 * (bits >> 16) + 1) * (1.f / 131072.f);
+                }
+                int km = mfine ? encode<2>(fabs(m[e]) * mi, um) : 0;
+                int kv = vfine ? encode<4>(v[e] * vi, uv) : 0;
+                if (vfine && v[e] > 0.0 && kv < 1) kv = 1;
+                if (m[e] < 0.0) km = -km;
+                mo |= static_cast<uint64_t>(static_cast<uint8_t>(km)) << (8 * e);
+                vo |= static_cast<uint64_t>(static_cast<uint8_t>(kv)) << (8 * e);
+            }
+            store_codes(t.exp_avg, at, mo, n);
+            store_codes(t.exp_avg_sq, at, vo, n);
+            if (block_live && (threadIdx.x & 31) == 0) {
+                t.exp_avg_scale[block] = mS;
+                t.exp_avg_sq_scale[block] = vS;
+            }
+        }
+        if constexpr (MASTER) store8<AG_F32>(t.master, at, p, n);
+        store8<P>(t.param, at, p, n);
+    }
+}
+
+__global__ __launch_bounds__(256) void ag_adamw_read_kernel(AdamwReadArgs a)
+{
+    int lo = 0, hi = a.count;                 // the tensor whose groups hold this one
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.first_group[mid] <= blockIdx.x) lo = mid;
+        else hi = mid;
+    }
+    const AdamwEntry t = a.entries[lo];
+    float* mo = a.exp_avg[lo];
+    float* vo = a.exp_avg_sq[lo];
+    const int64_t at = (static_cast<int64_t>(blockIdx.x - a.first_group[lo]) * 256 + threadIdx.x) * 8;
+    const int64_t left = t.n - at;
+    if (left <= 0) return;
+    const int n = static_cast<int>(left > 8 ? 8 : left);
+    const uint64_t mc = load_codes(t.exp_avg, at, n), vc = load_codes(t.exp_avg_sq, at, n);
+    const double ms = t.exp_avg_scale[at / AG_ADAMW_BLOCK] * kCodeM;
+    const double vs = t.exp_avg_sq_scale[at / AG_ADAMW_BLOCK] * kCodeV;
+    float m[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int cm = static_cast<int8_t>(mc >> (8 * e));
+        const uint32_t cv = static_cast<uint32_t>(vc >> (8 * e)) & 0xffu;
+        m[e] = static_cast<float>(static_cast<double>(cm * abs(cm)) * ms);
+        v[e] = static_cast<float>(static_cast<double>(cv * cv * cv * cv) * vs);
+    }
+    store8<AG_F32>(mo, at, m, n);
+    store8<AG_F32>(vo, at, v, n);
+}
+
+using AdamwFn = void (*)(AdamwArgs);
+template <int P, int G> AdamwFn pick_state(bool master, bool s8)
+{
+    if constexpr (P == AG_F32) {
+        if (master) return nullptr;
+        return s8 ? ag_adamw_kernel<P, G, false, true> : ag_adamw_kernel<P, G, false, false>;
+    } else {
+        if (master) return s8 ? ag_adamw_kernel<P, G, true, true> : ag_adamw_kernel<P, G, true, false>;
+        return s8 ? ag_adamw_kernel<P, G, false, true> : ag_adamw_kernel<P, G, false, false>;
+    }
+}
+template <int P> AdamwFn pick_grad(int g, bool master, bool s8)
+{
+    switch (g) {
+    case AG_F16: return pick_state<P, AG_F16>(master, s8);
+    case AG_BF16: return pick_state<P, AG_BF16>(master, s8);
+    case AG_F32: return pick_state<P, AG_F32>(master, s8);
+    default: return nullptr;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwLaunch& l, hipStream_t stream)
+{
+    AdamwFn fn = nullptr;
+    switch (l.param) {
+    case AG_F16: fn = pick_grad<AG_F16>(l.grad, l.master != 0, l.state8 != 0); break;
+    case AG_BF16: fn = pick_grad<AG_BF16>(l.grad, l.master != 0, l.state8 != 0); break;
+    case AG_F32: fn = pick_grad<AG_F32>(l.grad, l.master != 0, l.state8 != 0); break;
+    default: break;
+    }
+    if (fn == nullptr || l.chunks < 1 || l.chunks > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(l.chunks)), dim3(256), 0, stream, l.args);
+    return hipGetLastError();
+}
+
+hipError_t launch_adamw_read(const AdamwReadArgs& a, hipStream_t stream)
+{
+    const uint32_t groups = a.first_group[a.count];
+    if (a.count < 1 || groups < 1) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ag_adamw_read_kernel, dim3(groups), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace ag

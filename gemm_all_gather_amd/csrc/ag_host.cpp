@@ -20,12 +20,15 @@
 
 #include "ag.h"
 #include "ag_internal.h"
+#include "ag_status.h"
 
 static_assert(AG_NOALLOC_MAX_RANKS == ag::kNoAllocMaxRanks, "one limit for the allocation-free entry point");
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace ag {
 
 ag_status_t ok()
 {
@@ -33,7 +36,6 @@ ag_status_t ok()
     return AG_OK;
 }
 
-ag_status_t fail(ag_status_t s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ag_status_t fail(ag_status_t s, const char* fmt, ...)
 {
     char buf[512];
@@ -50,6 +52,14 @@ ag_status_t fail_hip(hipError_t e, const char* what)
     const ag_status_t s = (e == hipErrorOutOfMemory) ? AG_ERR_OUT_OF_MEMORY : AG_ERR_HIP;
     return fail(s, "%s failed: %s (%d)", what, hipGetErrorString(e), static_cast<int>(e));
 }
+
+}  // namespace ag
+
+namespace {
+
+using ag::fail;
+using ag::fail_hip;
+using ag::ok;
 
 bool is_pow2(uint64_t v) { return v != 0 && (v & (v - 1)) == 0; }
 int log2_exact(uint64_t v)

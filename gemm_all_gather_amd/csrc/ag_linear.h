@@ -1,0 +1,79 @@
+// Internal interface between the linear layer's host code (ag_linear_host.cpp)
+// and its kernels (ag_linear.hip).  Not part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ag {
+
+// What happens to a product's fp32 element before it is stored.
+struct LinearEpilogue {
+    const uint16_t* bias;       // per column, or null
+    const uint16_t* residual;   // or null
+    uint16_t* z;                // pre-activation output, or null
+    void* out;
+    int64_t ldr, ldz, ldo;
+    int32_t act;                // ag_act_t
+    int32_t out_f32;            // out holds fp32, else the operands' type
+    int32_t accumulate;         // out += instead of out =
+    int32_t reserved;
+};
+
+// out(i, j) = epilogue(sum_r A(i, r) B(j, r)).
+struct LinearGemmArgs {
+    const uint16_t* A;          // element (i, r) at A[i*lda + r], or A[r*lda + i] (transposed kernels)
+    const uint16_t* B;          // element (j, r) at B[j*ldb + r], or B[r*ldb + j]
+    int64_t lda, ldb;
+    int64_t I, J, R;
+    int32_t tiles_i, tiles_j;
+    int32_t splits;             // parts of the reduction
+    int32_t stages_per_split;   // 64-wide steps of a part
+    float* partial;             // splits > 1: part s at partial + s*I*partial_ld, rows of partial_ld
+    int64_t partial_ld;
+    LinearEpilogue epi;
+};
+
+enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1 };
+enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
+
+hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream);
+// Joins the parts of a split product in order and applies the epilogue.
+hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, hipStream_t stream);
+
+// Row streaming: out(m, n) for few rows m of x (I = N, J = M <= kLinearStreamRows).
+constexpr int kLinearStreamRows = 32;
+struct LinearStreamArgs {
+    const uint16_t* x;
+    const uint16_t* w;
+    int64_t ldx, ldw;
+    int64_t M, N, K;
+    LinearEpilogue epi;
+};
+hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, hipStream_t stream);
+
+// Copies rows to aligned rows (ld_dst a multiple of 8).
+hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
+                              int64_t cols, hipStream_t stream);
+
+// dz = dy * act'(z), rounded, and the column sums of the unrounded dz over row blocks.
+constexpr int kLinearSlopeRows = 64;   // rows of one partial column sum
+struct LinearSlopeArgs {
+    const uint16_t* dy;
+    const uint16_t* z;          // null when act is none
+    uint16_t* dz;               // null: not stored
+    float* sums;                // ceil(M / kLinearSlopeRows) rows of N, or null
+    int64_t lddy, ldz, lddz;
+    int64_t M, N;
+    int32_t act;
+    int32_t reserved;
+};
+hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
+// db(n) (+)= sum over parts of sums(part, n).
+hipError_t launch_linear_bias_grad(const float* sums, int64_t parts, int64_t N, void* db, int db_kind /* 0 f16, 1 bf16, 2 f32 */,
+                                   int accumulate, hipStream_t stream);
+
+// Tile shape and threads of a tile configuration (host-only).
+void linear_tile_shape(int tile, int* tm, int* tn, int* threads);
+
+}  // namespace ag

@@ -1,7 +1,9 @@
 /*
  * ag.h -- C ABI of libag: a symmetric heap of logical ranks on one MI355X
- * (gfx950), a persistent tiled multi-destination all-gather, and a tiled
- * GEMM whose epilogue performs the same multi-destination store.
+ * (gfx950), a persistent tiled multi-destination all-gather, a tiled GEMM
+ * whose epilogue performs the same multi-destination store, and what a rank
+ * trains with between collectives: a linear layer with its epilogue, its
+ * gradients, and an AdamW step over many tensors.
  *
  * Sources (the three pages on the iris all-gather):
  *  - ROCm/iris #626, "Summary": the device-side all-gather loads the local
@@ -463,6 +465,196 @@ ag_status_t ag_plan_gemm_all_gather_ex(const ag_heap_geometry_t* geom, int W, in
                                        size_t out_offset, int64_t M_local, int64_t N, int64_t K,
                                        ag_dtype_t dtype, int tile_m, int tile_n, int tile_k,
                                        int n_programs, const ag_gemm_options_t* options, ag_plan_t* plan);
+
+/* ------------------------------------------------------------------------
+ * Linear layer: the matrix product with bias, activation and residual in its
+ * epilogue, and its gradients.  One rank's product on dense matrices anywhere
+ * in device memory (a region of the heap, a tensor): what a sequence-parallel
+ * rank does between an all-gather of its input and its own loss.
+ *
+ *   z = x . w^T + bias                       (fp32)
+ *   y = act(z) + residual                    (fp32, rounded once to dtype)
+ *
+ * x         device, M x K, element (m,k) at x[m*ldx + k]
+ * w         device, N x K, element (n,k) at w[n*ldw + k]
+ * bias      device, N elements, or NULL
+ * residual  device, M x N (row stride ldr), or NULL; may be y itself (same
+ *           address and stride)
+ * y         device, M x N (row stride ldy)
+ * z         device, M x N (row stride ldz), or NULL: the pre-activation
+ *           rounded to dtype, which the backward pass reads
+ * dtype     AG_F16 or AG_BF16, shared by all of them (AG_F32 -> AG_ERR_UNSUPPORTED)
+ * M, N, K   any size from 0 (K = 0: y = act(bias) + residual)
+ * ld*       row strides in elements; 0 = dense (K or N); any value >= the row
+ * Pointers need only their element's alignment.  Operands of the product whose
+ * rows are not 4-byte aligned are copied to the workspace first (M above 32);
+ * rows of less than 2^20 elements apart (AG_ERR_UNSUPPORTED otherwise).
+ * Outputs must not overlap inputs or each other (but y and residual, above).
+ * Rows and columns between the matrices' rows (ld > row) are never written,
+ * and never read beyond the aligned 4 bytes that hold a row's last element.
+ *
+ * workspace  device memory of at least the plan's workspace_bytes, 256-byte
+ *            aligned, not shared by calls that may run at once; its contents
+ *            need no initialisation and are not kept.  May be NULL if 0 bytes.
+ * The result does not depend on the stream, on the workspace or on timing
+ * (partial sums are joined in a fixed order, without atomics).
+ * ------------------------------------------------------------------------ */
+typedef enum ag_act {
+    AG_ACT_NONE = 0,
+    AG_ACT_RELU = 1,       /* z < 0 ? 0 : z, slope 0 at z <= 0 */
+    AG_ACT_GELU = 2,       /* z/2 (1 + erf(z/sqrt 2)) */
+    AG_ACT_GELU_TANH = 3,  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    AG_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} ag_act_t;
+
+typedef struct ag_linear_args {
+    const void* x;
+    const void* w;
+    const void* bias;
+    const void* residual;
+    void* y;
+    void* z;
+    int64_t ldx, ldw, ldr, ldy, ldz;
+    int64_t M, N, K;
+    int32_t dtype;        /* ag_dtype_t */
+    int32_t act;          /* ag_act_t */
+    int32_t reserved[6];  /* must be 0 */
+} ag_linear_args_t;
+
+/* One matrix product as it will be launched. */
+typedef struct ag_product_plan {
+    int32_t variant;      /* 0 = not computed, 1 = row streaming (few rows of x), 2 = tiles */
+    int32_t tile_m, tile_n, tile_k;
+    int32_t splits;       /* parts of the reduction, joined by a second kernel when > 1 */
+    int32_t n_programs;   /* workgroups */
+    int32_t packed;       /* bit 0 / 1: first / second operand copied to aligned rows first */
+    int32_t reserved;
+} ag_product_plan_t;
+
+typedef struct ag_linear_plan {
+    ag_product_plan_t product;     /* y (linear); dx (linear_backward) */
+    ag_product_plan_t product_dw;  /* dw (linear_backward) */
+    uint64_t workspace_bytes;
+    uint64_t bytes_read;           /* algorithmic: each input once */
+    uint64_t bytes_written;
+    double flops;
+    int32_t launches;
+    int32_t reserved;
+} ag_linear_plan_t;
+
+ag_status_t ag_linear(const ag_linear_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only validation and launch decisions of ag_linear on a device of
+ * num_cus compute units (0 = the current HIP device's). */
+ag_status_t ag_plan_linear(const ag_linear_args_t* args, int num_cus, ag_linear_plan_t* plan);
+
+/* Gradients of the linear layer, from the gradient dy of y:
+ *
+ *   dz = dy * act'(z)
+ *   dx = dz . w            (M x K)
+ *   dw = dz^T . x          (N x K)       + dw if accumulate
+ *   db = sum over rows dz  (N)           + db if accumulate
+ *
+ * (the residual's gradient is dy itself).  Sums are fp32; dx has the
+ * operands' dtype, dw and db have dw_dtype: the operands' dtype or AG_F32.
+ * With an activation, dz is rounded once to dtype, the type its products'
+ * matrix instructions take; db sums the unrounded dz.  z is the pre-activation
+ * that ag_linear stored; it may be NULL when act is AG_ACT_NONE.  dx, dw and
+ * db may each be NULL (not computed); accumulate adds to dw and db in fp32
+ * before the one rounding.  x is read only for dw, w only for dx; either may
+ * be NULL when its gradient's partner is not asked for.  Sizes, strides,
+ * alignment, overlap and the workspace are as for ag_linear.  M = 0 gives
+ * zero gradients dw and db (or leaves them, with accumulate). */
+typedef struct ag_linear_backward_args {
+    const void* dy;
+    const void* z;
+    const void* x;
+    const void* w;
+    void* dx;
+    void* dw;
+    void* db;
+    int64_t lddy, ldz, ldx, ldw, lddx, lddw;
+    int64_t M, N, K;
+    int32_t dtype;        /* ag_dtype_t of dy, z, x, w and dx */
+    int32_t act;          /* ag_act_t */
+    int32_t dw_dtype;     /* ag_dtype_t of dw and db */
+    int32_t accumulate;   /* 0 or 1 */
+    int32_t reserved[4];  /* must be 0 */
+} ag_linear_backward_args_t;
+
+ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* workspace, size_t workspace_bytes,
+                               void* stream);
+ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int num_cus, ag_linear_plan_t* plan);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors in one launch, with states in 32 or in 8 bits.
+ * A handle keeps a device table of the tensors' addresses, made once (as a
+ * heap keeps its base table); the tensors must stay where they are while the
+ * handle is used.  For every element, with g = grad * grad_scale:
+ *
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *
+ * in fp32 (m and v of 8-bit states in fp64).  p is the master copy where
+ * there is one (fp32; param then receives it rounded), else param itself.
+ *
+ * 8-bit states: blocks of AG_ADAMW_BLOCK consecutive elements of a tensor
+ * share one fp32 maximum S per state.  A code c stands for
+ *   m = sign(c) (|c|/127)^2 S   (int8)       v = (c/255)^4 S   (uint8),
+ * so that m and sqrt(v) reach down to the same 1.6e-5 of their block's
+ * largest.  A value's code is floor(t + u), t its place on that scale and
+ * u = 1/2 (nearest), or with stochastic rounding a number in (0,1) that a
+ * counter hash makes from the seed and the element's place: updates far
+ * smaller than a code's step then count on average instead of never.  v > 0
+ * never rounds to the code 0, so no live first moment meets a zero
+ * denominator.  All-zero codes and scales are the zero state.  A NaN or an
+ * infinity makes its whole block's state NaN (the parameters: its element).
+ * ------------------------------------------------------------------------ */
+#define AG_ADAMW_BLOCK 256
+
+typedef struct ag_adamw ag_adamw_t;  /* opaque */
+
+typedef struct ag_adamw_tensor {
+    void* param;
+    const void* grad;
+    void* exp_avg;            /* float[n], or int8_t[n] */
+    void* exp_avg_sq;         /* float[n], or uint8_t[n] */
+    float* exp_avg_scale;     /* 8-bit states: float[ceil(n / AG_ADAMW_BLOCK)], else NULL */
+    float* exp_avg_sq_scale;
+    float* master;            /* float[n], or NULL (all tensors of a handle alike) */
+    int64_t n;                /* elements, >= 0 */
+} ag_adamw_tensor_t;
+
+/* Pointers need their element's alignment.  param_dtype and grad_dtype: any
+ * ag_dtype_t; master weights only with a 16-bit param_dtype.  state_bits: 32
+ * or 8.  Tensors must not overlap.  Allocates and fills the table (a
+ * synchronising call); 1 <= count <= 2^20, below 2^40 elements in all. */
+ag_status_t ag_adamw_create(const ag_adamw_tensor_t* tensors, int64_t count, ag_dtype_t param_dtype,
+                            ag_dtype_t grad_dtype, int state_bits, ag_adamw_t** out);
+/* The step that uses the table must have completed. */
+ag_status_t ag_adamw_destroy(ag_adamw_t* optimizer);
+
+typedef struct ag_adamw_hyper {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;                 /* >= 1: the number of this step */
+    const int64_t* dev_step;      /* optional device scalars, read by the kernel instead of the host's value: */
+    const float* dev_lr;          /*   a captured graph's step then follows them from replay to replay */
+    const float* dev_grad_scale;  /*   (multiplied with grad_scale: a clipping factor) */
+    uint64_t seed;                /* stochastic rounding's seed: another one for every step */
+    int32_t stochastic;           /* 1: stochastic rounding of 8-bit states, seed + *dev_step where there is one */
+    int32_t reserved[5];          /* must be 0 */
+} ag_adamw_hyper_t;
+
+/* 0 <= beta < 1, eps > 0, the rest finite.  One launch; nothing to do for zero elements. */
+ag_status_t ag_adamw_step(const ag_adamw_t* optimizer, const ag_adamw_hyper_t* hyper, void* stream);
+
+/* The values that 8-bit states stand for, as fp32 (checkpoints): exp_avg[i]
+ * and exp_avg_sq[i] are host arrays of count device addresses of float[n].
+ * AG_ERR_INVALID_ARG on a handle of 32-bit states. */
+ag_status_t ag_adamw_read_states(const ag_adamw_t* optimizer, float* const* exp_avg, float* const* exp_avg_sq,
+                                 void* stream);
 
 /* ------------------------------------------------------------------------ */
 const char* ag_status_string(ag_status_t status);  /* static string, never NULL */
