@@ -27,10 +27,11 @@ struct LinearGemmArgs {
     int64_t lda, ldb;
     int64_t I, J, R;
     int32_t tiles_i, tiles_j;
-    int32_t splits;             // parts of the reduction
-    int32_t stages_per_split;   // 64-wide steps of a part
-    float* partial;             // splits > 1: part s at partial + s*I*partial_ld, rows of partial_ld
-    int64_t partial_ld;
+    int32_t stages;             // 64-wide steps of the reduction, at least 1
+    int32_t full_tiles;         // tiles that one workgroup computes, the first of the order
+    int32_t tail_groups;        // workgroups that share the steps of the other tiles, tail_run steps each
+    int32_t tail_run;
+    float* partial;             // tail: two fp32 tiles per workgroup, for its pieces of tiles
     LinearEpilogue epi;
 };
 
@@ -38,8 +39,8 @@ enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1 };
 enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
 
 hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream);
-// Joins the parts of a split product in order and applies the epilogue.
-hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, hipStream_t stream);
+// Joins the pieces of the tail's cut tiles in order and applies the epilogue.
+hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int tile, hipStream_t stream);
 
 // Row streaming: out(m, n) for few rows m of x (I = N, J = M <= kLinearStreamRows).
 constexpr int kLinearStreamRows = 32;

@@ -189,50 +189,56 @@ __device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], co
 // ---------------------------------------------------------------- tiled product
 
 namespace linear_cfg {
-// TM x TN output tile, eight waves in a 4 x 2 grid, the reduction 64 at a time through two LDS slots.
-template <int TM_, int TN_, int OCC_>
+// T x T output tile, four waves in a 2 x 2 grid (one per SIMD).  The reduction advances 64 at a time; a stage's
+// operands are two parts of T rows (or columns) each, and NP parts fit the LDS ring.
+template <int T_, int NP_>
 struct Cfg {
-    static constexpr int TM = TM_, TN = TN_;
-    static constexpr int WGM = 4, WGN = 2, NW = 8, NT = 512, HALF = 4;
-    static constexpr int WTM = TM / WGM, WTN = TN / WGN;   // wave sub-tile
-    static constexpr int BM = WTM / 16, BN = WTN / 16;     // 16 x 16 blocks of it
-    static constexpr int OCC = OCC_;                       // waves per SIMD
-    static constexpr int A_BYTES = TM * 128, STAGE = (TM + TN) * 128;
-    static constexpr int C_PITCH = WTN * 4 + 16;           // a staged fp32 row of the epilogue
-    static constexpr int LPR = WTN / 8;                    // lanes per staged row
+    static constexpr int T = T_, NP = NP_;
+    static constexpr int NW = 4, NT = 256;
+    static constexpr int WT = T / 2;                       // wave sub-tile, square
+    static constexpr int NB = WT / 16;                     // 16 x 16 blocks of it, either way
+    static constexpr int PART = T * 128;                   // bytes of a part
+    static constexpr int LOADS = T / 32;                   // loads of a wave per part
+    static constexpr int READ_STEP = NB * NB / (4 * NB);   // products per fragment read
+    static constexpr int LOAD_STEP = NB * NB / (2 * LOADS);   // products per load
+    static constexpr int C_PITCH = WT * 4 + 16;            // a staged fp32 row of the epilogue
+    static constexpr int LPR = WT / 8;                     // lanes per staged row
     static constexpr int RPP = 64 / LPR;                   // rows per pass of the wave
-    static_assert((BM & (BM - 1)) == 0 && (BN & (BN - 1)) == 0, "transposed fragments address blocks by XOR");
-    static_assert(NW * 16 * C_PITCH <= 2 * STAGE, "every wave stages 16 rows of its sub-tile");
-    static_assert(2 * STAGE <= 160 * 1024, "gfx950 has 160 KiB of LDS");
+    static_assert((NB & (NB - 1)) == 0, "transposed fragments address blocks by XOR");
+    static_assert(READ_STEP >= 1 && LOAD_STEP >= 1, "reads and loads fit between the products");
+    static_assert(NP >= 4 && (NP - 2) * LOADS < 64, "vmcnt is 6 bits");
+    static_assert(NW * 16 * C_PITCH <= NP * PART, "every wave stages 16 rows of its sub-tile");
+    static_assert(NP * PART <= 160 * 1024, "gfx950 has 160 KiB of LDS");
 };
 }  // namespace linear_cfg
 
 namespace {
 
 // One operand's part of an LDS stage.  A wave instruction moves 1 KiB, lane l
-// to bytes [16 l, 16 l + 16) of it; HALF waves share the T/8 instructions.
+// to bytes [16 l, 16 l + 16) of it; the waves share the part's T/8 instructions.
 //
 // r-contiguous (TR false): the stage holds T rows of 64 r (128 bytes).  The 16-byte chunks of a row
 // are XOR-ed with row & 7, so that the fragment reads of 8 rows at one chunk spread over the banks.
 // transposed (TR true): 64 rows of r with T columns each (2 T bytes).  The 32-byte units of a row are
 // XOR-ed with f(row) = (row & 3) | 4 ((row >> 3) & 1): the eight rows that 32 lanes of a transposing
 // read touch (0-3 and 8-11 of a 32-row step) then lie on eight different 32-byte bank groups.
-template <class C, int T, bool TR>
+template <class C, bool TR>
 struct Part {
-    static constexpr int J = T / 8 / C::HALF;              // instructions per loading wave
+    static constexpr int T = C::T;
+    static constexpr int J = T / 8 / C::NW;                // instructions per wave
     static constexpr int RPI = TR ? 512 / T : 8;           // stage rows per instruction
-    static constexpr int STEP = RPI * C::HALF;             // stage rows between a wave's instructions
+    static constexpr int STEP = RPI * C::NW;               // stage rows between a wave's instructions
     static constexpr int UNITS = T / 16;                   // transposed: 32-byte units per row
 
     uint32_t off[TR && STEP == 8 ? 2 : 1];   // lane's byte offset within the operand tile, first instruction
     uint32_t r_lane;                         // r-contiguous: first r of the lane's chunk within the stage
 
-    __device__ __forceinline__ void init(int lane, int wp, uint32_t ld2)
+    __device__ __forceinline__ void init(int lane, int wave, uint32_t ld2)
     {
         if constexpr (TR) {
             static_assert(STEP == 8 || STEP == 16, "f changes with the instruction by bit 2 alone, or not");
             constexpr int LPR = 64 / RPI;                  // lanes per stage row
-            const uint32_t row = static_cast<uint32_t>(wp * RPI + lane / LPR);   // < STEP
+            const uint32_t row = static_cast<uint32_t>(wave * RPI + lane / LPR);   // < STEP
             const uint32_t f = (row & 3u) | (((row >> 3) & 1u) << 2);
             const uint32_t c = static_cast<uint32_t>(lane % LPR);
             const uint32_t col = (((c >> 1) ^ f) << 5) | ((c & 1u) << 4);
@@ -242,35 +248,55 @@ struct Part {
         } else {
             const uint32_t row = static_cast<uint32_t>(lane >> 3);
             const uint32_t chunk = static_cast<uint32_t>(lane & 7) ^ row;
-            off[0] = (static_cast<uint32_t>(wp * 8) + row) * ld2 + chunk * 16u;
+            off[0] = (static_cast<uint32_t>(wave * 8) + row) * ld2 + chunk * 16u;
             r_lane = chunk * 8u;
         }
     }
 
-    // Stage kt of the operand tile at base (its first row or column already applied).  live: false loads
-    // nothing (and writes zeros).  The descriptor starts at the stage and ends with the operand, so that what
-    // lies past the reduction's or the last column's end reads as zero and nothing past the operand is read; the
-    // end is rounded up to 4 bytes because the range check works on whole dwords (operands are 4-byte
-    // aligned: the dword of the last element is the operand's own).
-    // extent: bytes from base to the operand's end (r-contiguous), bytes of a row from base (transposed).
-    __device__ __forceinline__ void load(uint64_t base, int64_t extent, int64_t R, uint32_t ld2, uint8_t* dst, int kt,
-                                         int wp, bool live) const
+    // The operand tile's next stage to load.  The descriptor starts at the stage and ends with the operand, so
+    // that what lies past the reduction's or the last column's end reads as zero and nothing past the operand
+    // is read; the end is rounded up to 4 bytes because the range check works on whole dwords (operands are
+    // 4-byte aligned: the dword of the last element is the operand's own).
+    struct Next {
+        uint64_t base;
+        int64_t bytes;      // from base to the operand's end
+        int32_t r_left;     // of the reduction, from the stage
+        int32_t stages;     // still to load; past them loads fetch nothing (and write zeros)
+    };
+    // tile: the operand at the tile's first row or column; extent: bytes from there to the operand's
+    // end (r-contiguous), or of its row's rest (transposed).
+    static __device__ __forceinline__ Next start(uint64_t tile, int64_t extent, int64_t R, uint32_t ld2, int first, int count)
     {
-        const int64_t r0 = static_cast<int64_t>(kt) * 64;
+        const int64_t r0 = static_cast<int64_t>(first) * 64;
         const int64_t skip = TR ? r0 * ld2 : r0 * 2;
-        int64_t records = TR ? (R - 1 - r0) * static_cast<int64_t>(ld2) + extent : extent - skip;
-        if (!live || r0 >= R || records < 0) records = 0;
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + static_cast<uint64_t>(skip), static_cast<uint64_t>(records));
-        uint32_t l2 = ld2, o0 = off[0], o1 = off[TR && STEP == 8 ? 1 : 0];
-        if constexpr (!TR) o0 = r0 + r_lane < R ? o0 : kOutOfRange;   // chunks past the end belong to the next row
+        return Next{tile + static_cast<uint64_t>(skip), TR ? (R - 1 - r0) * static_cast<int64_t>(ld2) + extent : extent - skip,
+                    static_cast<int32_t>(R - r0), count};
+    }
+    struct At {
+        uint64_t base;
+        uint32_t records, o0, o1, ld2;
+    };
+    // The stage's load addresses; n moves on to the next one.
+    __device__ __forceinline__ At take(Next& n, uint32_t ld2) const
+    {
+        const bool live = n.stages > 0 && n.r_left > 0;
+        At t{n.base, live ? static_cast<uint32_t>(min(n.bytes, int64_t{0x7fffffff})) : 0u, off[0],
+             off[TR && STEP == 8 ? 1 : 0], ld2};
+        if constexpr (!TR) t.o0 = static_cast<int32_t>(r_lane) < n.r_left ? t.o0 : kOutOfRange;   // the next row's chunks
         // opaque copies: the instructions' offsets are not kept in registers across the loop
-        asm volatile("" : "+v"(o0), "+v"(o1), "+s"(l2));
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const uint32_t o = TR && STEP == 8 && (j & 1) ? o1 : o0;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (AG_LDS void*)(dst + (wp + C::HALF * j) * 1024), 16,
-                                                     o + static_cast<uint32_t>(STEP * j) * l2, 0, 0, 0);
-        }
+        asm volatile("" : "+v"(t.o0), "+v"(t.o1), "+s"(t.ld2));
+        const int64_t step = TR ? static_cast<int64_t>(ld2) * 64 : 128;
+        n.base += static_cast<uint64_t>(step);
+        n.bytes -= step;
+        n.r_left -= 64;
+        n.stages -= 1;
+        return t;
+    }
+    static __device__ __forceinline__ void load(const At& t, uint8_t* dst, int wave, int j)
+    {
+        const uint32_t o = TR && STEP == 8 && (j & 1) ? t.o1 : t.o0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(t.base, t.records), (AG_LDS void*)(dst + (wave + C::NW * j) * 1024),
+                                                 16, o + static_cast<uint32_t>(STEP * j) * t.ld2, 0, 0, 0);
     }
 };
 
@@ -278,8 +304,9 @@ struct Part {
 // l & 15 of a block, r = 8 (l >> 4) .. + 7 of the step, from either layout.  The reads are inline assembly:
 // the compiler cannot tell them from the LDS-direct loads still landing in the other slot and would
 // wait for those; every read is followed by wait_lgkmcnt0() before its use.
-template <class C, int T, bool TR, int NB>
+template <class C, bool TR>
 struct Frags {
+    static constexpr int T = C::T, NB = C::NB;
     uint32_t base;      // lane's byte offset within the operand's part of the stage, block 0 of step 0
 
     __device__ __forceinline__ void init(int lane, int first_row)
@@ -295,27 +322,23 @@ struct Frags {
             base = (static_cast<uint32_t>(first_row) + row) * 128u + (((static_cast<uint32_t>(lane) >> 4) ^ (row & 7u)) << 4);
         }
     }
+    // Block b of step kk (constants after unrolling).
     template <class V>
-    __device__ __forceinline__ void read(V (&dst)[NB], uint32_t part, int kk) const
+    __device__ __forceinline__ void read(V& dst, uint32_t part, int kk, int b) const
     {
         if constexpr (TR) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint32_t addr = (part + base) ^ (static_cast<uint32_t>(b) << 5);
-                u32x2 lo, hi;
-                if (kk == 0) {
-                    asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(lo) : "v"(addr));
-                    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(hi) : "v"(addr), "i"(8 * T));
-                } else {
-                    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(lo) : "v"(addr), "i"(64 * T));
-                    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(hi) : "v"(addr), "i"(72 * T));
-                }
-                dst[b] = __builtin_bit_cast(V, u32x4{lo.x, lo.y, hi.x, hi.y});
+            const uint32_t addr = (part + base) ^ (static_cast<uint32_t>(b) << 5);
+            u32x2 lo, hi;
+            if (kk == 0) {
+                asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(lo) : "v"(addr));
+                asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(hi) : "v"(addr), "i"(8 * T));
+            } else {
+                asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(lo) : "v"(addr), "i"(64 * T));
+                asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(hi) : "v"(addr), "i"(72 * T));
             }
+            dst = __builtin_bit_cast(V, u32x4{lo.x, lo.y, hi.x, hi.y});
         } else {
-            const uint32_t addr = (part + base) ^ (static_cast<uint32_t>(kk) << 6);   // chunk + 4: bit 2 of the XOR-ed chunk
-#pragma unroll
-            for (int b = 0; b < NB; ++b) read_at(dst[b], addr, b);
+            read_at(dst, (part + base) ^ (static_cast<uint32_t>(kk) << 6), b);   // chunk + 4: bit 2 of the XOR-ed chunk
         }
     }
     template <class V>
@@ -332,175 +355,248 @@ struct Frags {
     }
 };
 
+// c += b a^T with c in accumulation registers.  Inline assembly keeps the 256 accumulators of a 256 x 256 tile in
+// the accumulation half of the register file; left to itself the compiler spread them over both halves and
+// spilled.  It does not see these instructions' write latency: c is used again no sooner than BM * BN of them
+// later, and settle() stands between them and other uses.
+template <bool BF16, class V>
+__device__ __forceinline__ void mfma(f32x4& c, V b, V a)
+{
+    if constexpr (BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+    else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+}
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p)
 {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((AG_LDS const uint8_t*)p));
 }
 __device__ __forceinline__ int64_t dword_up(int64_t bytes) { return (bytes + 3) & ~int64_t{3}; }
 
+// Work of a product: the first full_tiles tiles, one per workgroup, then the other tiles' 64-wide steps, laid
+// end to end and cut into tail_groups equal runs, one per workgroup.  A run's piece of a tile that is
+// not the whole tile goes to the workgroup's partial tile as fp32: slot 0 for the piece that starts
+// inside a tile (its first), slot 1 for one that starts with it (its last); a second kernel joins the pieces.
 template <bool BF16, int FORM, class C>
-__global__ __launch_bounds__(C::NT, C::OCC) void ag_linear_gemm_kernel(LinearGemmArgs a)
+__global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
 {
     constexpr bool TA = FORM == kFormTN, TB = FORM != kFormNT;
-    using M = Mfma<BF16>;
-    using V = typename M::V;
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[2][C::STAGE];
+    constexpr int NB = C::NB, NP = C::NP;
+    using V = typename Mfma<BF16>::V;
+    using PartA = Part<C, TA>;
+    using PartB = Part<C, TB>;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[NP * C::PART];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / C::WGN, wn = wave % C::WGN;
-    const int half = wave / C::HALF, wp = wave % C::HALF;   // waves sit on SIMDs round-robin: each half has one on every SIMD
+    const int wm = wave >> 1, wn = wave & 1;
     const uint32_t lda2 = static_cast<uint32_t>(a.lda) * 2u, ldb2 = static_cast<uint32_t>(a.ldb) * 2u;
 
-    // workgroup -> part of the reduction and tile.  Workgroup p runs on XCD p % 8: every XCD gets a
-    // contiguous run of the tile order, which goes 8 tile rows at a time, so that its L2 serves shared rows.
-    const int tiles = a.tiles_i * a.tiles_j;
-    const int p = blockIdx.x, n = gridDim.x;
-    const int xcd = p & 7, per = n >> 3, more = n & 7;
-    const int v = xcd * per + min(xcd, more) + (p >> 3);
-    const int split = v / tiles;
-    const int t = v - split * tiles;
-    constexpr int GROUP = 8;
-    const int g = t / (GROUP * a.tiles_j);
-    const int gm = min(a.tiles_i - g * GROUP, GROUP);
-    const int in_group = t - g * GROUP * a.tiles_j;
-    const int64_t i0 = static_cast<int64_t>(g * GROUP + in_group % gm) * C::TM;
-    const int64_t j0 = static_cast<int64_t>(in_group / gm) * C::TN;
+    PartA pa;
+    PartB pb;
+    Frags<C, TA> ra;
+    Frags<C, TB> rb;
+    pa.init(lane, wave, lda2);
+    pb.init(lane, wave, ldb2);
+    ra.init(lane, wm * C::WT);
+    rb.init(lane, wn * C::WT);
 
-    const uint64_t a_base = reinterpret_cast<uint64_t>(a.A) + static_cast<uint64_t>(TA ? i0 * 2 : i0 * lda2);
-    const uint64_t b_base = reinterpret_cast<uint64_t>(a.B) + static_cast<uint64_t>(TB ? j0 * 2 : j0 * ldb2);
-    const int64_t a_extent = TA ? dword_up((a.I - i0) * 2) : (a.I - 1 - i0) * lda2 + dword_up(a.R * 2);
-    const int64_t b_extent = TB ? dword_up((a.J - j0) * 2) : (a.J - 1 - j0) * ldb2 + dword_up(a.R * 2);
+    // Workgroup p runs on XCD p % 8: every XCD gets a contiguous run of the order (of the whole tiles
+    // and of the tail's runs alike), so that its L2 serves the rows that neighbouring tiles share.
+    const bool in_tail = static_cast<int>(blockIdx.x) >= a.full_tiles;
+    const int p = static_cast<int>(blockIdx.x) - (in_tail ? a.full_tiles : 0);
+    const int n = in_tail ? a.tail_groups : a.full_tiles;
+    const int per = n >> 3, more = n & 7;
+    const int v = (p & 7) * per + min(p & 7, more) + (p >> 3);
+    int64_t step = in_tail ? static_cast<int64_t>(a.full_tiles) * a.stages + static_cast<int64_t>(v) * a.tail_run
+                           : static_cast<int64_t>(v) * a.stages;
+    const int64_t end = in_tail ? min(step + a.tail_run, static_cast<int64_t>(a.tiles_i) * a.tiles_j * a.stages)
+                                : step + a.stages;
 
-    Part<C, C::TM, TA> pa;
-    Part<C, C::TN, TB> pb;
-    Frags<C, C::TM, TA, C::BM> ra;
-    Frags<C, C::TN, TB, C::BN> rb;
-    pa.init(lane, wp, lda2);
-    pb.init(lane, wp, ldb2);
-    ra.init(lane, wm * C::WTM);
-    rb.init(lane, wn * C::WTN);
+    while (step < end) {
+        const int t = static_cast<int>(step / a.stages);
+        const int first = static_cast<int>(step - static_cast<int64_t>(t) * a.stages);
+        const int count = static_cast<int>(min(end - step, static_cast<int64_t>(a.stages - first)));
+        step += count;
+        // tile order: 8 tile rows at a time, column by column
+        constexpr int GROUP = 8;
+        const int g = t / (GROUP * a.tiles_j);
+        const int gm = min(a.tiles_i - g * GROUP, GROUP);
+        const int in_group = t - g * GROUP * a.tiles_j;
+        const int64_t i0 = static_cast<int64_t>(g * GROUP + in_group % gm) * C::T;
+        const int64_t j0 = static_cast<int64_t>(in_group / gm) * C::T;
 
-    const int stages_all = static_cast<int>((a.R + 63) >> 6);
-    const int first = split * a.stages_per_split;
-    const int count = max(0, min(stages_all - first, a.stages_per_split));
+        typename PartA::Next na = PartA::start(reinterpret_cast<uint64_t>(a.A) + static_cast<uint64_t>(TA ? i0 * 2 : i0 * lda2),
+                                               TA ? dword_up((a.I - i0) * 2) : (a.I - 1 - i0) * lda2 + dword_up(a.R * 2),
+                                               a.R, lda2, first, count);
+        typename PartB::Next nb = PartB::start(reinterpret_cast<uint64_t>(a.B) + static_cast<uint64_t>(TB ? j0 * 2 : j0 * ldb2),
+                                               TB ? dword_up((a.J - j0) * 2) : (a.J - 1 - j0) * ldb2 + dword_up(a.R * 2),
+                                               a.R, ldb2, first, count);
 
-    f32x4 acc[C::BM][C::BN];
+        f32x4 acc[NB][NB];
 #pragma unroll
-    for (int bm = 0; bm < C::BM; ++bm)
+        for (int bm = 0; bm < NB; ++bm)
 #pragma unroll
-        for (int bn = 0; bn < C::BN; ++bn) acc[bm][bn] = f32x4{0.f, 0.f, 0.f, 0.f};
-    V fa[C::BM], fb[C::BN];
+            for (int bn = 0; bn < NB; ++bn) {
+                acc[bm][bn] = f32x4{0.f, 0.f, 0.f, 0.f};
+                asm volatile("" : "+a"(acc[bm][bn]));
+            }
+        settle();
+        V fa[2][NB], fb[2][NB];   // fragments of the two 32-wide halves of a stage
 
-    auto load_a = [&](int slot, int s) { pa.load(a_base, a_extent, a.R, lda2, &ring[slot][0], first + s, wp, s < count); };
-    auto load_b = [&](int slot, int s) {
-        pb.load(b_base, b_extent, a.R, ldb2, &ring[slot][C::A_BYTES], first + s, wp, s < count);
-    };
-    // The last 16-byte chunk of an r-contiguous row holds elements past the reduction's end when R is no
-    // multiple of 8: they are set to zero in LDS, once, when the last stage has landed.
-    auto clear_tail = [&](int slot) {
-        const uint32_t chunk = static_cast<uint32_t>(a.R & 63) >> 3, from = static_cast<uint32_t>(a.R & 7);
-        for (int row = tid; row < C::TM + C::TN; row += C::NT) {
-            if ((TA && row < C::TM) || (TB && row >= C::TM)) continue;
-            const uint32_t r7 = static_cast<uint32_t>(row < C::TM ? row : row - C::TM) & 7u;
-            uint16_t* c = reinterpret_cast<uint16_t*>(&ring[slot][row * 128 + ((chunk ^ r7) << 4)]);
-            for (uint32_t e = from; e < 8; ++e) c[e] = 0;
+        // Part 2 s (A) and 2 s + 1 (B) of stage s lie in slots 2 s % NP and (2 s + 1) % NP.
+        auto wrap = [](int slot) { return slot >= NP ? slot - NP : slot; };
+        // The last 16-byte chunk of an r-contiguous row holds elements past the reduction's end when R is no
+        // multiple of 8: they are set to zero in LDS, once, when the last stage has landed.
+        const bool tail = !(TA && TB) && (a.R & 7) != 0 && first + count == a.stages;
+        auto clear_tail = [&](int slot_a, int slot_b) {
+            const uint32_t chunk = static_cast<uint32_t>(a.R & 63) >> 3, from = static_cast<uint32_t>(a.R & 7);
+            for (int row = tid; row < 2 * C::T; row += C::NT) {
+                if ((TA && row < C::T) || (TB && row >= C::T)) continue;
+                const int r = row < C::T ? row : row - C::T;
+                uint16_t* c = reinterpret_cast<uint16_t*>(ring + (row < C::T ? slot_a : slot_b) * C::PART + r * 128 +
+                                                          ((chunk ^ (static_cast<uint32_t>(r) & 7u)) << 4));
+                for (uint32_t e = from; e < 8; ++e) c[e] = 0;
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto read = [&](int f, uint32_t part_a, uint32_t part_b, int kk, int i) {   // i-th fragment: A's blocks, then B's
+            if (i < NB) ra.read(fa[f][i], part_a, kk, i);
+            else rb.read(fb[f][i - NB], part_b, kk, i - NB);
+        };
+        const uint32_t lds = lds_address(ring);
+
+        // prologue: all slots on their way, the first stage landed and its first fragments read
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            if (q % 2 == 0) {
+                const typename PartA::At la = pa.take(na, lda2);
+#pragma unroll
+                for (int j = 0; j < C::LOADS; ++j) PartA::load(la, ring + q * C::PART, wave, j);
+            } else {
+                const typename PartB::At lb = pb.take(nb, ldb2);
+#pragma unroll
+                for (int j = 0; j < C::LOADS; ++j) PartB::load(lb, ring + q * C::PART, wave, j);
+            }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vmcnt<(NP - 2) * C::LOADS>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-    };
-    const bool tail = !(TA && TB) && (a.R & 7) != 0 && first + count == stages_all;
-
-    // Two slots.  Stage s + 2's A part is loaded by half s % 2 of the waves right after the barrier that
-    // ends the reads of stage s, into the slot it frees; its B part by the other half at the start of stage
-    // s + 1.  A wave that issues loads is held until the CU takes them, so on every SIMD one wave goes on issuing matrix
-    // instructions meanwhile; and a wave's loads in flight at a boundary are those of the next stage alone.
-    auto stage = [&](int s, int slot) {
+        if (tail && count == 1) clear_tail(0, 1);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (kk == 0 && s >= 1 && half != ((s - 1) & 1)) load_b(slot ^ 1, s + 1);
-            const uint32_t part = lds_address(&ring[slot][0]);
-            ra.read(fa, part, kk);
-            rb.read(fb, part + C::A_BYTES, kk);
+        for (int i = 0; i < 2 * NB; ++i) read(0, lds, lds + C::PART, 0, i);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_lgkmcnt0();
+        __builtin_amdgcn_sched_barrier(0);
+
+        // A stage is two halves of NB x NB products each.  Between the first half's products the second half's
+        // fragments are read; then this wave's reads of the stage's slots are complete and the next stage has
+        // landed, and one barrier makes both true for all waves.  Between the second half's products the next
+        // stage's first fragments are read and the two slots are refilled with parts NP and NP + 1 further on, one
+        // load every few products: a wave is held at a load until the CU takes it (about one 1 KiB instruction
+        // per 22 cycles per CU), so loads in a row would leave the matrix pipe idle.  The order is pinned by
+        // scheduling barriers (scalar and address arithmetic may cross them); the fragment reads are
+        // waited for as a whole before the half that uses them.
+        int slot = 0;
+#pragma unroll 1
+        for (int s = 0; s < count; ++s) {
+            const int slot_b = wrap(slot + 1), next_a = wrap(slot + 2), next_b = wrap(slot + 3);
+            const uint32_t here_a = lds + slot * C::PART, here_b = lds + slot_b * C::PART;
+            const uint32_t there_a = lds + next_a * C::PART, there_b = lds + next_b * C::PART;
+#pragma unroll
+            for (int i = 0; i < NB * NB; ++i) {
+                if (i % C::READ_STEP == 0 && i / C::READ_STEP < 2 * NB) read(1, here_a, here_b, 1, i / C::READ_STEP);
+                mfma<BF16>(acc[i / NB][i % NB], fb[0][i % NB], fa[0][i / NB]);
+                __builtin_amdgcn_sched_barrier(0x6);
+            }
+            const typename PartA::At la = pa.take(na, lda2);
+            const typename PartB::At lb = pb.take(nb, ldb2);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_lgkmcnt0();
+            wait_vmcnt<(NP - 4) * C::LOADS>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if (tail && s + 2 == count) clear_tail(next_a, next_b);
+#pragma unroll
+            for (int i = 0; i < NB * NB; ++i) {
+                if (i % C::READ_STEP == 0 && i / C::READ_STEP < 2 * NB) read(0, there_a, there_b, 0, i / C::READ_STEP);
+                if (i % C::LOAD_STEP == C::LOAD_STEP - 1) {
+                    // parts 2 s + NP and 2 s + NP + 1: B first where NP is odd
+                    const int j = i / C::LOAD_STEP;
+                    uint8_t* dst = ring + (j < C::LOADS ? slot : slot_b) * C::PART;
+                    if ((j < C::LOADS) == (NP % 2 == 0)) PartA::load(la, dst, wave, j % C::LOADS);
+                    else PartB::load(lb, dst, wave, j % C::LOADS);
+                }
+                mfma<BF16>(acc[i / NB][i % NB], fb[1][i % NB], fa[1][i / NB]);
+                __builtin_amdgcn_sched_barrier(0x6);
+            }
             __builtin_amdgcn_sched_barrier(0);
             wait_lgkmcnt0();
             __builtin_amdgcn_sched_barrier(0);
-            if (kk == 1) {
-                wait_vmcnt<0>();
-                __builtin_amdgcn_s_barrier();
-                __builtin_amdgcn_sched_barrier(0);
-                if (half == (s & 1)) load_a(slot, s + 2);
-            }
-#pragma unroll
-            for (int bm = 0; bm < C::BM; ++bm)
-#pragma unroll
-                for (int bn = 0; bn < C::BN; ++bn) acc[bm][bn] = M::run(fb[bn], fa[bm], acc[bm][bn]);
+            slot = next_a;
         }
-        if (tail && s + 2 == count) clear_tail(slot ^ 1);
-    };
+        settle();
 
-    if (half == 0) {
-        load_a(0, 0);
-        load_b(0, 0);
-        wait_vmcnt<0>();
-    } else {
-        load_a(1, 1);
-        load_b(1, 1);
-    }
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    if (tail && count == 1) clear_tail(0);
-    for (int s = 0; s < count; s += 2) {
-        stage(s, 0);
-        if (s + 1 < count) stage(s + 1, 1);
-    }
-
-    // ---- epilogue.  A lane's accumulators hold 4 consecutive columns of one row of each block; every wave
-    // passes its sub-tile through its own piece of LDS, 16 rows at a time in fp32, and then holds 8
-    // consecutive columns per lane and whole row pieces per group of lanes: wide, coalesced accesses for the
-    // residual, the pre-activation and the output, and the one rounding at the very end.
-    wait_vmcnt<0>();   // loads of stages past the end have landed too
-    wait_lgkmcnt0();
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    uint8_t* mine = &ring[0][0] + wave * (16 * C::C_PITCH);
-    const int64_t col = j0 + wn * C::WTN + (lane % C::LPR) * 8;
-    const int n_col = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
-    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.splits == 1 && a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n_col);
+        // ---- epilogue.  A lane's accumulators hold 4 consecutive columns of one row of each block; every wave
+        // passes its sub-tile through its own piece of LDS, 16 rows at a time in fp32, and then holds 8
+        // consecutive columns per lane and whole row pieces per group of lanes: wide, coalesced accesses for
+        // the residual, the pre-activation and the output, and the one rounding at the very end.
+        wait_vmcnt<0>();   // loads of stages past the end have landed too
+        wait_lgkmcnt0();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        uint8_t* mine = ring + wave * (16 * C::C_PITCH);
+        const int tile_col = wn * C::WT + (lane % C::LPR) * 8;
+        const int64_t col = j0 + tile_col;
+        const int n_col = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
+        const bool whole = count == a.stages;
+        float* partial = a.partial + (static_cast<int64_t>(v) * 2 + (first == 0 ? 1 : 0)) * (C::T * C::T) + tile_col;
+        float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (whole && a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n_col);
 #pragma unroll
-    for (int bm = 0; bm < C::BM; ++bm) {
+        for (int bm = 0; bm < NB; ++bm) {
 #pragma unroll
-        for (int bn = 0; bn < C::BN; ++bn)
-            *reinterpret_cast<f32x4*>(mine + (lane & 15) * C::C_PITCH + (bn * 16 + (lane >> 4) * 4) * 4) = acc[bm][bn];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            for (int bn = 0; bn < NB; ++bn)
+                *reinterpret_cast<f32x4*>(mine + (lane & 15) * C::C_PITCH + (bn * 16 + (lane >> 4) * 4) * 4) = acc[bm][bn];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
-        for (int pass = 0; pass < 16 / C::RPP; ++pass) {
-            const int r = pass * C::RPP + lane / C::LPR;
-            const f32x4* src = reinterpret_cast<const f32x4*>(mine + r * C::C_PITCH + (lane % C::LPR) * 32);
-            const f32x4 lo = src[0], hi = src[1];
-            const int64_t row = i0 + wm * C::WTM + bm * 16 + r;
-            if (row < a.I && n_col > 0) {
-                float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                if (a.splits > 1) {
-                    f32x4* d = reinterpret_cast<f32x4*>(a.partial + (split * a.I + row) * a.partial_ld + col);
-                    d[0] = lo;      // rows of the parts are padded to whole vectors
-                    d[1] = hi;
-                } else {
-                    finish<BF16>(x, bias, a.epi, row, col, n_col);
+            for (int pass = 0; pass < 16 / C::RPP; ++pass) {
+                const int r = pass * C::RPP + lane / C::LPR;
+                const f32x4* src = reinterpret_cast<const f32x4*>(mine + r * C::C_PITCH + (lane % C::LPR) * 32);
+                const f32x4 lo = src[0], hi = src[1];
+                const int tile_row = wm * C::WT + bm * 16 + r;
+                const int64_t row = i0 + tile_row;
+                if (row < a.I && n_col > 0) {
+                    if (whole) {
+                        float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                        finish<BF16>(x, bias, a.epi, row, col, n_col);
+                    } else {
+                        f32x4* d = reinterpret_cast<f32x4*>(partial + tile_row * C::T);
+                        d[0] = lo;
+                        d[1] = hi;
+                    }
                 }
             }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();   // staging reads done before the next piece's loads land
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// 128 x 128 tiles take 64 KiB and 128 registers: two workgroups per CU, one computing while the other is at
-// its loads, first or last stage.
-using Cfg256 = linear_cfg::Cfg<256, 256, 2>;
-using Cfg128 = linear_cfg::Cfg<128, 128, 4>;
+// 256 x 256: a wave's 128 x 128 sub-tile keeps LDS reads (128 KiB a stage) and the slots' refill (64 KiB) below
+// the matrix pipe's 2048 cycles a stage at 128 bytes per cycle; its accumulators take 256 registers.
+// 128 x 128: for products with few tiles.
+using Cfg256 = linear_cfg::Cfg<256, 5>;
+using Cfg128 = linear_cfg::Cfg<128, 10>;
 
 using LinearFn = void (*)(LinearGemmArgs);
 template <bool BF16, class C> LinearFn pick_form(int form)
@@ -513,23 +609,33 @@ template <bool BF16, class C> LinearFn pick_form(int form)
     }
 }
 
-// ---------------------------------------------------------------- join of split products
+// ---------------------------------------------------------------- join of cut tiles
 
-// Adds the parts of 8 consecutive columns per thread in order, then the epilogue.
+// Adds the pieces of a tail tile in the reduction's order, 8 consecutive columns per thread, then the epilogue.
 template <bool BF16>
-__global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a)
+__global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, int tm, int tn)
 {
-    const int64_t per_row = a.partial_ld / 8;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t row = id / per_row, col = (id - row * per_row) * 8;
+    const int per_tile = tm * tn / 2048;           // workgroups
+    const int tail_tile = static_cast<int>(blockIdx.x) / per_tile;
+    const int t = a.full_tiles + tail_tile;
+    const int64_t begin = static_cast<int64_t>(tail_tile) * a.stages, end = begin + a.stages;
+    const int g0 = static_cast<int>(begin / a.tail_run), g1 = static_cast<int>((end - 1) / a.tail_run);
+    if (g0 == g1) return;                          // one workgroup had the whole tile
+    const int id = (static_cast<int>(blockIdx.x) % per_tile) * 256 + threadIdx.x;
+    const int tile_row = id / (tn / 8), tile_col = (id % (tn / 8)) * 8;
+    constexpr int GROUP = 8;
+    const int g = t / (GROUP * a.tiles_j);
+    const int gm = min(a.tiles_i - g * GROUP, GROUP);
+    const int in_group = t - g * GROUP * a.tiles_j;
+    const int64_t row = static_cast<int64_t>(g * GROUP + in_group % gm) * tm + tile_row;
+    const int64_t col = static_cast<int64_t>(in_group / gm) * tn + tile_col;
     if (row >= a.I || col >= a.J) return;
-    const float* p = a.partial + row * a.partial_ld + col;
-    const int64_t step = a.I * a.partial_ld;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const f32x4 lo = reinterpret_cast<const f32x4*>(p + s * step)[0];
-        const f32x4 hi = reinterpret_cast<const f32x4*>(p + s * step)[1];
+    for (int q = g0; q <= g1; ++q) {
+        const bool starts = static_cast<int64_t>(q) * a.tail_run <= begin;      // the piece that holds the first step
+        const f32x4* src = reinterpret_cast<const f32x4*>(a.partial + (static_cast<int64_t>(q) * 2 + (starts ? 1 : 0)) * (tm * tn) +
+                                                          tile_row * tn + tile_col);
+        const f32x4 lo = src[0], hi = src[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] += lo[e];
@@ -732,8 +838,7 @@ __global__ __launch_bounds__(256) void ag_linear_bias_grad_kernel(const float* s
 
 void linear_tile_shape(int tile, int* tm, int* tn, int* threads)
 {
-    *tm = tile == kLinearTile256 ? Cfg256::TM : Cfg128::TM;
-    *tn = tile == kLinearTile256 ? Cfg256::TN : Cfg128::TN;
+    *tm = *tn = tile == kLinearTile256 ? Cfg256::T : Cfg128::T;
     *threads = Cfg256::NT;
 }
 
@@ -741,8 +846,8 @@ hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int t
 {
     LinearFn fn = tile == kLinearTile256 ? (bf16 ? pick_form<true, Cfg256>(form) : pick_form<false, Cfg256>(form))
                                          : (bf16 ? pick_form<true, Cfg128>(form) : pick_form<false, Cfg128>(form));
-    const int64_t grid = static_cast<int64_t>(a.tiles_i) * a.tiles_j * a.splits;
-    if (fn == nullptr || grid < 1 || grid > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t grid = static_cast<int64_t>(a.full_tiles) + a.tail_groups;
+    if (fn == nullptr || grid < 1 || grid > 0x7fffffff || a.stages < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(grid)), dim3(Cfg256::NT), 0, stream, a);
     return hipGetLastError();
 }
@@ -757,11 +862,14 @@ bool grid_of(int64_t work, int64_t per, dim3* grid)
 }
 }  // namespace
 
-hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, hipStream_t stream)
+hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int tile, hipStream_t stream)
 {
+    int tm, tn, threads;
+    linear_tile_shape(tile, &tm, &tn, &threads);
+    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j - a.full_tiles;
     dim3 grid;
-    if (!grid_of(a.I * (a.partial_ld / 8), 256, &grid)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(bf16 ? ag_linear_join_kernel<true> : ag_linear_join_kernel<false>, grid, dim3(256), 0, stream, a);
+    if (!grid_of(tiles * (tm * tn / 2048), 1, &grid)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(bf16 ? ag_linear_join_kernel<true> : ag_linear_join_kernel<false>, grid, dim3(256), 0, stream, a, tm, tn);
     return hipGetLastError();
 }
 

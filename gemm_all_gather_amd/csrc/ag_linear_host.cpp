@@ -108,19 +108,23 @@ struct Product {
     bool stream = false;
     int form = ag::kFormNT, tile = ag::kLinearTile128;
     int64_t I = 0, J = 0, R = 0;
-    int64_t tiles_i = 0, tiles_j = 0, stages_per_split = 0;
-    int splits = 1;
+    int64_t tiles_i = 0, tiles_j = 0, stages = 0;
+    int64_t full_tiles = 0, tail_groups = 0, tail_run = 0;
+    bool join = false;           // some tail tile is cut
     uint64_t partial_bytes = 0;
-    int launches() const { return !on ? 0 : splits > 1 ? 2 : 1; }
+    int launches() const { return !on ? 0 : join ? 2 : 1; }
 };
 
-// Tile and split with the shortest estimated time.  A workgroup's 64-wide step costs what it measured in
-// long products on all CUs; a split adds its partial sums' traffic and a second launch.
+// Tile and cut with the shortest estimated time.  Whole rounds of tiles on all CUs go one to a workgroup; the
+// rest either too (one more round), or its steps are shared out evenly over G workgroups.  A
+// workgroup's 64-wide step costs what it measured in long products on all CUs; a cut adds the partial
+// tiles' traffic and a second launch.
 ag_status_t choose(Product* p, int cus)
 {
     struct Kind { double step_us, fixed_us; };
-    static const Kind kinds[2] = {{1.65, 8.0}, {0.62, 4.0}};   // kLinearTile256, kLinearTile128
-    const int64_t stages = (p->R + 63) / 64;
+    static const Kind kinds[2] = {{1.55, 9.0}, {0.42, 4.0}};   // kLinearTile256, kLinearTile128
+    constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
+    p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
     double best = 0;
     bool found = false;
     for (int tile = 0; tile < 2; ++tile) {
@@ -128,24 +132,35 @@ ag_status_t choose(Product* p, int cus)
         ag::linear_tile_shape(tile, &tm, &tn, &threads);
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
         if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffffff) continue;
-        for (int64_t s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(16, stages)); ++s) {
-            const int64_t per = std::max<int64_t>(1, (stages + s - 1) / s);
-            const int64_t splits = std::max<int64_t>(1, (stages + per - 1) / per);
-            if (splits != s || ti * tj * splits > 0x7fffffff) continue;
-            const uint64_t bytes = splits == 1 ? 0 : up256(static_cast<uint64_t>(splits) * p->I * ((p->J + 7) / 8 * 8) * 4);
-            if (bytes > (uint64_t{512} << 20)) continue;
-            const double rounds = static_cast<double>((ti * tj * splits + cus - 1) / cus);
-            const double us = rounds * (per * kinds[tile].step_us + kinds[tile].fixed_us) +
-                              (splits > 1 ? 4.0 + 2.0 * static_cast<double>(bytes) / 4e6 : 0.0);
-            if (!found || us < best) {
-                found = true;
-                best = us;
-                p->tile = tile;
-                p->tiles_i = ti;
-                p->tiles_j = tj;
-                p->splits = static_cast<int>(splits);
-                p->stages_per_split = per;
-                p->partial_bytes = bytes;
+        const int64_t tiles = ti * tj, rounds = tiles / cus;
+        const double tile_us = p->stages * kinds[tile].step_us + kinds[tile].fixed_us;
+        auto consider = [&](int64_t full, int64_t groups, int64_t run, bool join, double us) {
+            if (found && us >= best) return;
+            found = true;
+            best = us;
+            p->tile = tile;
+            p->tiles_i = ti;
+            p->tiles_j = tj;
+            p->full_tiles = full;
+            p->tail_groups = groups;
+            p->tail_run = run;
+            p->join = join;
+            p->partial_bytes = join ? up256(static_cast<uint64_t>(groups) * 2 * tm * tn * 4) : 0;
+        };
+        consider(tiles, 0, 1, false, static_cast<double>((tiles + cus - 1) / cus) * tile_us);
+        for (int64_t keep = rounds; keep >= std::max<int64_t>(0, rounds - 1); --keep) {
+            const int64_t tail = tiles - keep * cus;
+            if (tail == 0 || tail > 2 * cus) continue;
+            for (int part = 4; part >= 1; --part) {
+                const int64_t wanted = std::max<int64_t>(1, cus * part / 4);
+                const int64_t run = std::max<int64_t>(4, (tail * p->stages + wanted - 1) / wanted);
+                const int64_t groups = (tail * p->stages + run - 1) / run;
+                if (run >= p->stages && keep == rounds) continue;       // nothing is cut to gain by
+                const double pieces = static_cast<double>(std::min<int64_t>(2 * groups, tail + groups));
+                const double bytes = pieces * tm * tn * 4;
+                const double us = keep * tile_us + run * kinds[tile].step_us + 2 * kinds[tile].fixed_us + kJoinUs +
+                                  2 * bytes / kBytesPerUs;
+                consider(keep * cus, groups, run, true, us);
             }
         }
     }
@@ -161,16 +176,15 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
         out->tile_m = static_cast<int32_t>((p.I + 15) / 16 * 16);
         out->tile_n = 16;
         out->tile_k = 128;
-        out->splits = 1;
-        out->n_programs = static_cast<int32_t>((p.J + 15) / 16);
+        out->full_tiles = out->n_programs = static_cast<int32_t>((p.J + 15) / 16);
         return;
     }
     int threads;
     out->variant = 2;
     ag::linear_tile_shape(p.tile, &out->tile_m, &out->tile_n, &threads);
     out->tile_k = 64;
-    out->splits = p.splits;
-    out->n_programs = static_cast<int32_t>(p.tiles_i * p.tiles_j * p.splits);
+    out->full_tiles = static_cast<int32_t>(p.full_tiles);
+    out->n_programs = static_cast<int32_t>(p.full_tiles + p.tail_groups);
     out->packed = (pack_a ? 1 : 0) | (pack_b ? 2 : 0);
 }
 
@@ -213,15 +227,16 @@ ag_status_t run_product(const Product& p, const uint16_t* A, int64_t lda, const 
     a.R = p.R;
     a.tiles_i = static_cast<int32_t>(p.tiles_i);
     a.tiles_j = static_cast<int32_t>(p.tiles_j);
-    a.splits = p.splits;
-    a.stages_per_split = static_cast<int32_t>(p.stages_per_split);
+    a.stages = static_cast<int32_t>(p.stages);
+    a.full_tiles = static_cast<int32_t>(p.full_tiles);
+    a.tail_groups = static_cast<int32_t>(p.tail_groups);
+    a.tail_run = static_cast<int32_t>(p.tail_run);
     a.partial = partial;
-    a.partial_ld = (p.J + 7) / 8 * 8;
     a.epi = epi;
     hipError_t e = ag::launch_linear_gemm(a, bf16, p.form, p.tile, stream);
     if (e != hipSuccess) return fail_hip(e, "linear product");
-    if (p.splits > 1) {
-        e = ag::launch_linear_join(a, bf16, stream);
+    if (p.join) {
+        e = ag::launch_linear_join(a, bf16, p.tile, stream);
         if (e != hipSuccess) return fail_hip(e, "linear join");
     }
     return AG_OK;

@@ -1,6 +1,10 @@
 """The linear layer's and AdamW's refusals and plans without a GPU, and the pins of their oracle."""
 
 import ctypes
+import os
+import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -106,8 +110,8 @@ def test_plan_linear_counts_work_and_workspace():
     assert p.flops == 2.0 * 1000 * 3584 * 8192
     assert p.bytes_read == 2 * (1000 * 8192 + 3584 * 8192 + 3584 + 1000 * 3584) and p.bytes_written == 4 * 1000 * 3584
     q = p.product
-    assert q.variant == 2 and q.packed == 0 and p.launches == (2 if q.splits > 1 else 1)
-    assert (p.workspace_bytes > 0) == (q.splits > 1)
+    assert q.variant == 2 and q.packed == 0 and p.launches == (2 if p.workspace_bytes else 1)
+    assert q.full_tiles <= q.n_programs and -(-1000 // q.tile_m) * -(-3584 // q.tile_n) >= q.full_tiles
     few = ag.plan_linear(**dict(FORWARD, M=1))
     assert few.product.variant == 1 and few.workspace_bytes == 0 and few.launches == 1
     # rows off 4-byte alignment are copied, by the tiles alone
@@ -122,7 +126,7 @@ def test_plan_linear_backward_counts_work_and_workspace():
     assert p.workspace_bytes >= 2 * 1000 * 3584        # dz
     none = ag.plan_linear_backward(**dict(BACKWARD, act="none", z=None, db=None, dw=None, x=None))
     assert none.product_dw.variant == 0 and none.flops == 2.0 * 1000 * 3584 * 8192
-    assert none.launches == (2 if none.product.splits > 1 else 1)
+    assert none.launches == (2 if none.workspace_bytes else 1)
 
 
 def test_launches_without_a_device_report_hip_errors():
@@ -270,3 +274,72 @@ def test_oracle_random_bits_are_uniform_and_unrelated_between_seeds():
     for shift in range(-3, 4):      # no place of one seed is a shifted place of the next
         assert abs(np.mean(x * np.roll(y, shift))) < 6 / 12 / np.sqrt(n)
     assert abs(np.mean(x[1:] * x[:-1])) < 6 / 12 / np.sqrt(n)
+
+
+# ------------------------------------------------------------------ the generated code
+
+def _registers(operand):
+    """The vector registers that an operand names, e.g. v[4:7] or v9."""
+    m = re.fullmatch(r"v\[(\d+):(\d+)\]", operand)
+    if m:
+        return set(range(int(m.group(1)), int(m.group(2)) + 1))
+    m = re.fullmatch(r"v(\d+)", operand)
+    return {int(m.group(1))} if m else set()
+
+
+def unwaited_uses(lines):
+    """Instructions that touch a register which an LDS read before them may still be writing.
+
+    Straight-line: a read stays in flight until a wait for the LDS counter to reach zero.
+    """
+    flying, found = {}, []
+    for ln in lines:
+        if ln.startswith("s_waitcnt") and "lgkmcnt(0)" in ln:
+            flying.clear()
+            continue
+        parts = re.split(r"[\s,]+", ln)
+        used = set().union(*(_registers(p) for p in parts[1:])) if len(parts) > 1 else set()
+        if used & set(flying):
+            found.append(ln)
+        if ln.startswith(("ds_read_b128", "ds_read_b64_tr_b16")):
+            for r in _registers(parts[1]):
+                flying[r] = ln
+    return found
+
+
+def test_unwaited_uses_sees_a_missing_wait():
+    read = ["ds_read_b128 v[4:7], v1", "ds_read_b64_tr_b16 v[8:9], v2 offset:64"]
+    use = "v_mfma_f32_16x16x32_bf16 a[0:3], v[4:7], v[20:23], a[0:3]"
+    assert unwaited_uses(read + [use]) == [use]
+    assert unwaited_uses(read + ["v_mov_b32_e32 v30, v9"]) == ["v_mov_b32_e32 v30, v9"]
+    assert unwaited_uses(read + ["s_waitcnt lgkmcnt(0)", use]) == []
+    assert unwaited_uses(read + ["v_add_u32_e32 v1, v2, v3"]) == []
+
+
+@pytest.fixture(scope="module")
+def linear_asm(tmp_path_factory):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "gemm_all_gather_amd", "csrc")
+    out = str(tmp_path_factory.mktemp("isa") / "linear.s")
+    subprocess.run([hipcc, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
+                    "-packed-fp32-ops", f"-I{csrc}", f"-I{os.path.join(root, 'include')}", "--cuda-device-only", "-S",
+                    "-o", out, os.path.join(csrc, "ag_linear.hip")], check=True, capture_output=True)
+    return open(out).read()
+
+
+def test_product_kernels_wait_for_fragments_and_never_spill(linear_asm):
+    kernels = re.findall(r"^(_Z\S*ag_linear_gemm_kernel\S*):", linear_asm, re.M)
+    assert len(kernels) >= 12
+    for k in kernels:
+        start = linear_asm.index(f"\n{k}:")
+        lines = [ln.split(";", 1)[0].strip() for ln in linear_asm[start:linear_asm.index("s_endpgm", start)].splitlines()]
+        lines = [ln for ln in lines if ln and not ln.endswith(":")]
+        assert sum(ln.startswith("v_mfma") for ln in lines) >= 32, k
+        # the epilogue's own LDS reads are the compiler's; the loop's end with the last product
+        last = max(i for i, ln in enumerate(lines) if ln.startswith("v_mfma"))
+        assert not unwaited_uses(lines[:last + 1]), (k, unwaited_uses(lines[:last + 1])[:3])
+        meta = re.search(r"\.amdhsa_kernel " + re.escape(k) + r"\n(.*?)\.end_amdhsa_kernel", linear_asm, re.S).group(1)
+        assert re.search(r"private_segment_fixed_size 0\n", meta), k

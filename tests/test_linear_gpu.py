@@ -109,7 +109,7 @@ def test_linear_larger_sizes(M, N, K):
         log(what)
         f = Forward(M, N, K, dtype, "gelu_tanh", pad=pad)
         p = ag.plan_linear(**f.args())
-        log(f"  tile {p.product.tile_m}x{p.product.tile_n} splits {p.product.splits} packed {p.product.packed}")
+        log(f"  tile {p.product.tile_m}x{p.product.tile_n} full {p.product.full_tiles} of {p.product.n_programs} programs packed {p.product.packed}")
         f.run()
         f.check(what)
 
