@@ -85,6 +85,19 @@ __device__ __forceinline__ float sigmoid(float u)
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * u));
 }
 
+// The normal distribution's integral up to z, and exp(-z^2/2) on the way: Abramowitz and Stegun 7.1.26, erf(x) =
+// 1 - (a1 t + .. + a5 t^5) exp(-x^2) with t = 1/(1 + p x) for x = |z|/sqrt 2, within 1.5e-7 of erf (the slopes and
+// values it goes into are rounded to 2^-8 or 2^-11 of themselves).  The left tail is the polynomial itself, without
+// cancellation.  No branches: erff's would not unroll over a tile's epilogue.
+__device__ __forceinline__ float normal_integral(float z, float& gauss)
+{
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * kSqrt1_2 * fabsf(z));
+    gauss = __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
+    const float q = 0.5f * gauss * t *
+                    (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    return z < 0.f ? q : 1.f - q;
+}
+
 __device__ __forceinline__ void activate(float (&v)[8], int act)
 {
     switch (act) {   // uniform
@@ -94,7 +107,10 @@ __device__ __forceinline__ void activate(float (&v)[8], int act)
         break;
     case AG_ACT_GELU:
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.5f * v[e] * (1.f + erff(v[e] * kSqrt1_2));
+        for (int e = 0; e < 8; ++e) {
+            float gauss;
+            v[e] *= normal_integral(v[e], gauss);
+        }
         break;
     case AG_ACT_GELU_TANH:   // (1 + tanh(u))/2 = sigmoid(2u)
 #pragma unroll
@@ -118,9 +134,11 @@ __device__ __forceinline__ void apply_slope(float (&v)[8], const float (&z)[8], 
         break;
     case AG_ACT_GELU:
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] *= 0.5f * (1.f + erff(z[e] * kSqrt1_2)) +
-                    z[e] * kInvSqrt2Pi * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z[e] * z[e]);
+        for (int e = 0; e < 8; ++e) {
+            float gauss;
+            const float whole = normal_integral(z[e], gauss);
+            v[e] *= whole + z[e] * kInvSqrt2Pi * gauss;
+        }
         break;
     case AG_ACT_GELU_TANH:   // with s = sigmoid(2u): s + z s (1 - s) 2u'
 #pragma unroll
@@ -141,22 +159,10 @@ __device__ __forceinline__ void apply_slope(float (&v)[8], const float (&z)[8], 
     }
 }
 
-// Bias, pre-activation, activation, residual, earlier gradient, rounding and
-// store of n <= 8 consecutive elements (row, col..) in fp32.
+// n <= 8 consecutive gradient elements: earlier gradient, rounding, store.
 template <bool BF16>
-__device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], const LinearEpilogue& ep, int64_t row,
-                                       int64_t col, int n)
+__device__ __forceinline__ void finish_gradient(float (&v)[8], const LinearEpilogue& ep, int64_t row, int64_t col, int n)
 {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += bias[e];
-    if (ep.z) store_16<BF16>(ep.z + row * ep.ldz + col, v, n);
-    activate(v, ep.act);
-    if (ep.residual) {
-        float r[8];
-        load_f32<BF16>(r, ep.residual + row * ep.ldr + col, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += r[e];
-    }
     if (ep.out_f32) {
         float* p = static_cast<float*>(ep.out) + row * ep.ldo + col;
         if (n >= 8) {
@@ -182,6 +188,24 @@ __device__ __forceinline__ void finish(float (&v)[8], const float (&bias)[8], co
         }
         store_16<BF16>(p, v, n);
     }
+}
+
+// n <= 8 consecutive elements of a layer's output: bias, pre-activation, activation, residual, rounding, store.
+template <bool BF16>
+__device__ __forceinline__ void finish_layer(float (&v)[8], const float (&bias)[8], const LinearEpilogue& ep, int act,
+                                             int64_t row, int64_t col, int n)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    if (ep.z) store_16<BF16>(ep.z + row * ep.ldz + col, v, n);
+    activate(v, act);
+    if (ep.residual) {
+        float r[8];
+        load_f32<BF16>(r, ep.residual + row * ep.ldr + col, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+    store_16<BF16>(static_cast<uint16_t*>(ep.out) + row * ep.ldo + col, v, n);
 }
 
 }  // namespace
@@ -378,11 +402,64 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p)
 }
 __device__ __forceinline__ int64_t dword_up(int64_t bytes) { return (bytes + 3) & ~int64_t{3}; }
 
-// Work of a product: the first full_tiles tiles, one per workgroup, then the other tiles' 64-wide steps, laid
-// end to end and cut into tail_groups equal runs, one per workgroup.  A run's piece of a tile that is
-// not the whole tile goes to the workgroup's partial tile as fp32: slot 0 for the piece that starts
-// inside a tile (its first), slot 1 for one that starts with it (its last); a second kernel joins the pieces.
-template <bool BF16, int FORM, class C>
+// Work of a product: the first full_tiles tiles, a tile at a time per workgroup, round by round; then the other
+// tiles' 64-wide steps, laid end to end and cut into tail_groups equal runs, one per workgroup.  A
+// run's piece of a tile that is not the whole tile goes to the workgroup's partial tile as fp32: slot 0 for a
+// piece that starts inside a tile (its first), slot 1 for one that starts with it (its last); a second
+// kernel joins the pieces.
+struct Piece {
+    int tile, first, count;     // 64-wide steps first .. first + count - 1 of the tile; count 0: no more work
+};
+
+__device__ __forceinline__ int spread(int p, int n)
+{
+    // Workgroup p runs on XCD p % 8: every XCD gets a contiguous run of n consecutive tiles (or
+    // runs), so that its L2 serves the rows that neighbouring tiles share.
+    return (p & 7) * (n >> 3) + min(p & 7, n & 7) + (p >> 3);
+}
+
+__device__ __forceinline__ Piece piece_of(const LinearGemmArgs& a, int q)
+{
+    const int p = blockIdx.x, n = gridDim.x;
+    const int rounds = a.full_tiles / n + (p < a.full_tiles % n ? 1 : 0);
+    if (q < rounds) return Piece{q * n + spread(p, min(n, a.full_tiles - q * n)), 0, a.stages};
+    if (p >= a.tail_groups) return Piece{0, 0, 0};
+    const int tail_steps = (a.tiles_i * a.tiles_j - a.full_tiles) * a.stages;
+    const int begin = spread(p, a.tail_groups) * a.tail_run, end = min(begin + a.tail_run, tail_steps);
+    const int at = q == rounds ? begin : (begin / a.stages + (q - rounds)) * a.stages;
+    if (at >= end) return Piece{0, 0, 0};
+    const int tile = at / a.stages, first = at - tile * a.stages;
+    return Piece{a.full_tiles + tile, first, min(a.stages - first, end - at)};
+}
+
+// First row and column of a tile: the order goes 8 tile rows at a time, column by column.
+__device__ __forceinline__ void place_tile(const LinearGemmArgs& a, int t, int tile, int64_t* i0, int64_t* j0)
+{
+    constexpr int GROUP = 8;
+    const int g = t / (GROUP * a.tiles_j);
+    const int rows = min(a.tiles_i - g * GROUP, GROUP);
+    const int in_group = t - g * GROUP * a.tiles_j;
+    *i0 = static_cast<int64_t>(g * GROUP + in_group % rows) * tile;
+    *j0 = static_cast<int64_t>(in_group / rows) * tile;
+}
+
+// Two neighbouring blocks' accumulators, 4 columns each per lane of each 16-lane row, become 8 consecutive columns:
+// row q of the lanes holds columns 8 q .. 8 q + 7 of the blocks' 32.
+__device__ __forceinline__ void widen(float (&v)[8], const f32x4& x, const f32x4& y)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t xe, ye;    // moved out of the accumulation registers here, not earlier
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(xe) : "a"(x[e]));
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(ye) : "a"(y[e]));
+        u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(xe, ye, false, false));
+        t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(t.x, t.y, false, false));
+        v[e] = __uint_as_float(t.x);
+        v[4 + e] = __uint_as_float(t.y);
+    }
+}
+
+template <bool BF16, int FORM, int ACT, class C>
 __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
 {
     constexpr bool TA = FORM == kFormTN, TB = FORM != kFormNT;
@@ -407,37 +484,92 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
     ra.init(lane, wm * C::WT);
     rb.init(lane, wn * C::WT);
 
-    // Workgroup p runs on XCD p % 8: every XCD gets a contiguous run of the order (of the whole tiles
-    // and of the tail's runs alike), so that its L2 serves the rows that neighbouring tiles share.
-    const bool in_tail = static_cast<int>(blockIdx.x) >= a.full_tiles;
-    const int p = static_cast<int>(blockIdx.x) - (in_tail ? a.full_tiles : 0);
-    const int n = in_tail ? a.tail_groups : a.full_tiles;
-    const int per = n >> 3, more = n & 7;
-    const int v = (p & 7) * per + min(p & 7, more) + (p >> 3);
-    int64_t step = in_tail ? static_cast<int64_t>(a.full_tiles) * a.stages + static_cast<int64_t>(v) * a.tail_run
-                           : static_cast<int64_t>(v) * a.stages;
-    const int64_t end = in_tail ? min(step + a.tail_run, static_cast<int64_t>(a.tiles_i) * a.tiles_j * a.stages)
-                                : step + a.stages;
+    // The ring takes the parts of all the workgroup's pieces in one stream, so that the next tile's first stages
+    // are on their way during a tile's last ones and its epilogue.  A's and B's loads each walk the pieces.
+    auto start_a = [&](int q) {
+        const Piece w = piece_of(a, q);
+        int64_t i0, j0;
+        place_tile(a, w.tile, C::T, &i0, &j0);
+        return PartA::start(reinterpret_cast<uint64_t>(a.A) + static_cast<uint64_t>(TA ? i0 * 2 : i0 * lda2),
+                            TA ? dword_up((a.I - i0) * 2) : (a.I - 1 - i0) * lda2 + dword_up(a.R * 2), a.R, lda2, w.first,
+                            w.count);
+    };
+    auto start_b = [&](int q) {
+        const Piece w = piece_of(a, q);
+        int64_t i0, j0;
+        place_tile(a, w.tile, C::T, &i0, &j0);
+        return PartB::start(reinterpret_cast<uint64_t>(a.B) + static_cast<uint64_t>(TB ? j0 * 2 : j0 * ldb2),
+                            TB ? dword_up((a.J - j0) * 2) : (a.J - 1 - j0) * ldb2 + dword_up(a.R * 2), a.R, ldb2, w.first,
+                            w.count);
+    };
+    int qa = 0, qb = 0;
+    typename PartA::Next na = start_a(0);
+    typename PartB::Next nb = start_b(0);
+    auto take_a = [&] {
+        const typename PartA::At t = pa.take(na, lda2);
+        if (na.stages == 0) na = start_a(++qa);     // past the last piece: no stages, nothing more is fetched
+        return t;
+    };
+    auto take_b = [&] {
+        const typename PartB::At t = pb.take(nb, ldb2);
+        if (nb.stages == 0) nb = start_b(++qb);
+        return t;
+    };
 
-    while (step < end) {
-        const int t = static_cast<int>(step / a.stages);
-        const int first = static_cast<int>(step - static_cast<int64_t>(t) * a.stages);
-        const int count = static_cast<int>(min(end - step, static_cast<int64_t>(a.stages - first)));
-        step += count;
-        // tile order: 8 tile rows at a time, column by column
-        constexpr int GROUP = 8;
-        const int g = t / (GROUP * a.tiles_j);
-        const int gm = min(a.tiles_i - g * GROUP, GROUP);
-        const int in_group = t - g * GROUP * a.tiles_j;
-        const int64_t i0 = static_cast<int64_t>(g * GROUP + in_group % gm) * C::T;
-        const int64_t j0 = static_cast<int64_t>(in_group / gm) * C::T;
+    V fa[2][NB], fb[2][NB];   // fragments of the two 32-wide halves of a stage
+    auto wrap = [](int slot) { return slot >= NP ? slot - NP : slot; };
+    // The last 16-byte chunk of an r-contiguous row holds elements past the reduction's end when R is no multiple
+    // of 8: they are set to zero in LDS, once, when a tile's last stage has landed.
+    const bool ragged = !(TA && TB) && (a.R & 7) != 0;
+    auto clear_tail = [&](int slot_a, int slot_b) {
+        const uint32_t chunk = static_cast<uint32_t>(a.R & 63) >> 3, from = static_cast<uint32_t>(a.R & 7);
+        for (int row = tid; row < 2 * C::T; row += C::NT) {
+            if ((TA && row < C::T) || (TB && row >= C::T)) continue;
+            const int r = row < C::T ? row : row - C::T;
+            uint16_t* c = reinterpret_cast<uint16_t*>(ring + (row < C::T ? slot_a : slot_b) * C::PART + r * 128 +
+                                                      ((chunk ^ (static_cast<uint32_t>(r) & 7u)) << 4));
+            for (uint32_t e = from; e < 8; ++e) c[e] = 0;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto read = [&](int f, uint32_t part_a, uint32_t part_b, int kk, int i) {   // i-th fragment: A's blocks, then B's
+        if (i < NB) ra.read(fa[f][i], part_a, kk, i);
+        else rb.read(fb[f][i - NB], part_b, kk, i - NB);
+    };
+    const uint32_t lds = lds_address(ring);
 
-        typename PartA::Next na = PartA::start(reinterpret_cast<uint64_t>(a.A) + static_cast<uint64_t>(TA ? i0 * 2 : i0 * lda2),
-                                               TA ? dword_up((a.I - i0) * 2) : (a.I - 1 - i0) * lda2 + dword_up(a.R * 2),
-                                               a.R, lda2, first, count);
-        typename PartB::Next nb = PartB::start(reinterpret_cast<uint64_t>(a.B) + static_cast<uint64_t>(TB ? j0 * 2 : j0 * ldb2),
-                                               TB ? dword_up((a.J - j0) * 2) : (a.J - 1 - j0) * ldb2 + dword_up(a.R * 2),
-                                               a.R, ldb2, first, count);
+    // prologue: all slots on their way, the first stage landed and its first fragments read
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        if (q % 2 == 0) {
+            const typename PartA::At la = take_a();
+#pragma unroll
+            for (int j = 0; j < C::LOADS; ++j) PartA::load(la, ring + q * C::PART, wave, j);
+        } else {
+            const typename PartB::At lb = take_b();
+#pragma unroll
+            for (int j = 0; j < C::LOADS; ++j) PartB::load(lb, ring + q * C::PART, wave, j);
+        }
+    }
+    wait_vmcnt<(NP - 2) * C::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    Piece w = piece_of(a, 0);
+    if (ragged && w.count == 1 && w.first + 1 == a.stages) clear_tail(0, 1);
+#pragma unroll
+    for (int i = 0; i < 2 * NB; ++i) read(0, lds, lds + C::PART, 0, i);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_lgkmcnt0();
+    __builtin_amdgcn_sched_barrier(0);
+
+    int slot = 0;               // of the stage's A part; its B part lies in the next one
+    for (int q = 0; w.count > 0;) {
+        const Piece next = piece_of(a, q + 1);
+        // whether the stage after the piece's last is a tile's last one too
+        const bool next_short = next.count > 0 && next.first + 1 == a.stages;
+        const bool ends = w.first + w.count == a.stages;
 
         f32x4 acc[NB][NB];
 #pragma unroll
@@ -448,54 +580,6 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
                 asm volatile("" : "+a"(acc[bm][bn]));
             }
         settle();
-        V fa[2][NB], fb[2][NB];   // fragments of the two 32-wide halves of a stage
-
-        // Part 2 s (A) and 2 s + 1 (B) of stage s lie in slots 2 s % NP and (2 s + 1) % NP.
-        auto wrap = [](int slot) { return slot >= NP ? slot - NP : slot; };
-        // The last 16-byte chunk of an r-contiguous row holds elements past the reduction's end when R is no
-        // multiple of 8: they are set to zero in LDS, once, when the last stage has landed.
-        const bool tail = !(TA && TB) && (a.R & 7) != 0 && first + count == a.stages;
-        auto clear_tail = [&](int slot_a, int slot_b) {
-            const uint32_t chunk = static_cast<uint32_t>(a.R & 63) >> 3, from = static_cast<uint32_t>(a.R & 7);
-            for (int row = tid; row < 2 * C::T; row += C::NT) {
-                if ((TA && row < C::T) || (TB && row >= C::T)) continue;
-                const int r = row < C::T ? row : row - C::T;
-                uint16_t* c = reinterpret_cast<uint16_t*>(ring + (row < C::T ? slot_a : slot_b) * C::PART + r * 128 +
-                                                          ((chunk ^ (static_cast<uint32_t>(r) & 7u)) << 4));
-                for (uint32_t e = from; e < 8; ++e) c[e] = 0;
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        auto read = [&](int f, uint32_t part_a, uint32_t part_b, int kk, int i) {   // i-th fragment: A's blocks, then B's
-            if (i < NB) ra.read(fa[f][i], part_a, kk, i);
-            else rb.read(fb[f][i - NB], part_b, kk, i - NB);
-        };
-        const uint32_t lds = lds_address(ring);
-
-        // prologue: all slots on their way, the first stage landed and its first fragments read
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            if (q % 2 == 0) {
-                const typename PartA::At la = pa.take(na, lda2);
-#pragma unroll
-                for (int j = 0; j < C::LOADS; ++j) PartA::load(la, ring + q * C::PART, wave, j);
-            } else {
-                const typename PartB::At lb = pb.take(nb, ldb2);
-#pragma unroll
-                for (int j = 0; j < C::LOADS; ++j) PartB::load(lb, ring + q * C::PART, wave, j);
-            }
-        }
-        wait_vmcnt<(NP - 2) * C::LOADS>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        if (tail && count == 1) clear_tail(0, 1);
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) read(0, lds, lds + C::PART, 0, i);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_lgkmcnt0();
-        __builtin_amdgcn_sched_barrier(0);
 
         // A stage is two halves of NB x NB products each.  Between the first half's products the second half's
         // fragments are read; then this wave's reads of the stage's slots are complete and the next stage has
@@ -505,9 +589,8 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         // per 22 cycles per CU), so loads in a row would leave the matrix pipe idle.  The order is pinned by
         // scheduling barriers (scalar and address arithmetic may cross them); the fragment reads are
         // waited for as a whole before the half that uses them.
-        int slot = 0;
 #pragma unroll 1
-        for (int s = 0; s < count; ++s) {
+        for (int s = 0; s < w.count; ++s) {
             const int slot_b = wrap(slot + 1), next_a = wrap(slot + 2), next_b = wrap(slot + 3);
             const uint32_t here_a = lds + slot * C::PART, here_b = lds + slot_b * C::PART;
             const uint32_t there_a = lds + next_a * C::PART, there_b = lds + next_b * C::PART;
@@ -517,19 +600,19 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
                 mfma<BF16>(acc[i / NB][i % NB], fb[0][i % NB], fa[0][i / NB]);
                 __builtin_amdgcn_sched_barrier(0x6);
             }
-            const typename PartA::At la = pa.take(na, lda2);
-            const typename PartB::At lb = pb.take(nb, ldb2);
+            const typename PartA::At la = take_a();
+            const typename PartB::At lb = take_b();
             __builtin_amdgcn_sched_barrier(0);
             wait_lgkmcnt0();
             wait_vmcnt<(NP - 4) * C::LOADS>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            if (tail && s + 2 == count) clear_tail(next_a, next_b);
+            if (ragged && (s + 2 == w.count ? ends : s + 1 == w.count && next_short)) clear_tail(next_a, next_b);
 #pragma unroll
             for (int i = 0; i < NB * NB; ++i) {
                 if (i % C::READ_STEP == 0 && i / C::READ_STEP < 2 * NB) read(0, there_a, there_b, 0, i / C::READ_STEP);
                 if (i % C::LOAD_STEP == C::LOAD_STEP - 1) {
-                    // parts 2 s + NP and 2 s + NP + 1: B first where NP is odd
+                    // parts NP and NP + 1 further on: B first where NP is odd
                     const int j = i / C::LOAD_STEP;
                     uint8_t* dst = ring + (j < C::LOADS ? slot : slot_b) * C::PART;
                     if ((j < C::LOADS) == (NP % 2 == 0)) PartA::load(la, dst, wave, j % C::LOADS);
@@ -545,51 +628,53 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         }
         settle();
 
-        // ---- epilogue.  A lane's accumulators hold 4 consecutive columns of one row of each block; every wave
-        // passes its sub-tile through its own piece of LDS, 16 rows at a time in fp32, and then holds 8
-        // consecutive columns per lane and whole row pieces per group of lanes: wide, coalesced accesses for
-        // the residual, the pre-activation and the output, and the one rounding at the very end.
-        wait_vmcnt<0>();   // loads of stages past the end have landed too
-        wait_lgkmcnt0();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        uint8_t* mine = ring + wave * (16 * C::C_PITCH);
-        const int tile_col = wn * C::WT + (lane % C::LPR) * 8;
-        const int64_t col = j0 + tile_col;
-        const int n_col = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
-        const bool whole = count == a.stages;
-        float* partial = a.partial + (static_cast<int64_t>(v) * 2 + (first == 0 ? 1 : 0)) * (C::T * C::T) + tile_col;
-        float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (whole && a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n_col);
+        // ---- epilogue, from the registers: a lane's accumulators hold 4 consecutive columns of one row of each
+        // block; lanes trade halves of neighbouring blocks, and each then has 8 consecutive columns in fp32 for
+        // 16-byte accesses (64 bytes of a row together) and the one rounding at the very end.
+        int64_t i0, j0;
+        place_tile(a, w.tile, C::T, &i0, &j0);
+        const bool whole = w.count == a.stages;
+        int own = lane;
+        asm volatile("" : "+v"(own));   // opaque: the lane's addresses are made here, not kept across the loop
+        const int tile_row = wm * C::WT + (own & 15), tile_col = wn * C::WT + (own >> 4) * 8;
+        float bias[NB / 2][8];
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) bias[b][e] = 0.f;
+            const int64_t left = a.J - (j0 + tile_col + 32 * b);
+            if (FORM == kFormNT && whole && a.epi.bias && left > 0)
+                load_f32<BF16>(bias[b], a.epi.bias + j0 + tile_col + 32 * b, static_cast<int>(min(int64_t{8}, left)));
+        }
+        float* partial = a.partial + (static_cast<int64_t>(spread(blockIdx.x, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
+                                         (C::T * C::T);
 #pragma unroll
         for (int bm = 0; bm < NB; ++bm) {
+            const int64_t row = i0 + tile_row + 16 * bm;
 #pragma unroll
-            for (int bn = 0; bn < NB; ++bn)
-                *reinterpret_cast<f32x4*>(mine + (lane & 15) * C::C_PITCH + (bn * 16 + (lane >> 4) * 4) * 4) = acc[bm][bn];
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 1
-            for (int pass = 0; pass < 16 / C::RPP; ++pass) {
-                const int r = pass * C::RPP + lane / C::LPR;
-                const f32x4* src = reinterpret_cast<const f32x4*>(mine + r * C::C_PITCH + (lane % C::LPR) * 32);
-                const f32x4 lo = src[0], hi = src[1];
-                const int tile_row = wm * C::WT + bm * 16 + r;
-                const int64_t row = i0 + tile_row;
-                if (row < a.I && n_col > 0) {
-                    if (whole) {
-                        float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                        finish<BF16>(x, bias, a.epi, row, col, n_col);
+            for (int b = 0; b < NB / 2; ++b) {
+                float x[8];
+                widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                const int64_t col = j0 + tile_col + 32 * b;
+                const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
+                if (row < a.I && n > 0) {
+                    if (!whole) {
+                        f32x4* d = reinterpret_cast<f32x4*>(partial + (tile_row + 16 * bm) * C::T + tile_col + 32 * b);
+                        d[0] = f32x4{x[0], x[1], x[2], x[3]};
+                        d[1] = f32x4{x[4], x[5], x[6], x[7]};
+                    } else if constexpr (FORM == kFormNT) {
+                        finish_layer<BF16>(x, bias[b], a.epi, ACT, row, col, n);
                     } else {
-                        f32x4* d = reinterpret_cast<f32x4*>(partial + tile_row * C::T);
-                        d[0] = lo;
-                        d[1] = hi;
+                        finish_gradient<BF16>(x, a.epi, row, col, n);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
             }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        __builtin_amdgcn_s_barrier();   // staging reads done before the next piece's loads land
-        __builtin_amdgcn_sched_barrier(0);
+        w = next;
+        ++q;
     }
+    wait_vmcnt<0>();   // loads past the last stage write LDS: they end with the workgroup
 }
 
 // 256 x 256: a wave's 128 x 128 sub-tile keeps LDS reads (128 KiB a stage) and the slots' refill (64 KiB) below
@@ -599,12 +684,20 @@ using Cfg256 = linear_cfg::Cfg<256, 5>;
 using Cfg128 = linear_cfg::Cfg<128, 10>;
 
 using LinearFn = void (*)(LinearGemmArgs);
-template <bool BF16, class C> LinearFn pick_form(int form)
+template <bool BF16, class C> LinearFn pick_form(int form, int act)
 {
     switch (form) {
-    case kFormNT: return ag_linear_gemm_kernel<BF16, kFormNT, C>;
-    case kFormNN: return ag_linear_gemm_kernel<BF16, kFormNN, C>;
-    case kFormTN: return ag_linear_gemm_kernel<BF16, kFormTN, C>;
+    case kFormNT:
+        switch (act) {
+        case AG_ACT_NONE: return ag_linear_gemm_kernel<BF16, kFormNT, AG_ACT_NONE, C>;
+        case AG_ACT_RELU: return ag_linear_gemm_kernel<BF16, kFormNT, AG_ACT_RELU, C>;
+        case AG_ACT_GELU: return ag_linear_gemm_kernel<BF16, kFormNT, AG_ACT_GELU, C>;
+        case AG_ACT_GELU_TANH: return ag_linear_gemm_kernel<BF16, kFormNT, AG_ACT_GELU_TANH, C>;
+        case AG_ACT_SILU: return ag_linear_gemm_kernel<BF16, kFormNT, AG_ACT_SILU, C>;
+        default: return nullptr;
+        }
+    case kFormNN: return ag_linear_gemm_kernel<BF16, kFormNN, AG_ACT_NONE, C>;
+    case kFormTN: return ag_linear_gemm_kernel<BF16, kFormTN, AG_ACT_NONE, C>;
     default: return nullptr;
     }
 }
@@ -612,29 +705,26 @@ template <bool BF16, class C> LinearFn pick_form(int form)
 // ---------------------------------------------------------------- join of cut tiles
 
 // Adds the pieces of a tail tile in the reduction's order, 8 consecutive columns per thread, then the epilogue.
-template <bool BF16>
-__global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, int tm, int tn)
+template <bool BF16, bool LAYER>
+__global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, int tile)
 {
-    const int per_tile = tm * tn / 2048;           // workgroups
+    const int per_tile = tile * tile / 2048;       // workgroups
     const int tail_tile = static_cast<int>(blockIdx.x) / per_tile;
-    const int t = a.full_tiles + tail_tile;
-    const int64_t begin = static_cast<int64_t>(tail_tile) * a.stages, end = begin + a.stages;
-    const int g0 = static_cast<int>(begin / a.tail_run), g1 = static_cast<int>((end - 1) / a.tail_run);
+    const int begin = tail_tile * a.stages, end = begin + a.stages;
+    const int g0 = begin / a.tail_run, g1 = (end - 1) / a.tail_run;
     if (g0 == g1) return;                          // one workgroup had the whole tile
     const int id = (static_cast<int>(blockIdx.x) % per_tile) * 256 + threadIdx.x;
-    const int tile_row = id / (tn / 8), tile_col = (id % (tn / 8)) * 8;
-    constexpr int GROUP = 8;
-    const int g = t / (GROUP * a.tiles_j);
-    const int gm = min(a.tiles_i - g * GROUP, GROUP);
-    const int in_group = t - g * GROUP * a.tiles_j;
-    const int64_t row = static_cast<int64_t>(g * GROUP + in_group % gm) * tm + tile_row;
-    const int64_t col = static_cast<int64_t>(in_group / gm) * tn + tile_col;
+    const int tile_row = id / (tile / 8), tile_col = (id % (tile / 8)) * 8;
+    int64_t row, col;
+    place_tile(a, a.full_tiles + tail_tile, tile, &row, &col);
+    row += tile_row;
+    col += tile_col;
     if (row >= a.I || col >= a.J) return;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int q = g0; q <= g1; ++q) {
-        const bool starts = static_cast<int64_t>(q) * a.tail_run <= begin;      // the piece that holds the first step
-        const f32x4* src = reinterpret_cast<const f32x4*>(a.partial + (static_cast<int64_t>(q) * 2 + (starts ? 1 : 0)) * (tm * tn) +
-                                                          tile_row * tn + tile_col);
+        const bool starts = q * a.tail_run <= begin;      // the piece that holds the first step
+        const f32x4* src = reinterpret_cast<const f32x4*>(a.partial + (static_cast<int64_t>(q) * 2 + (starts ? 1 : 0)) * (tile * tile) +
+                                                          tile_row * tile + tile_col);
         const f32x4 lo = src[0], hi = src[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -644,8 +734,12 @@ __global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, i
     }
     const int n = static_cast<int>(min(int64_t{8}, a.J - col));
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
-    finish<BF16>(v, bias, a.epi, row, col, n);
+    if constexpr (LAYER) {
+        if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
+        finish_layer<BF16>(v, bias, a.epi, a.epi.act, row, col, n);
+    } else {
+        finish_gradient<BF16>(v, a.epi, row, col, n);
+    }
 }
 
 // ---------------------------------------------------------------- a few rows of x
@@ -736,7 +830,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void ag_linear_stream_kernel(Lin
             float v[8] = {s[0], s[1], s[2], s[3], 0.f, 0.f, 0.f, 0.f};
             float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
-            finish<BF16>(v, bias, a.epi, m, col, n);
+            finish_layer<BF16>(v, bias, a.epi, a.epi.act, m, col, n);
         }
     }
 }
@@ -842,13 +936,12 @@ void linear_tile_shape(int tile, int* tm, int* tn, int* threads)
     *threads = Cfg256::NT;
 }
 
-hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream)
+hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, int programs, hipStream_t stream)
 {
-    LinearFn fn = tile == kLinearTile256 ? (bf16 ? pick_form<true, Cfg256>(form) : pick_form<false, Cfg256>(form))
-                                         : (bf16 ? pick_form<true, Cfg128>(form) : pick_form<false, Cfg128>(form));
-    const int64_t grid = static_cast<int64_t>(a.full_tiles) + a.tail_groups;
-    if (fn == nullptr || grid < 1 || grid > 0x7fffffff || a.stages < 1) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(grid)), dim3(Cfg256::NT), 0, stream, a);
+    LinearFn fn = tile == kLinearTile256 ? (bf16 ? pick_form<true, Cfg256>(form, a.epi.act) : pick_form<false, Cfg256>(form, a.epi.act))
+                                         : (bf16 ? pick_form<true, Cfg128>(form, a.epi.act) : pick_form<false, Cfg128>(form, a.epi.act));
+    if (fn == nullptr || programs < 1 || programs < a.tail_groups || a.stages < 1 || a.tail_run < 1) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(Cfg256::NT), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -862,14 +955,16 @@ bool grid_of(int64_t work, int64_t per, dim3* grid)
 }
 }  // namespace
 
-hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int tile, hipStream_t stream)
+hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream)
 {
-    int tm, tn, threads;
-    linear_tile_shape(tile, &tm, &tn, &threads);
+    int t, threads;
+    linear_tile_shape(tile, &t, &t, &threads);
     const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j - a.full_tiles;
     dim3 grid;
-    if (!grid_of(tiles * (tm * tn / 2048), 1, &grid)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(bf16 ? ag_linear_join_kernel<true> : ag_linear_join_kernel<false>, grid, dim3(256), 0, stream, a, tm, tn);
+    if (!grid_of(tiles * (t * t / 2048), 1, &grid)) return hipErrorInvalidValue;
+    auto fn = form == kFormNT ? (bf16 ? ag_linear_join_kernel<true, true> : ag_linear_join_kernel<false, true>)
+                              : (bf16 ? ag_linear_join_kernel<true, false> : ag_linear_join_kernel<false, false>);
+    hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, a, t);
     return hipGetLastError();
 }
 

@@ -109,7 +109,7 @@ struct Product {
     int form = ag::kFormNT, tile = ag::kLinearTile128;
     int64_t I = 0, J = 0, R = 0;
     int64_t tiles_i = 0, tiles_j = 0, stages = 0;
-    int64_t full_tiles = 0, tail_groups = 0, tail_run = 0;
+    int64_t full_tiles = 0, tail_groups = 0, tail_run = 0, programs = 0;
     bool join = false;           // some tail tile is cut
     uint64_t partial_bytes = 0;
     int launches() const { return !on ? 0 : join ? 2 : 1; }
@@ -131,7 +131,7 @@ ag_status_t choose(Product* p, int cus)
         int tm, tn, threads;
         ag::linear_tile_shape(tile, &tm, &tn, &threads);
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
-        if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffffff) continue;
+        if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffff00) continue;
         const int64_t tiles = ti * tj, rounds = tiles / cus;
         const double tile_us = p->stages * kinds[tile].step_us + kinds[tile].fixed_us;
         auto consider = [&](int64_t full, int64_t groups, int64_t run, bool join, double us) {
@@ -144,13 +144,14 @@ ag_status_t choose(Product* p, int cus)
             p->full_tiles = full;
             p->tail_groups = groups;
             p->tail_run = run;
+            p->programs = std::max(groups, std::min<int64_t>(full, cus));
             p->join = join;
             p->partial_bytes = join ? up256(static_cast<uint64_t>(groups) * 2 * tm * tn * 4) : 0;
         };
         consider(tiles, 0, 1, false, static_cast<double>((tiles + cus - 1) / cus) * tile_us);
         for (int64_t keep = rounds; keep >= std::max<int64_t>(0, rounds - 1); --keep) {
             const int64_t tail = tiles - keep * cus;
-            if (tail == 0 || tail > 2 * cus) continue;
+            if (tail == 0 || tail > 2 * cus || tail * p->stages > 0x3fffffff) continue;
             for (int part = 4; part >= 1; --part) {
                 const int64_t wanted = std::max<int64_t>(1, cus * part / 4);
                 const int64_t run = std::max<int64_t>(4, (tail * p->stages + wanted - 1) / wanted);
@@ -184,7 +185,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
     ag::linear_tile_shape(p.tile, &out->tile_m, &out->tile_n, &threads);
     out->tile_k = 64;
     out->full_tiles = static_cast<int32_t>(p.full_tiles);
-    out->n_programs = static_cast<int32_t>(p.full_tiles + p.tail_groups);
+    out->n_programs = static_cast<int32_t>(p.programs);
     out->packed = (pack_a ? 1 : 0) | (pack_b ? 2 : 0);
 }
 
@@ -233,10 +234,10 @@ ag_status_t run_product(const Product& p, const uint16_t* A, int64_t lda, const 
     a.tail_run = static_cast<int32_t>(p.tail_run);
     a.partial = partial;
     a.epi = epi;
-    hipError_t e = ag::launch_linear_gemm(a, bf16, p.form, p.tile, stream);
+    hipError_t e = ag::launch_linear_gemm(a, bf16, p.form, p.tile, static_cast<int>(p.programs), stream);
     if (e != hipSuccess) return fail_hip(e, "linear product");
     if (p.join) {
-        e = ag::launch_linear_join(a, bf16, p.tile, stream);
+        e = ag::launch_linear_join(a, bf16, p.form, p.tile, stream);
         if (e != hipSuccess) return fail_hip(e, "linear join");
     }
     return AG_OK;
