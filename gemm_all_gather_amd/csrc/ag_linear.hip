@@ -238,6 +238,8 @@ struct Cfg {
 
 namespace {
 
+__device__ __forceinline__ int64_t dword_up(int64_t bytes) { return (bytes + 3) & ~int64_t{3}; }
+
 // One operand's part of an LDS stage.  A wave instruction moves 1 KiB, lane l
 // to bytes [16 l, 16 l + 16) of it; the waves share the part's T/8 instructions.
 //
@@ -254,73 +256,74 @@ struct Part {
     static constexpr int STEP = RPI * C::NW;               // stage rows between a wave's instructions
     static constexpr int UNITS = T / 16;                   // transposed: 32-byte units per row
 
-    uint32_t off[TR && STEP == 8 ? 2 : 1];   // lane's byte offset within the operand tile, first instruction
-    uint32_t r_lane;                         // r-contiguous: first r of the lane's chunk within the stage
+    uint32_t off[J];    // lane's byte offset within the operand tile's stage, per instruction
 
     __device__ __forceinline__ void init(int lane, int wave, uint32_t ld2)
     {
         if constexpr (TR) {
-            static_assert(STEP == 8 || STEP == 16, "f changes with the instruction by bit 2 alone, or not");
             constexpr int LPR = 64 / RPI;                  // lanes per stage row
-            const uint32_t row = static_cast<uint32_t>(wave * RPI + lane / LPR);   // < STEP
-            const uint32_t f = (row & 3u) | (((row >> 3) & 1u) << 2);
             const uint32_t c = static_cast<uint32_t>(lane % LPR);
-            const uint32_t col = (((c >> 1) ^ f) << 5) | ((c & 1u) << 4);
-            off[0] = row * ld2 + col;
-            if constexpr (STEP == 8) off[1] = row * ld2 + (col ^ 128u);          // rows with bit 3 set
-            r_lane = 0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint32_t row = static_cast<uint32_t>(wave * RPI + lane / LPR + STEP * j);
+                const uint32_t f = (row & 3u) | (((row >> 3) & 1u) << 2);
+                off[j] = row * ld2 + ((((c >> 1) ^ f) << 5) | ((c & 1u) << 4));
+            }
         } else {
             const uint32_t row = static_cast<uint32_t>(lane >> 3);
             const uint32_t chunk = static_cast<uint32_t>(lane & 7) ^ row;
-            off[0] = (static_cast<uint32_t>(wave * 8) + row) * ld2 + chunk * 16u;
-            r_lane = chunk * 8u;
+#pragma unroll
+            for (int j = 0; j < J; ++j) off[j] = (static_cast<uint32_t>(wave * 8 + STEP * j) + row) * ld2 + chunk * 16u;
         }
     }
 
-    // The operand tile's next stage to load.  The descriptor starts at the stage and ends with the operand, so
-    // that what lies past the reduction's or the last column's end reads as zero and nothing past the operand
-    // is read; the end is rounded up to 4 bytes because the range check works on whole dwords (operands are
-    // 4-byte aligned: the dword of the last element is the operand's own).
+    // The operand tile's next stage to load.  Its descriptor starts at the stage and ends with the operand, so that
+    // what lies past the operand is neither read nor anything but zero; the end is rounded up to 4 bytes
+    // because the range check works on whole dwords (operands are 4-byte aligned: the dword of the last
+    // element is the operand's own).
     struct Next {
         uint64_t base;
-        int64_t bytes;      // from base to the operand's end
-        int32_t r_left;     // of the reduction, from the stage
-        int32_t stages;     // still to load; past them loads fetch nothing (and write zeros)
+        int32_t bytes;      // r-contiguous: from base to the end of the tile's rows; transposed: of a row, from base
+        int32_t r_left;     // transposed: rows of the reduction from the stage on
+        int32_t stages;     // still to load
     };
-    // tile: the operand at the tile's first row or column; extent: bytes from there to the operand's
-    // end (r-contiguous), or of its row's rest (transposed).
-    static __device__ __forceinline__ Next start(uint64_t tile, int64_t extent, int64_t R, uint32_t ld2, int first, int count)
+    // operand: its address; at, size: the tile's first row (column) and the operand's number of them.
+    static __device__ __forceinline__ Next start(const uint16_t* operand, int64_t at, int64_t size, int64_t R, uint32_t ld2,
+                                                 int first, int count)
     {
         const int64_t r0 = static_cast<int64_t>(first) * 64;
-        const int64_t skip = TR ? r0 * ld2 : r0 * 2;
-        return Next{tile + static_cast<uint64_t>(skip), TR ? (R - 1 - r0) * static_cast<int64_t>(ld2) + extent : extent - skip,
-                    static_cast<int32_t>(R - r0), count};
+        const int64_t place = TR ? r0 * ld2 + at * 2 : at * ld2 + r0 * 2;
+        const int64_t bytes = TR ? dword_up((size - at) * 2) : (min(size - at, int64_t{T}) - 1) * ld2 + dword_up((R - r0) * 2);
+        const bool live = count > 0 && R > 0;
+        return Next{reinterpret_cast<uint64_t>(operand) + static_cast<uint64_t>(place),
+                    live ? static_cast<int32_t>(min(bytes, int64_t{0x7fffffff})) : 0, live ? static_cast<int32_t>(R - r0) : 0, count};
     }
+    // The stage's descriptor (base and size); n moves on to the next one.
     struct At {
         uint64_t base;
-        uint32_t records, o0, o1, ld2;
+        uint32_t records;
     };
-    // The stage's load addresses; n moves on to the next one.
-    __device__ __forceinline__ At take(Next& n, uint32_t ld2) const
+    static __device__ __forceinline__ At take(Next& n, uint32_t ld2)
     {
-        const bool live = n.stages > 0 && n.r_left > 0;
-        At t{n.base, live ? static_cast<uint32_t>(min(n.bytes, int64_t{0x7fffffff})) : 0u, off[0],
-             off[TR && STEP == 8 ? 1 : 0], ld2};
-        if constexpr (!TR) t.o0 = static_cast<int32_t>(r_lane) < n.r_left ? t.o0 : kOutOfRange;   // the next row's chunks
-        // opaque copies: the instructions' offsets are not kept in registers across the loop
-        asm volatile("" : "+v"(t.o0), "+v"(t.o1), "+s"(t.ld2));
-        const int64_t step = TR ? static_cast<int64_t>(ld2) * 64 : 128;
-        n.base += static_cast<uint64_t>(step);
-        n.bytes -= step;
-        n.r_left -= 64;
+        At t;
+        t.base = n.base;
+        if constexpr (TR) {
+            t.records = n.r_left > 0 ? static_cast<uint32_t>(min(n.r_left, 64) - 1) * ld2 + static_cast<uint32_t>(n.bytes) : 0u;
+            n.base += static_cast<uint64_t>(ld2) * 64;
+            n.r_left -= 64;
+        } else {
+            t.records = static_cast<uint32_t>(max(n.bytes, 0));
+            n.base += 128;
+            n.bytes -= 128;
+        }
         n.stages -= 1;
         return t;
     }
-    static __device__ __forceinline__ void load(const At& t, uint8_t* dst, int wave, int j)
+    __device__ __forceinline__ void load(const At& t, uint8_t* dst, int j) const { fetch(t, dst + C::NW * j * 1024, off[j]); }
+    static __device__ __forceinline__ void fetch(const At& t, uint8_t* dst, uint32_t at)
     {
-        const uint32_t o = TR && STEP == 8 && (j & 1) ? t.o1 : t.o0;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(t.base, t.records), (AG_LDS void*)(dst + (wave + C::NW * j) * 1024),
-                                                 16, o + static_cast<uint32_t>(STEP * j) * t.ld2, 0, 0, 0);
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(t.base, t.records);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AG_LDS void*)dst, 16, at, 0, 0, 0);
     }
 };
 
@@ -400,7 +403,6 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p)
 {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((AG_LDS const uint8_t*)p));
 }
-__device__ __forceinline__ int64_t dword_up(int64_t bytes) { return (bytes + 3) & ~int64_t{3}; }
 
 // Work of a product: the first full_tiles tiles, a tile at a time per workgroup, round by round; then the other
 // tiles' 64-wide steps, laid end to end and cut into tail_groups equal runs, one per workgroup.  A
@@ -490,45 +492,47 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         const Piece w = piece_of(a, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::T, &i0, &j0);
-        return PartA::start(reinterpret_cast<uint64_t>(a.A) + static_cast<uint64_t>(TA ? i0 * 2 : i0 * lda2),
-                            TA ? dword_up((a.I - i0) * 2) : (a.I - 1 - i0) * lda2 + dword_up(a.R * 2), a.R, lda2, w.first,
-                            w.count);
+        return PartA::start(a.A, i0, a.I, a.R, lda2, w.first, w.count);
     };
     auto start_b = [&](int q) {
         const Piece w = piece_of(a, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::T, &i0, &j0);
-        return PartB::start(reinterpret_cast<uint64_t>(a.B) + static_cast<uint64_t>(TB ? j0 * 2 : j0 * ldb2),
-                            TB ? dword_up((a.J - j0) * 2) : (a.J - 1 - j0) * ldb2 + dword_up(a.R * 2), a.R, ldb2, w.first,
-                            w.count);
+        return PartB::start(a.B, j0, a.J, a.R, ldb2, w.first, w.count);
     };
     int qa = 0, qb = 0;
     typename PartA::Next na = start_a(0);
     typename PartB::Next nb = start_b(0);
     auto take_a = [&] {
-        const typename PartA::At t = pa.take(na, lda2);
+        const typename PartA::At t = PartA::take(na, lda2);
         if (na.stages == 0) na = start_a(++qa);     // past the last piece: no stages, nothing more is fetched
         return t;
     };
     auto take_b = [&] {
-        const typename PartB::At t = pb.take(nb, ldb2);
+        const typename PartB::At t = PartB::take(nb, ldb2);
         if (nb.stages == 0) nb = start_b(++qb);
         return t;
     };
 
     V fa[2][NB], fb[2][NB];   // fragments of the two 32-wide halves of a stage
     auto wrap = [](int slot) { return slot >= NP ? slot - NP : slot; };
-    // The last 16-byte chunk of an r-contiguous row holds elements past the reduction's end when R is no multiple
-    // of 8: they are set to zero in LDS, once, when a tile's last stage has landed.
-    const bool ragged = !(TA && TB) && (a.R & 7) != 0;
+    // Where the reduction is no multiple of 64, the last stage of an r-contiguous operand goes on into the next
+    // rows: that is set to zero in LDS, once, when a tile's last stage has landed.
+    const bool ragged = !(TA && TB) && (a.R & 63) != 0;
     auto clear_tail = [&](int slot_a, int slot_b) {
-        const uint32_t chunk = static_cast<uint32_t>(a.R & 63) >> 3, from = static_cast<uint32_t>(a.R & 7);
+        const uint32_t from = static_cast<uint32_t>(a.R & 63);
         for (int row = tid; row < 2 * C::T; row += C::NT) {
             if ((TA && row < C::T) || (TB && row >= C::T)) continue;
             const int r = row < C::T ? row : row - C::T;
-            uint16_t* c = reinterpret_cast<uint16_t*>(ring + (row < C::T ? slot_a : slot_b) * C::PART + r * 128 +
-                                                      ((chunk ^ (static_cast<uint32_t>(r) & 7u)) << 4));
-            for (uint32_t e = from; e < 8; ++e) c[e] = 0;
+            uint8_t* line = ring + (row < C::T ? slot_a : slot_b) * C::PART + r * 128;
+            for (uint32_t c = from >> 3; c < 8; ++c) {
+                uint8_t* chunk = line + ((c ^ (static_cast<uint32_t>(r) & 7u)) << 4);
+                if (c * 8 >= from) {
+                    *reinterpret_cast<u32x4*>(chunk) = u32x4{0u, 0u, 0u, 0u};
+                } else {
+                    for (uint32_t e = from & 7u; e < 8; ++e) reinterpret_cast<uint16_t*>(chunk)[e] = 0;
+                }
+            }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -546,11 +550,11 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         if (q % 2 == 0) {
             const typename PartA::At la = take_a();
 #pragma unroll
-            for (int j = 0; j < C::LOADS; ++j) PartA::load(la, ring + q * C::PART, wave, j);
+            for (int j = 0; j < C::LOADS; ++j) pa.load(la, ring + q * C::PART + wave * 1024, j);
         } else {
             const typename PartB::At lb = take_b();
 #pragma unroll
-            for (int j = 0; j < C::LOADS; ++j) PartB::load(lb, ring + q * C::PART, wave, j);
+            for (int j = 0; j < C::LOADS; ++j) pb.load(lb, ring + q * C::PART + wave * 1024, j);
         }
     }
     wait_vmcnt<(NP - 2) * C::LOADS>();
@@ -614,9 +618,9 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
                 if (i % C::LOAD_STEP == C::LOAD_STEP - 1) {
                     // parts NP and NP + 1 further on: B first where NP is odd
                     const int j = i / C::LOAD_STEP;
-                    uint8_t* dst = ring + (j < C::LOADS ? slot : slot_b) * C::PART;
-                    if ((j < C::LOADS) == (NP % 2 == 0)) PartA::load(la, dst, wave, j % C::LOADS);
-                    else PartB::load(lb, dst, wave, j % C::LOADS);
+                    uint8_t* dst = ring + (j < C::LOADS ? slot : slot_b) * C::PART + wave * 1024;
+                    if ((j < C::LOADS) == (NP % 2 == 0)) pa.load(la, dst, j % C::LOADS);
+                    else pb.load(lb, dst, j % C::LOADS);
                 }
                 mfma<BF16>(acc[i / NB][i % NB], fb[1][i % NB], fa[1][i / NB]);
                 __builtin_amdgcn_sched_barrier(0x6);

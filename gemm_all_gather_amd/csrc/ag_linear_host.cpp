@@ -122,7 +122,7 @@ struct Product {
 ag_status_t choose(Product* p, int cus)
 {
     struct Kind { double step_us, fixed_us; };
-    static const Kind kinds[2] = {{1.55, 9.0}, {0.42, 4.0}};   // kLinearTile256, kLinearTile128
+    static const Kind kinds[2] = {{1.50, 6.0}, {0.52, 4.0}};   // kLinearTile256, kLinearTile128
     constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
     p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
     double best = 0;

@@ -490,8 +490,9 @@ ag_status_t ag_plan_gemm_all_gather_ex(const ag_heap_geometry_t* geom, int W, in
  * rows are not 4-byte aligned are copied to the workspace first (M above 32);
  * rows of less than 2^20 elements apart (AG_ERR_UNSUPPORTED otherwise).
  * Outputs must not overlap inputs or each other (but y and residual, above).
- * Rows and columns between the matrices' rows (ld > row) are never written,
- * and never read beyond the aligned 4 bytes that hold a row's last element.
+ * What lies between a matrix's rows (ld > row) is never written and never has
+ * an effect; nothing is read before a matrix's first element or after the
+ * aligned 4 bytes that hold its last one.
  *
  * workspace  device memory of at least the plan's workspace_bytes, 256-byte
  *            aligned, not shared by calls that may run at once; its contents
