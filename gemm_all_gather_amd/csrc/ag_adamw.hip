@@ -144,9 +144,18 @@ __device__ __forceinline__ AdamwScalars scalars(const AdamwArgs& a)
     return s;
 }
 
+// sqrt to 1 ulp; the instruction takes no subnormal numbers, so small arguments are scaled by 2^96 before it.
+__device__ __forceinline__ float root(float x)
+{
+    const bool small = x < 1e-30f;
+    const float r = __builtin_amdgcn_sqrtf(small ? x * 0x1p96f : x);
+    return small ? r * 0x1p-48f : r;
+}
+
+// The quotient by the reciprocal instruction (1 ulp): its error is 2^-22 of the step, below the parameter's own rounding.
 __device__ __forceinline__ float update(float p, float m, float v, const AdamwScalars& s)
 {
-    return p * s.decay - s.rate * m / (sqrtf(v * s.inv_bias2) + s.eps);
+    return p * s.decay - s.rate * m * __builtin_amdgcn_rcpf(root(v * s.inv_bias2) + s.eps);
 }
 
 // 32 random bits of the state element at place i (counted over all tensors' blocks): multiply and xor-shift
@@ -162,36 +171,48 @@ __device__ __forceinline__ uint32_t random_bits(uint64_t mixed_seed, uint64_t i)
 }
 
 // The code floor(t + u), t = top * r^(1/POWER), of r = value / maximum in [0, 1], u in (0, 1) a multiple of 2^-17.
-// t is found in fp32 (error below 6e-5).  Where t + u lies within 2.5e-4 of a whole number, which side
-// it is on is decided in fp64 by comparing r top^POWER with (k - u)^POWER: the code is that of exact
-// arithmetic on r, so it depends on no instruction's last bit.
+// guess() finds it in fp32: r is within 2^-22 of itself (value, reciprocal and product rounded), the roots within
+// 2^-22 with it, so t + u within 1e-4 (255 (2^-22 + 2^-24) + 2^-16).  Where t + u lies closer than 1.25e-4 to a whole
+// number, `near` is set and decide() says which side it is on in fp64, by comparing r top^POWER with (k - u)^POWER:
+// the code is that of exact arithmetic, so it depends on no instruction's last bit.
 template <int POWER>
-__device__ __forceinline__ int encode(double r, float u)
+__device__ __forceinline__ float guess(float value, float inverse, float u, bool& near)
 {
     constexpr float top = POWER == 2 ? 127.f : 255.f;
-    float t = __builtin_amdgcn_sqrtf(static_cast<float>(r));
+    float t = __builtin_amdgcn_sqrtf(value * inverse);
     if (POWER == 4) t = __builtin_amdgcn_sqrtf(t);
     const float x = t * top + u;
-    float k = floorf(x);
-    const float near = rintf(x);
-    if (fabsf(x - near) < 2.5e-4f) {
-        const double b = static_cast<double>(near) - static_cast<double>(u);
-        const double b2 = b * b;
-        const bool reached = b <= 0.0 || (POWER == 2 ? r * (127.0 * 127.0) >= b2 : r * (255.0 * 255.0 * 255.0 * 255.0) >= b2 * b2);
-        k = reached ? near : near - 1.f;
-    }
-    return static_cast<int>(fminf(k, top));
+    near = fabsf(x - rintf(x)) < 1.25e-4f;
+    return fminf(floorf(x), top);
+}
+template <int POWER>
+__device__ __forceinline__ float decide(double value, float maximum, float u)
+{
+    constexpr float top = POWER == 2 ? 127.f : 255.f;
+    const double r = value / static_cast<double>(maximum);
+    float t = __builtin_amdgcn_sqrtf(static_cast<float>(r));
+    if (POWER == 4) t = __builtin_amdgcn_sqrtf(t);
+    const float x = t * top + u, k = rintf(x);
+    if (!(fabsf(x - k) < 1.25e-4f)) return fminf(floorf(x), top);
+    const double b = static_cast<double>(k) - static_cast<double>(u), b2 = b * b;
+    const bool reached = b <= 0.0 || (POWER == 2 ? r * (127.0 * 127.0) >= b2 : r * (255.0 * 255.0 * 255.0 * 255.0) >= b2 * b2);
+    return fminf(reached ? k : k - 1.f, top);
 }
 
 // Largest of the 32 lanes of a block.  Bit patterns of non-negative floats compare as integers, and a NaN's is above all.
+template <int CTRL> __device__ __forceinline__ uint32_t max_dpp(uint32_t v)
+{
+    const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true));
+    return v > o ? v : o;
+}
 __device__ __forceinline__ uint32_t block_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d, 64));
-        v = v > o ? v : o;
-    }
-    return v;
+    v = max_dpp<0xB1>(v);       // quad_perm 1 0 3 2
+    v = max_dpp<0x4E>(v);       // quad_perm 2 3 0 1
+    v = max_dpp<0x141>(v);      // row_half_mirror
+    v = max_dpp<0x140>(v);      // row_mirror
+    const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));   // rows 0 and 1, 2 and 3
+    return t.x > t.y ? t.x : t.y;
 }
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -246,46 +267,74 @@ __global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
             const double ms = block_live ? t.exp_avg_scale[block] * kCodeM : 0.0;
             const double vs = block_live ? t.exp_avg_sq_scale[block] * kCodeV : 0.0;
             double m[8], v[8];
+            float ma[8], vf[8];
             uint32_t mmax = 0, vmax = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int cm = static_cast<int8_t>(mc >> (8 * e));
-                const uint32_t cv = static_cast<uint32_t>(vc >> (8 * e)) & 0xffu;
-                m[e] = blend(a.beta1, static_cast<double>(cm * abs(cm)) * ms, a.one_minus_beta1 * g[e]);
-                v[e] = blend(a.beta2, static_cast<double>(cv * cv * cv * cv) * vs, a.one_minus_beta2 * g[e] * g[e]);
-                const uint32_t mb = __builtin_bit_cast(uint32_t, static_cast<float>(m[e])) & 0x7fffffffu;
-                const uint32_t vb = __builtin_bit_cast(uint32_t, static_cast<float>(v[e])) & 0x7fffffffu;
+                // c |c| and c^2 are exact in fp32, c^4 in fp64
+                const float cm = static_cast<float>(static_cast<int8_t>(mc >> (8 * e)));
+                const float cv = static_cast<float>(static_cast<uint8_t>(vc >> (8 * e)));
+                const double cv2 = static_cast<double>(cv * cv);
+                m[e] = blend(a.beta1, static_cast<double>(cm * fabsf(cm)) * ms, a.one_minus_beta1 * g[e]);
+                v[e] = blend(a.beta2, cv2 * cv2 * vs, a.one_minus_beta2 * g[e] * g[e]);
+                const float mf = static_cast<float>(m[e]);
+                ma[e] = fabsf(mf);
+                vf[e] = static_cast<float>(v[e]);
+                const uint32_t mb = __float_as_uint(ma[e]), vb = __float_as_uint(vf[e]) & 0x7fffffffu;
                 mmax = mmax > mb ? mmax : mb;
                 vmax = vmax > vb ? vmax : vb;
-                p[e] = update(p[e], static_cast<float>(m[e]), static_cast<float>(v[e]), s);
+                p[e] = update(p[e], mf, vf[e], s);
             }
             mmax = block_max(mmax);
             vmax = block_max(vmax);
             // a block that holds an infinity or a NaN reads back as NaN: all codes 0, the maximum NaN
             const bool mfine = mmax < kInfBits, vfine = vmax < kInfBits;
-            const float mS = mfine ? __builtin_bit_cast(float, mmax) : __builtin_nanf("");
-            const float vS = vfine ? __builtin_bit_cast(float, vmax) : __builtin_nanf("");
-            const double mi = mfine && mmax != 0 ? 1.0 / static_cast<double>(mS) : 0.0;
-            const double vi = vfine && vmax != 0 ? 1.0 / static_cast<double>(vS) : 0.0;
-            uint64_t mo = 0, vo = 0;
+            const float mS = mfine ? __uint_as_float(mmax) : __builtin_nanf("");
+            const float vS = vfine ? __uint_as_float(vmax) : __builtin_nanf("");
+            // a maximum so small that its reciprocal would overflow leaves the codes to decide()
+            const float mi = mfine && mS > 1e-30f ? __builtin_amdgcn_rcpf(mS) : 0.f;
+            const float vi = vfine && vS > 1e-30f ? __builtin_amdgcn_rcpf(vS) : 0.f;
+            const bool mtiny = mfine && mmax != 0 && mi == 0.f, vtiny = vfine && vmax != 0 && vi == 0.f;
+            float km[8], kv[8], um[8], uv[8];
+            uint32_t open = 0;      // codes to decide: bits 0-7 first moments, 8-15 second
             const uint64_t place = (static_cast<uint64_t>(t.first_block) * AG_ADAMW_BLOCK) + static_cast<uint64_t>(at);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float um = 0.5f, uv = 0.5f;
+                um[e] = uv[e] = 0.5f;
                 if (a.stochastic) {   // uniform
                     const uint32_t bits = random_bits(s.seed, place + e);
-                    um = static_cast<float>(2 * (bits & 0xffffu) + 1) * (1.f / 131072.f);
-                    uv = static_cast<float>(2 * (bits >> 16) + 1) * (1.f / 131072.f);
+                    um[e] = static_cast<float>(2 * (bits & 0xffffu) + 1) * (1.f / 131072.f);
+                    uv[e] = static_cast<float>(2 * (bits >> 16) + 1) * (1.f / 131072.f);
                 }
-                int km = mfine ? encode<2>(fabs(m[e]) * mi, um) : 0;
-                int kv = vfine ? encode<4>(v[e] * vi, uv) : 0;
-                if (vfine && v[e] > 0.0 && kv < 1) kv = 1;
-                if (m[e] < 0.0) km = -km;
-                mo |= static_cast<uint64_t>(static_cast<uint8_t>(km)) << (8 * e);
-                vo |= static_cast<uint64_t>(static_cast<uint8_t>(kv)) << (8 * e);
+                bool near;
+                km[e] = guess<2>(ma[e], mi, um[e], near);
+                open |= near ? 1u << e : 0u;
+                kv[e] = guess<4>(vf[e], vi, uv[e], near);
+                open |= near ? 256u << e : 0u;
             }
-            store_codes(t.exp_avg, at, mo, n);
-            store_codes(t.exp_avg_sq, at, vo, n);
+            if (mtiny) open |= 0xffu;
+            if (vtiny) open |= 0xff00u;
+            if (!mfine || mmax == 0) open &= ~0xffu;
+            if (!vfine || vmax == 0) open &= ~0xff00u;
+            if (__any(open != 0)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (open & (1u << e)) km[e] = decide<2>(fabs(m[e]), mS, um[e]);
+                    if (open & (256u << e)) kv[e] = decide<4>(v[e], vS, uv[e]);
+                }
+            }
+            uint32_t mo[2] = {0, 0}, vo[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                int cm = mfine ? static_cast<int>(km[e]) : 0;
+                int cv = vfine ? static_cast<int>(kv[e]) : 0;
+                if (vfine && v[e] > 0.0 && cv < 1) cv = 1;
+                if (m[e] < 0.0) cm = -cm;
+                mo[e / 4] |= (static_cast<uint32_t>(cm) & 0xffu) << (8 * (e % 4));
+                vo[e / 4] |= static_cast<uint32_t>(cv) << (8 * (e % 4));
+            }
+            store_codes(t.exp_avg, at, mo[0] | static_cast<uint64_t>(mo[1]) << 32, n);
+            store_codes(t.exp_avg_sq, at, vo[0] | static_cast<uint64_t>(vo[1]) << 32, n);
             if (block_live && (threadIdx.x & 31) == 0) {
                 t.exp_avg_scale[block] = mS;
                 t.exp_avg_sq_scale[block] = vS;

@@ -58,16 +58,15 @@ hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst
                               int64_t cols, hipStream_t stream);
 
 // dz = dy * act'(z), rounded, and the column sums of the unrounded dz over row blocks.
-constexpr int kLinearSlopeRows = 64;   // rows of one partial column sum
 struct LinearSlopeArgs {
     const uint16_t* dy;
     const uint16_t* z;          // null when act is none
     uint16_t* dz;               // null: not stored
-    float* sums;                // ceil(M / kLinearSlopeRows) rows of N, or null
+    float* sums;                // ceil(M / rows) rows of N, or null
     int64_t lddy, ldz, lddz;
     int64_t M, N;
     int32_t act;
-    int32_t reserved;
+    int32_t rows;               // of one workgroup and partial column sum
 };
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
 // db(n) (+)= sum over parts of sums(part, n).

@@ -159,15 +159,15 @@ __device__ __forceinline__ void apply_slope(float (&v)[8], const float (&z)[8], 
     }
 }
 
-// n <= 8 consecutive gradient elements: earlier gradient, rounding, store.
+// n <= 8 consecutive gradient elements to p: earlier gradient, rounding, store.
 template <bool BF16>
-__device__ __forceinline__ void finish_gradient(float (&v)[8], const LinearEpilogue& ep, int64_t row, int64_t col, int n)
+__device__ __forceinline__ void put_gradient(float (&v)[8], void* at, int f32, int accumulate, int n)
 {
-    if (ep.out_f32) {
-        float* p = static_cast<float*>(ep.out) + row * ep.ldo + col;
+    if (f32) {
+        float* p = static_cast<float*>(at);
         if (n >= 8) {
             f32x4u lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-            if (ep.accumulate) {
+            if (accumulate) {
                 lo += *reinterpret_cast<const f32x4u*>(p);
                 hi += *reinterpret_cast<const f32x4u*>(p + 4);
             }
@@ -176,11 +176,11 @@ __device__ __forceinline__ void finish_gradient(float (&v)[8], const LinearEpilo
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < n) p[e] = ep.accumulate ? p[e] + v[e] : v[e];
+                if (e < n) p[e] = accumulate ? p[e] + v[e] : v[e];
         }
     } else {
-        uint16_t* p = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col;
-        if (ep.accumulate) {
+        uint16_t* p = static_cast<uint16_t*>(at);
+        if (accumulate) {
             float o[8];
             load_f32<BF16>(o, p, n);
 #pragma unroll
@@ -188,6 +188,11 @@ __device__ __forceinline__ void finish_gradient(float (&v)[8], const LinearEpilo
         }
         store_16<BF16>(p, v, n);
     }
+}
+template <bool BF16>
+__device__ __forceinline__ void finish_gradient(float (&v)[8], const LinearEpilogue& ep, int64_t row, int64_t col, int n)
+{
+    put_gradient<BF16>(v, static_cast<char*>(ep.out) + (row * ep.ldo + col) * (ep.out_f32 ? 4 : 2), ep.out_f32, ep.accumulate, n);
 }
 
 // n <= 8 consecutive elements of a layer's output: bias, pre-activation, activation, residual, rounding, store.
@@ -461,6 +466,18 @@ __device__ __forceinline__ void widen(float (&v)[8], const f32x4& x, const f32x4
     }
 }
 
+// A lane's place in a matrix, going down 16 rows at a time.
+struct Walk {
+    char* p;
+    int64_t rows16;
+    __device__ __forceinline__ Walk(const void* m, int64_t row, int64_t col, int64_t ld, int size)
+        : p(static_cast<char*>(const_cast<void*>(m)) + (row * ld + col) * size), rows16(16 * ld * size)
+    {
+    }
+    template <class T> __device__ __forceinline__ T* at(int elements16) const { return reinterpret_cast<T*>(p + 2 * elements16); }
+    __device__ __forceinline__ void down() { p += rows16; }
+};
+
 template <bool BF16, int FORM, int ACT, class C>
 __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
 {
@@ -637,42 +654,84 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         // 16-byte accesses (64 bytes of a row together) and the one rounding at the very end.
         int64_t i0, j0;
         place_tile(a, w.tile, C::T, &i0, &j0);
-        const bool whole = w.count == a.stages;
         int own = lane;
         asm volatile("" : "+v"(own));   // opaque: the lane's addresses are made here, not kept across the loop
         const int tile_row = wm * C::WT + (own & 15), tile_col = wn * C::WT + (own >> 4) * 8;
-        float bias[NB / 2][8];
+        const int64_t row0 = i0 + tile_row, col0 = j0 + tile_col;
+        if (w.count != a.stages) {
+            float* d = a.partial + (static_cast<int64_t>(spread(blockIdx.x, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
+                                       (C::T * C::T) + tile_row * C::T + tile_col;
 #pragma unroll
-        for (int b = 0; b < NB / 2; ++b) {
+            for (int bm = 0; bm < NB; ++bm, d += 16 * C::T)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) bias[b][e] = 0.f;
-            const int64_t left = a.J - (j0 + tile_col + 32 * b);
-            if (FORM == kFormNT && whole && a.epi.bias && left > 0)
-                load_f32<BF16>(bias[b], a.epi.bias + j0 + tile_col + 32 * b, static_cast<int>(min(int64_t{8}, left)));
-        }
-        float* partial = a.partial + (static_cast<int64_t>(spread(blockIdx.x, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
-                                         (C::T * C::T);
-#pragma unroll
-        for (int bm = 0; bm < NB; ++bm) {
-            const int64_t row = i0 + tile_row + 16 * bm;
-#pragma unroll
-            for (int b = 0; b < NB / 2; ++b) {
-                float x[8];
-                widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
-                const int64_t col = j0 + tile_col + 32 * b;
-                const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
-                if (row < a.I && n > 0) {
-                    if (!whole) {
-                        f32x4* d = reinterpret_cast<f32x4*>(partial + (tile_row + 16 * bm) * C::T + tile_col + 32 * b);
-                        d[0] = f32x4{x[0], x[1], x[2], x[3]};
-                        d[1] = f32x4{x[4], x[5], x[6], x[7]};
-                    } else if constexpr (FORM == kFormNT) {
-                        finish_layer<BF16>(x, bias[b], a.epi, ACT, row, col, n);
-                    } else {
-                        finish_gradient<BF16>(x, a.epi, row, col, n);
-                    }
+                for (int b = 0; b < NB / 2; ++b) {
+                    float x[8];
+                    widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                    *reinterpret_cast<f32x4*>(d + 32 * b) = f32x4{x[0], x[1], x[2], x[3]};
+                    *reinterpret_cast<f32x4*>(d + 32 * b + 4) = f32x4{x[4], x[5], x[6], x[7]};
+                    __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
                 }
-                __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
+        } else if (i0 + C::T <= a.I && j0 + C::T <= a.J) {
+            // the whole tile inside: no bounds, and every address one step from the one before
+            Walk out(a.epi.out, row0, col0, a.epi.ldo, a.epi.out_f32 ? 4 : 2);
+            Walk z(a.epi.z, row0, col0, a.epi.ldz, 2), res(a.epi.residual, row0, col0, a.epi.ldr, 2);
+            float bias[NB / 2][8] = {};
+            if (FORM == kFormNT && a.epi.bias) {
+#pragma unroll
+                for (int b = 0; b < NB / 2; ++b) load_f32<BF16>(bias[b], a.epi.bias + col0 + 32 * b, 8);
+            }
+#pragma unroll
+            for (int bm = 0; bm < NB; ++bm) {
+#pragma unroll
+                for (int b = 0; b < NB / 2; ++b) {
+                    float x[8];
+                    widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                    if constexpr (FORM == kFormNT) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] += bias[b][e];
+                        if (a.epi.z) store_16<BF16>(z.at<uint16_t>(32 * b), x, 8);
+                        activate(x, ACT);
+                        if (a.epi.residual) {
+                            float r[8];
+                            load_f32<BF16>(r, res.at<uint16_t>(32 * b), 8);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] += r[e];
+                        }
+                        store_16<BF16>(out.at<uint16_t>(32 * b), x, 8);
+                    } else if (FORM == kFormTN && (a.epi.out_f32 || a.epi.accumulate)) {
+                        put_gradient<BF16>(x, out.at<void>(a.epi.out_f32 ? 64 * b : 32 * b), a.epi.out_f32, a.epi.accumulate, 8);
+                    } else {
+                        store_16<BF16>(out.at<uint16_t>(32 * b), x, 8);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                out.down();
+                if (FORM == kFormNT) {
+                    z.down();
+                    res.down();
+                }
+            }
+        } else {
+#pragma unroll
+            for (int bm = 0; bm < NB; ++bm) {
+                const int64_t row = row0 + 16 * bm;
+#pragma unroll
+                for (int b = 0; b < NB / 2; ++b) {
+                    float x[8];
+                    widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                    const int64_t col = col0 + 32 * b;
+                    const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
+                    if (row < a.I && n > 0) {
+                        if constexpr (FORM == kFormNT) {
+                            float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                            if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
+                            finish_layer<BF16>(x, bias, a.epi, ACT, row, col, n);
+                        } else {
+                            finish_gradient<BF16>(x, a.epi, row, col, n);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         w = next;
@@ -861,7 +920,7 @@ __global__ __launch_bounds__(256) void ag_linear_pack_kernel(const uint16_t* src
 
 // ---------------------------------------------------------------- activation's gradient, bias gradient
 
-// 32 column groups of 8 x 8 row lanes; a workgroup takes 256 columns of kLinearSlopeRows rows.
+// 32 column groups of 8 x 8 row lanes; a workgroup takes 256 columns of a.rows rows.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
 {
@@ -870,12 +929,12 @@ __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
     const uint32_t col_blocks = static_cast<uint32_t>((a.N + 255) / 256);
     const int64_t bx = blockIdx.x % col_blocks, by = blockIdx.x / col_blocks;
     const int64_t col = (bx * 32 + c) * 8;
-    const int64_t row0 = by * kLinearSlopeRows;
+    const int64_t row0 = by * a.rows;
     const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.N - col)));
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
 #pragma unroll 4
-        for (int i = rl; i < kLinearSlopeRows; i += 8) {
+        for (int i = rl; i < a.rows; i += 8) {
             const int64_t row = row0 + i;
             if (row >= a.M) break;
             float v[8];
@@ -911,8 +970,10 @@ __global__ __launch_bounds__(256) void ag_linear_bias_grad_kernel(const float* s
     const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
     float s = 0.f;
-    if (col < N)
+    if (col < N) {
+#pragma unroll 8
         for (int64_t q = rl; q < parts; q += 8) s += sums[q * N + col];
+    }
     part[rl][c] = s;
     __syncthreads();
     if (rl == 0 && col < N) {
@@ -994,7 +1055,7 @@ hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream)
 {
     dim3 grid;
-    if (!grid_of((a.N + 255) / 256 * ((a.M + kLinearSlopeRows - 1) / kLinearSlopeRows), 1, &grid)) return hipErrorInvalidValue;
+    if (a.rows < 1 || !grid_of((a.N + 255) / 256 * ((a.M + a.rows - 1) / a.rows), 1, &grid)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(bf16 ? ag_linear_slope_kernel<true> : ag_linear_slope_kernel<false>, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }

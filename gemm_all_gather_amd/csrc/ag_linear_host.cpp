@@ -121,8 +121,9 @@ struct Product {
 // tiles' traffic and a second launch.
 ag_status_t choose(Product* p, int cus)
 {
-    struct Kind { double step_us, fixed_us; };
-    static const Kind kinds[2] = {{1.50, 6.0}, {0.52, 4.0}};   // kLinearTile256, kLinearTile128
+    // us of a 64-wide step by form (NT, NN, TN), and of a tile's start and epilogue; kLinearTile256, kLinearTile128
+    struct Kind { double step_us[3], fixed_us; };
+    static const Kind kinds[2] = {{{1.50, 1.53, 1.57}, 6.0}, {{0.51, 0.58, 0.71}, 4.0}};
     constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
     p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
     double best = 0;
@@ -133,7 +134,8 @@ ag_status_t choose(Product* p, int cus)
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
         if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffff00) continue;
         const int64_t tiles = ti * tj, rounds = tiles / cus;
-        const double tile_us = p->stages * kinds[tile].step_us + kinds[tile].fixed_us;
+        const double step_us = kinds[tile].step_us[p->form];
+        const double tile_us = p->stages * step_us + kinds[tile].fixed_us;
         auto consider = [&](int64_t full, int64_t groups, int64_t run, bool join, double us) {
             if (found && us >= best) return;
             found = true;
@@ -159,7 +161,7 @@ ag_status_t choose(Product* p, int cus)
                 if (run >= p->stages && keep == rounds) continue;       // nothing is cut to gain by
                 const double pieces = static_cast<double>(std::min<int64_t>(2 * groups, tail + groups));
                 const double bytes = pieces * tm * tn * 4;
-                const double us = keep * tile_us + run * kinds[tile].step_us + 2 * kinds[tile].fixed_us + kJoinUs +
+                const double us = keep * tile_us + run * step_us + 2 * kinds[tile].fixed_us + kJoinUs +
                                   2 * bytes / kBytesPerUs;
                 consider(keep * cus, groups, run, true, us);
             }
@@ -321,7 +323,7 @@ struct Backward {
     Operand ox, ow, odz;
     bool slope = false, store_dz = false;
     uint64_t dz_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
-    int64_t parts = 0, lddz = 0;
+    int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
 };
 
@@ -363,12 +365,14 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         b->slope = b->store_dz || want_db;
     }
     b->lddz = (N + 7) / 8 * 8;
+    // about 1024 workgroups of 256 columns: enough for every CU, and few partial sums of a long column
+    b->rows = std::max<int64_t>(8, std::min<int64_t>(256, (M * ((N + 255) / 256) / 1024 + 7) / 8 * 8));
     if (b->store_dz) {
         b->dz_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
     }
     if (want_db) {
-        b->parts = (M + ag::kLinearSlopeRows - 1) / ag::kLinearSlopeRows;
+        b->parts = (M + b->rows - 1) / b->rows;
         b->sums_offset = used;
         used += up256(static_cast<uint64_t>(b->parts) * N * 4);
     }
@@ -529,6 +533,7 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         a.M = args->M;
         a.N = args->N;
         a.act = args->act;
+        a.rows = static_cast<int32_t>(b.rows);
         const hipError_t e = ag::launch_linear_slope(a, bf16, stream);
         if (e != hipSuccess) return fail_hip(e, "linear slope");
         if (b.store_dz) {
