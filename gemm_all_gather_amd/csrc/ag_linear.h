@@ -70,8 +70,18 @@ struct LinearSlopeArgs {
 };
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
 // db(n) (+)= sum over parts of sums(part, n).
-hipError_t launch_linear_bias_grad(const float* sums, int64_t parts, int64_t N, void* db, int db_kind /* 0 f16, 1 bf16, 2 f32 */,
-                                   int accumulate, hipStream_t stream);
+struct LinearBiasGradArgs {
+    const float* sums;
+    void* db;
+    int64_t parts, N;
+    int32_t kind;               // of db: 0 f16, 1 bf16, 2 f32
+    int32_t accumulate;
+};
+hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream);
+
+// dx, dw and (db.db set) db in one launch of 128 x 128 tiles, without tails.
+hipError_t launch_linear_grads(const LinearGemmArgs& dx, const LinearGemmArgs& dw, int dx_programs, int dw_programs,
+                               const LinearBiasGradArgs& db, int bf16, hipStream_t stream);
 
 // Tile shape and threads of a tile configuration (host-only).
 void linear_tile_shape(int tile, int* tm, int* tn, int* threads);

@@ -425,9 +425,9 @@ __device__ __forceinline__ int spread(int p, int n)
     return (p & 7) * (n >> 3) + min(p & 7, n & 7) + (p >> 3);
 }
 
-__device__ __forceinline__ Piece piece_of(const LinearGemmArgs& a, int q)
+// p of n: this workgroup among the product's.
+__device__ __forceinline__ Piece piece_of(const LinearGemmArgs& a, int p, int n, int q)
 {
-    const int p = blockIdx.x, n = gridDim.x;
     const int rounds = a.full_tiles / n + (p < a.full_tiles % n ? 1 : 0);
     if (q < rounds) return Piece{q * n + spread(p, min(n, a.full_tiles - q * n)), 0, a.stages};
     if (p >= a.tail_groups) return Piece{0, 0, 0};
@@ -479,15 +479,13 @@ struct Walk {
 };
 
 template <bool BF16, int FORM, int ACT, class C>
-__global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
+__device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, int programs, uint8_t* ring)
 {
     constexpr bool TA = FORM == kFormTN, TB = FORM != kFormNT;
     constexpr int NB = C::NB, NP = C::NP;
     using V = typename Mfma<BF16>::V;
     using PartA = Part<C, TA>;
     using PartB = Part<C, TB>;
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[NP * C::PART];
-
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -506,13 +504,13 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
     // The ring takes the parts of all the workgroup's pieces in one stream, so that the next tile's first stages
     // are on their way during a tile's last ones and its epilogue.  A's and B's loads each walk the pieces.
     auto start_a = [&](int q) {
-        const Piece w = piece_of(a, q);
+        const Piece w = piece_of(a, program, programs, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::T, &i0, &j0);
         return PartA::start(a.A, i0, a.I, a.R, lda2, w.first, w.count);
     };
     auto start_b = [&](int q) {
-        const Piece w = piece_of(a, q);
+        const Piece w = piece_of(a, program, programs, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::T, &i0, &j0);
         return PartB::start(a.B, j0, a.J, a.R, ldb2, w.first, w.count);
@@ -577,7 +575,7 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
     wait_vmcnt<(NP - 2) * C::LOADS>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    Piece w = piece_of(a, 0);
+    Piece w = piece_of(a, program, programs, 0);
     if (ragged && w.count == 1 && w.first + 1 == a.stages) clear_tail(0, 1);
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) read(0, lds, lds + C::PART, 0, i);
@@ -587,7 +585,7 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
 
     int slot = 0;               // of the stage's A part; its B part lies in the next one
     for (int q = 0; w.count > 0;) {
-        const Piece next = piece_of(a, q + 1);
+        const Piece next = piece_of(a, program, programs, q + 1);
         // whether the stage after the piece's last is a tile's last one too
         const bool next_short = next.count > 0 && next.first + 1 == a.stages;
         const bool ends = w.first + w.count == a.stages;
@@ -659,7 +657,7 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
         const int tile_row = wm * C::WT + (own & 15), tile_col = wn * C::WT + (own >> 4) * 8;
         const int64_t row0 = i0 + tile_row, col0 = j0 + tile_col;
         if (w.count != a.stages) {
-            float* d = a.partial + (static_cast<int64_t>(spread(blockIdx.x, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
+            float* d = a.partial + (static_cast<int64_t>(spread(program, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
                                        (C::T * C::T) + tile_row * C::T + tile_col;
 #pragma unroll
             for (int bm = 0; bm < NB; ++bm, d += 16 * C::T)
@@ -740,6 +738,53 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
     wait_vmcnt<0>();   // loads past the last stage write LDS: they end with the workgroup
 }
 
+template <bool BF16, int FORM, int ACT, class C>
+__global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::NP * C::PART];
+    gemm_body<BF16, FORM, ACT, C>(a, blockIdx.x, gridDim.x, ring);
+}
+
+// Sums the partial column sums of 32 columns: 8 row lanes, then a fixed order through LDS (8 x 33 floats).
+__device__ __forceinline__ void bias_grad_body(const LinearBiasGradArgs& a, int block, float* part)
+{
+    const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int64_t col = static_cast<int64_t>(block) * 32 + c;
+    float s = 0.f;
+    if (col < a.N) {
+#pragma unroll 8
+        for (int64_t q = rl; q < a.parts; q += 8) s += a.sums[q * a.N + col];
+    }
+    part[rl * 33 + c] = s;
+    __syncthreads();
+    if (rl == 0 && col < a.N) {
+        s = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s += part[r * 33 + c];
+        if (a.kind == 2) {
+            float* p = static_cast<float*>(a.db) + col;
+            *p = a.accumulate ? *p + s : s;
+        } else {
+            uint16_t* p = static_cast<uint16_t*>(a.db) + col;
+            if (a.accumulate) s += a.kind == 1 ? to_f32<true>(*p) : to_f32<false>(*p);
+            *p = a.kind == 1 ? from_f32<true>(s) : from_f32<false>(s);
+        }
+    }
+}
+
+// dx, dw and the bias gradient's sum in one launch, for layers whose tiles together leave CUs free: workgroups
+// below dx_programs take dx, the next dw_programs dw, the others 32 columns each of db.
+template <bool BF16, class C>
+__global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_kernel(LinearGemmArgs dx, LinearGemmArgs dw, int dx_programs,
+                                                                   int dw_programs, LinearBiasGradArgs db)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::NP * C::PART];
+    const int p = blockIdx.x;
+    if (p < dx_programs) gemm_body<BF16, kFormNN, AG_ACT_NONE, C>(dx, p, dx_programs, ring);
+    else if (p < dx_programs + dw_programs) gemm_body<BF16, kFormTN, AG_ACT_NONE, C>(dw, p - dx_programs, dw_programs, ring);
+    else bias_grad_body(db, p - dx_programs - dw_programs, reinterpret_cast<float*>(ring));
+}
+
 // 256 x 256: a wave's 128 x 128 sub-tile keeps LDS reads (128 KiB a stage) and the slots' refill (64 KiB) below
 // the matrix pipe's 2048 cycles a stage at 128 bytes per cycle; its accumulators take 256 registers.
 // 128 x 128: for products with few tiles.
@@ -784,6 +829,7 @@ __global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, i
     col += tile_col;
     if (row >= a.I || col >= a.J) return;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int q = g0; q <= g1; ++q) {
         const bool starts = q * a.tail_run <= begin;      // the piece that holds the first step
         const f32x4* src = reinterpret_cast<const f32x4*>(a.partial + (static_cast<int64_t>(q) * 2 + (starts ? 1 : 0)) * (tile * tile) +
@@ -810,7 +856,10 @@ __global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, i
 // y for up to 16 MB rows of x: the weights are streamed once, straight into matrix-instruction fragments,
 // 16 rows of w per workgroup.  The workgroup's waves share the reduction, 128 wide at a time, and add up
 // through LDS in a fixed order.  D rows are rows of w, D columns rows of x.
-constexpr int kStreamWaves = 8;
+#ifndef AG_LINEAR_STREAM_WAVES
+#define AG_LINEAR_STREAM_WAVES 16
+#endif
+constexpr int kStreamWaves = AG_LINEAR_STREAM_WAVES;
 
 template <bool BF16>
 __device__ __forceinline__ typename Mfma<BF16>::V stream_load(const uint16_t* p, int64_t left)
@@ -848,24 +897,41 @@ __global__ __launch_bounds__(64 * kStreamWaves) void ag_linear_stream_kernel(Lin
     for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
     const V zero = __builtin_bit_cast(V, u32x4{0u, 0u, 0u, 0u});
 
-    int64_t k = wave * 128;
-    for (; k + 128 <= a.K; k += kStreamWaves * 128) {
-        V fw[4], fx[MB][4];
+    struct Block {
+        V w[4], x[MB][4];
+    };
+    auto load = [&](Block& t, int64_t k) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) fw[u] = __builtin_bit_cast(V, load8(w + k + u * 32));
+        for (int u = 0; u < 4; ++u) t.w[u] = __builtin_bit_cast(V, load8(w + k + u * 32));
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                fx[b][u] = zero;
-                if (live[b]) fx[b][u] = __builtin_bit_cast(V, load8(x[b] + k + u * 32));
+                t.x[b][u] = zero;
+                if (live[b]) t.x[b][u] = __builtin_bit_cast(V, load8(x[b] + k + u * 32));
             }
+    };
+    auto multiply = [&](const Block& t) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int b = 0; b < MB; ++b) acc[b] = Mfma<BF16>::run(fw[u], fx[b][u], acc[b]);
+            for (int b = 0; b < MB; ++b) acc[b] = Mfma<BF16>::run(t.w[u], t.x[b][u], acc[b]);
+    };
+    // two 128-wide blocks on their way per wave while a third is multiplied
+    constexpr int64_t NEXT = kStreamWaves * 128;
+    const int64_t whole = a.K / 128 * 128;
+    int64_t k = wave * 128;
+    Block even, odd;
+    if (k < whole) load(even, k);
+    for (; k < whole; k += 2 * NEXT) {
+        const bool more = k + NEXT < whole;
+        if (more) load(odd, k + NEXT);
+        multiply(even);
+        if (k + 2 * NEXT < whole) load(even, k + 2 * NEXT);
+        if (more) multiply(odd);
     }
-    if (k < a.K) {   // the last, shorter 128: one wave's
+    if (whole < a.K && wave == (whole / 128) % kStreamWaves) {   // the last, shorter block
+        k = whole;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t left = a.K - k - u * 32 - k_lane;
@@ -963,32 +1029,10 @@ __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
     }
 }
 
-__global__ __launch_bounds__(256) void ag_linear_bias_grad_kernel(const float* sums, int64_t parts, int64_t N, void* db,
-                                                                  int kind, int accumulate)
+__global__ __launch_bounds__(256) void ag_linear_bias_grad_kernel(LinearBiasGradArgs a)
 {
-    __shared__ float part[8][33];
-    const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
-    float s = 0.f;
-    if (col < N) {
-#pragma unroll 8
-        for (int64_t q = rl; q < parts; q += 8) s += sums[q * N + col];
-    }
-    part[rl][c] = s;
-    __syncthreads();
-    if (rl == 0 && col < N) {
-        s = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) s += part[r][c];
-        if (kind == 2) {
-            float* p = static_cast<float*>(db) + col;
-            *p = accumulate ? *p + s : s;
-        } else {
-            uint16_t* p = static_cast<uint16_t*>(db) + col;
-            if (accumulate) s += kind == 1 ? to_f32<true>(*p) : to_f32<false>(*p);
-            *p = kind == 1 ? from_f32<true>(s) : from_f32<false>(s);
-        }
-    }
+    __shared__ float part[8 * 33];
+    bias_grad_body(a, blockIdx.x, part);
 }
 
 }  // namespace
@@ -1060,12 +1104,24 @@ hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t s
     return hipGetLastError();
 }
 
-hipError_t launch_linear_bias_grad(const float* sums, int64_t parts, int64_t N, void* db, int db_kind, int accumulate,
-                                   hipStream_t stream)
+hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream)
 {
     dim3 grid;
-    if (!grid_of(N, 32, &grid)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(ag_linear_bias_grad_kernel, grid, dim3(256), 0, stream, sums, parts, N, db, db_kind, accumulate);
+    if (!grid_of(a.N, 32, &grid)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ag_linear_bias_grad_kernel, grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_grads(const LinearGemmArgs& dx, const LinearGemmArgs& dw, int dx_programs, int dw_programs,
+                               const LinearBiasGradArgs& db, int bf16, hipStream_t stream)
+{
+    const int64_t db_programs = db.db ? (db.N + 31) / 32 : 0;
+    const int64_t grid = dx_programs + dw_programs + db_programs;
+    if (dx_programs < 1 || dw_programs < 1 || grid > 0x7fffffff || dx.tail_groups != 0 || dw.tail_groups != 0)
+        return hipErrorInvalidValue;
+    static_assert(Cfg128::NT == 256, "the bias gradient takes 256 threads");
+    hipLaunchKernelGGL((bf16 ? ag_linear_grads_kernel<true, Cfg128> : ag_linear_grads_kernel<false, Cfg128>),
+                       dim3(static_cast<uint32_t>(grid)), dim3(Cfg128::NT), 0, stream, dx, dw, dx_programs, dw_programs, db);
     return hipGetLastError();
 }
 

@@ -111,19 +111,39 @@ struct Product {
     int64_t tiles_i = 0, tiles_j = 0, stages = 0;
     int64_t full_tiles = 0, tail_groups = 0, tail_run = 0, programs = 0;
     bool join = false;           // some tail tile is cut
+    double us = 0;               // estimated
     uint64_t partial_bytes = 0;
     int launches() const { return !on ? 0 : join ? 2 : 1; }
 };
 
+// What a workgroup's 64-wide step measured in long products on all CUs.
+struct Kind {
+    double step_us[3], fixed_us;     // a 64-wide step by form (NT, NN, TN); a launch's start and epilogue
+};
+constexpr Kind kKinds[2] = {{{1.50, 1.53, 1.57}, 6.0}, {{0.51, 0.58, 0.71}, 4.0}};   // kLinearTile256, kLinearTile128
+
+// One round of whole tiles, as few as they are.
+void whole_tiles(Product* p, int tile)
+{
+    int tm, tn, threads;
+    ag::linear_tile_shape(tile, &tm, &tn, &threads);
+    p->tile = tile;
+    p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
+    p->tiles_i = (p->I + tm - 1) / tm;
+    p->tiles_j = (p->J + tn - 1) / tn;
+    p->full_tiles = p->programs = p->tiles_i * p->tiles_j;
+    p->tail_groups = 0;
+    p->tail_run = 1;
+    p->join = false;
+    p->partial_bytes = 0;
+    p->us = p->stages * kKinds[tile].step_us[p->form] + kKinds[tile].fixed_us;
+}
+
 // Tile and cut with the shortest estimated time.  Whole rounds of tiles on all CUs go one to a workgroup; the
-// rest either too (one more round), or its steps are shared out evenly over G workgroups.  A
-// workgroup's 64-wide step costs what it measured in long products on all CUs; a cut adds the partial
-// tiles' traffic and a second launch.
+// rest either too (one more round), or its steps are shared out evenly over G workgroups.  A cut adds the
+// partial tiles' traffic and a second launch.
 ag_status_t choose(Product* p, int cus)
 {
-    // us of a 64-wide step by form (NT, NN, TN), and of a tile's start and epilogue; kLinearTile256, kLinearTile128
-    struct Kind { double step_us[3], fixed_us; };
-    static const Kind kinds[2] = {{{1.50, 1.53, 1.57}, 6.0}, {{0.51, 0.58, 0.71}, 4.0}};
     constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
     p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
     double best = 0;
@@ -134,12 +154,12 @@ ag_status_t choose(Product* p, int cus)
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
         if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffff00) continue;
         const int64_t tiles = ti * tj, rounds = tiles / cus;
-        const double step_us = kinds[tile].step_us[p->form];
-        const double tile_us = p->stages * step_us + kinds[tile].fixed_us;
+        const double step_us = kKinds[tile].step_us[p->form];
+        const double tile_us = p->stages * step_us + kKinds[tile].fixed_us;
         auto consider = [&](int64_t full, int64_t groups, int64_t run, bool join, double us) {
             if (found && us >= best) return;
             found = true;
-            best = us;
+            best = p->us = us;
             p->tile = tile;
             p->tiles_i = ti;
             p->tiles_j = tj;
@@ -161,7 +181,7 @@ ag_status_t choose(Product* p, int cus)
                 if (run >= p->stages && keep == rounds) continue;       // nothing is cut to gain by
                 const double pieces = static_cast<double>(std::min<int64_t>(2 * groups, tail + groups));
                 const double bytes = pieces * tm * tn * 4;
-                const double us = keep * tile_us + run * step_us + 2 * kinds[tile].fixed_us + kJoinUs +
+                const double us = keep * tile_us + run * step_us + 2 * kKinds[tile].fixed_us + kJoinUs +
                                   2 * bytes / kBytesPerUs;
                 consider(keep * cus, groups, run, true, us);
             }
@@ -217,8 +237,8 @@ ag_status_t pack(const Operand& o, void* workspace, hipStream_t stream, const ui
     return AG_OK;
 }
 
-ag_status_t run_product(const Product& p, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
-                        const ag::LinearEpilogue& epi, float* partial, int bf16, hipStream_t stream)
+ag::LinearGemmArgs gemm_args(const Product& p, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
+                             const ag::LinearEpilogue& epi, float* partial)
 {
     ag::LinearGemmArgs a{};
     a.A = A;
@@ -236,6 +256,11 @@ ag_status_t run_product(const Product& p, const uint16_t* A, int64_t lda, const 
     a.tail_run = static_cast<int32_t>(p.tail_run);
     a.partial = partial;
     a.epi = epi;
+    return a;
+}
+
+ag_status_t run_product(const Product& p, const ag::LinearGemmArgs& a, int bf16, hipStream_t stream)
+{
     hipError_t e = ag::launch_linear_gemm(a, bf16, p.form, p.tile, static_cast<int>(p.programs), stream);
     if (e != hipSuccess) return fail_hip(e, "linear product");
     if (p.join) {
@@ -322,6 +347,7 @@ struct Backward {
     Product px, pw;
     Operand ox, ow, odz;
     bool slope = false, store_dz = false;
+    bool together = false;      // dx, dw and db in one launch
     uint64_t dz_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
     int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
@@ -398,10 +424,22 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         b->ox = Operand{b->x.at, b->x.ld, M, K};
         place(&b->ox, &used);
     }
+    // Both products' 128 x 128 tiles on CUs of their own: one launch for what follows dz.
+    if (b->px.on && b->pw.on) {
+        Product x = b->px, w = b->pw;
+        whole_tiles(&x, ag::kLinearTile128);
+        whole_tiles(&w, ag::kLinearTile128);
+        if (x.full_tiles + w.full_tiles <= cus &&
+            std::max(x.us, w.us) < b->px.us + b->pw.us) {
+            b->together = true;
+            b->px = x;
+            b->pw = w;
+        }
+    }
     b->partial_offset = used;
     b->workspace = used + std::max(b->px.partial_bytes, b->pw.partial_bytes);
-    b->launches = (b->slope ? 1 : 0) + (want_db ? 1 : 0) + b->px.launches() + b->pw.launches() + (b->ow.pack ? 1 : 0) +
-                  (b->ox.pack ? 1 : 0);
+    b->launches = (b->slope ? 1 : 0) + (b->together ? 1 : (want_db ? 1 : 0) + b->px.launches() + b->pw.launches()) +
+                  (b->ow.pack ? 1 : 0) + (b->ox.pack ? 1 : 0);
     return AG_OK;
 }
 
@@ -468,7 +506,7 @@ ag_status_t ag_linear(const ag_linear_args_t* args, void* workspace, size_t work
     if ((s = pack(f.ox, workspace, stream, &A, &lda)) != AG_OK) return s;
     if ((s = pack(f.ow, workspace, stream, &B, &ldb)) != AG_OK) return s;
     float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.partial_offset);
-    s = run_product(f.product, A, lda, B, ldb, e, partial, bf16, stream);
+    s = run_product(f.product, gemm_args(f.product, A, lda, B, ldb, e, partial), bf16, stream);
     return s == AG_OK ? ok() : s;
 }
 
@@ -541,11 +579,16 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
             lddz = b.lddz;
         }
     }
+    ag::LinearBiasGradArgs db{};
     if (want_db) {
-        const int kind = args->dw_dtype == AG_F32 ? 2 : bf16;
-        const hipError_t e = ag::launch_linear_bias_grad(sums, b.parts, args->N, args->db, kind, args->accumulate, stream);
-        if (e != hipSuccess) return fail_hip(e, "linear bias gradient");
+        db.sums = sums;
+        db.db = args->db;
+        db.parts = b.parts;
+        db.N = args->N;
+        db.kind = args->dw_dtype == AG_F32 ? 2 : bf16;
+        db.accumulate = args->accumulate;
     }
+    ag::LinearGemmArgs dx{}, dw{};
     if (b.px.on) {
         const uint16_t* W;
         int64_t ldw;
@@ -553,7 +596,7 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         ag::LinearEpilogue e{};
         e.out = args->dx;
         e.ldo = b.dx.ld;
-        if ((s = run_product(b.px, dz, lddz, W, ldw, e, partial, bf16, stream)) != AG_OK) return s;
+        dx = gemm_args(b.px, dz, lddz, W, ldw, e, partial);
     }
     if (b.pw.on) {
         const uint16_t* X;
@@ -564,8 +607,19 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         e.ldo = b.dw.ld;
         e.out_f32 = args->dw_dtype == AG_F32;
         e.accumulate = args->accumulate;
-        if ((s = run_product(b.pw, dz, lddz, X, ldx, e, partial, bf16, stream)) != AG_OK) return s;
+        dw = gemm_args(b.pw, dz, lddz, X, ldx, e, partial);
     }
+    if (b.together) {
+        const hipError_t e = ag::launch_linear_grads(dx, dw, static_cast<int>(b.px.programs), static_cast<int>(b.pw.programs), db,
+                                                     bf16, stream);
+        return e == hipSuccess ? ok() : fail_hip(e, "linear gradients");
+    }
+    if (want_db) {
+        const hipError_t e = ag::launch_linear_bias_grad(db, stream);
+        if (e != hipSuccess) return fail_hip(e, "linear bias gradient");
+    }
+    if (b.px.on && (s = run_product(b.px, dx, bf16, stream)) != AG_OK) return s;
+    if (b.pw.on && (s = run_product(b.pw, dw, bf16, stream)) != AG_OK) return s;
     return ok();
 }
 
