@@ -35,7 +35,7 @@ struct LinearGemmArgs {
     LinearEpilogue epi;
 };
 
-enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1 };
+enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1, kLinearTile256x128 = 2, kLinearTiles = 3 };
 enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
 
 hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, int programs, hipStream_t stream);
@@ -51,7 +51,7 @@ struct LinearStreamArgs {
     int64_t M, N, K;
     LinearEpilogue epi;
 };
-hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, hipStream_t stream);
+hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, int cus, hipStream_t stream);
 
 // Copies rows to aligned rows (ld_dst a multiple of 8).
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,

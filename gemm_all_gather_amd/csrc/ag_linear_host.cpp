@@ -120,7 +120,9 @@ struct Product {
 struct Kind {
     double step_us[3], fixed_us;     // a 64-wide step by form (NT, NN, TN); a launch's start and epilogue
 };
-constexpr Kind kKinds[2] = {{{1.50, 1.53, 1.57}, 6.0}, {{0.51, 0.58, 0.71}, 4.0}};   // kLinearTile256, kLinearTile128
+constexpr Kind kKinds[ag::kLinearTiles] = {{{1.42, 1.46, 1.48}, 6.0},     // 256 x 256
+                                           {{0.53, 0.60, 0.75}, 4.0},     // 128 x 128
+                                           {{1.02, 0.98, 1.00}, 5.0}};    // 256 x 128
 
 // One round of whole tiles, as few as they are.
 void whole_tiles(Product* p, int tile)
@@ -148,7 +150,7 @@ ag_status_t choose(Product* p, int cus)
     p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
     double best = 0;
     bool found = false;
-    for (int tile = 0; tile < 2; ++tile) {
+    for (int tile = 0; tile < ag::kLinearTiles; ++tile) {
         int tm, tn, threads;
         ag::linear_tile_shape(tile, &tm, &tn, &threads);
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
@@ -498,7 +500,7 @@ ag_status_t ag_linear(const ag_linear_args_t* args, void* workspace, size_t work
     if (f.product.stream) {
         ag::LinearStreamArgs a{static_cast<const uint16_t*>(args->x), static_cast<const uint16_t*>(args->w), f.x.ld, f.w.ld,
                                args->M, args->N, args->K, e};
-        const hipError_t err = ag::launch_linear_stream(a, bf16, stream);
+        const hipError_t err = ag::launch_linear_stream(a, bf16, cus, stream);
         return err == hipSuccess ? ok() : fail_hip(err, "linear stream");
     }
     const uint16_t *A, *B;
