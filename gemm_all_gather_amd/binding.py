@@ -97,7 +97,7 @@ class LinearBackwardArgs(ctypes.Structure):
 
 
 class ProductPlan(ctypes.Structure):
-    _fields_ = _fields(ctypes.c_int32, "variant tile_m tile_n tile_k full_tiles n_programs packed reserved")
+    _fields_ = _fields(ctypes.c_int32, "variant tile_m tile_n tile_k full_tiles splits n_programs packed")
 
 
 class LinearPlan(ctypes.Structure):

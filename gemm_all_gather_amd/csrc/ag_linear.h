@@ -29,9 +29,9 @@ struct LinearGemmArgs {
     int32_t tiles_i, tiles_j;
     int32_t stages;             // 64-wide steps of the reduction, at least 1
     int32_t full_tiles;         // tiles that one workgroup computes whole, the first of the order
-    int32_t tail_groups;        // workgroups that share the steps of the other tiles, tail_run steps each
-    int32_t tail_run;
-    float* partial;             // tail: two fp32 tiles per workgroup, for its pieces of tiles
+    int32_t splits;             // parts of the other tiles' reductions, split_stages steps each (the last may be shorter)
+    int32_t split_stages;
+    float* partial;             // fp32 tile (part, tail tile)
     LinearEpilogue epi;
 };
 
@@ -39,7 +39,7 @@ enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1, kLinearTile256x128 = 2
 enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
 
 hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, int programs, hipStream_t stream);
-// Joins the pieces of the tail's cut tiles in order and applies the epilogue.
+// Joins the parts of the cut tiles in order and applies the epilogue.
 hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream);
 
 // Row streaming: out(m, n) for few rows m of x (I = N, J = M <= kLinearStreamRows).

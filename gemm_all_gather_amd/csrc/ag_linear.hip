@@ -414,12 +414,14 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p)
 }
 
 // Work of a product: the first full_tiles tiles, a tile at a time per workgroup, round by round; then the other
-// tiles' 64-wide steps, laid end to end and cut into tail_groups equal runs, one per workgroup.  A
-// run's piece of a tile that is not the whole tile goes to the workgroup's partial tile as fp32: slot 0 for a
-// piece that starts inside a tile (its first), slot 1 for one that starts with it (its last); a second
-// kernel joins the pieces.
+// (tail) tiles' reductions cut into `splits` parts of split_stages 64-wide steps, again a part at a time, all
+// tiles' first parts before all second ones: workgroups that run together share operand rows at the same place
+// of the reduction (runs of equal length laid end to end over the tiles do not, and took twice the time per
+// step: 1024 x 3584 x 8192 over 256 workgroups 129 us, one tile a workgroup 62).  A part's fp32 tile goes to
+// partial tile (part, tail tile); a second kernel joins them.
 struct Piece {
     int tile, first, count;     // 64-wide steps first .. first + count - 1 of the tile; count 0: no more work
+    int unit;                   // of a cut tile: its partial tile
 };
 
 __device__ __forceinline__ int spread(int p, int n)
@@ -429,18 +431,17 @@ __device__ __forceinline__ int spread(int p, int n)
     return (p & 7) * (n >> 3) + min(p & 7, n & 7) + (p >> 3);
 }
 
-// p of n: this workgroup among the product's.
+// The q-th piece of workgroup p of n.
 __device__ __forceinline__ Piece piece_of(const LinearGemmArgs& a, int p, int n, int q)
 {
     const int rounds = a.full_tiles / n + (p < a.full_tiles % n ? 1 : 0);
-    if (q < rounds) return Piece{q * n + spread(p, min(n, a.full_tiles - q * n)), 0, a.stages};
-    if (p >= a.tail_groups) return Piece{0, 0, 0};
-    const int tail_steps = (a.tiles_i * a.tiles_j - a.full_tiles) * a.stages;
-    const int begin = spread(p, a.tail_groups) * a.tail_run, end = min(begin + a.tail_run, tail_steps);
-    const int at = q == rounds ? begin : (begin / a.stages + (q - rounds)) * a.stages;
-    if (at >= end) return Piece{0, 0, 0};
-    const int tile = at / a.stages, first = at - tile * a.stages;
-    return Piece{a.full_tiles + tile, first, min(a.stages - first, end - at)};
+    if (q < rounds) return Piece{q * n + spread(p, min(n, a.full_tiles - q * n)), 0, a.stages, 0};
+    const int tail = a.tiles_i * a.tiles_j - a.full_tiles, units = tail * a.splits;
+    const int at = (q - rounds) * n;
+    if (at + p >= units) return Piece{0, 0, 0, 0};
+    const int unit = at + spread(p, min(n, units - at));
+    const int part = unit / tail, first = part * a.split_stages;
+    return Piece{a.full_tiles + unit - part * tail, first, min(a.split_stages, a.stages - first), unit};
 }
 
 // First row and column of a tile: the order goes 8 tile rows at a time, column by column.
@@ -668,8 +669,7 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
         const int tile_row = wm * C::WM + (own & 15), tile_col = wn * C::WN + (own >> 4) * 8;
         const int64_t row0 = i0 + tile_row, col0 = j0 + tile_col;
         if (w.count != a.stages) {
-            float* d = a.partial + (static_cast<int64_t>(spread(program, a.tail_groups)) * 2 + (w.first == 0 ? 1 : 0)) *
-                                       (C::TM * C::TN) + tile_row * C::TN + tile_col;
+            float* d = a.partial + static_cast<int64_t>(w.unit) * (C::TM * C::TN) + tile_row * C::TN + tile_col;
 #pragma unroll
             for (int bm = 0; bm < BM; ++bm, d += 16 * C::TN)
 #pragma unroll
@@ -824,15 +824,12 @@ template <bool BF16, class C> LinearFn pick_form(int form, int act)
 
 // ---------------------------------------------------------------- join of cut tiles
 
-// Adds the pieces of a tail tile in the reduction's order, 8 consecutive columns per thread, then the epilogue.
+// Adds the parts of a tail tile in order, 8 consecutive columns per thread, then the epilogue.
 template <bool BF16, bool LAYER>
 __global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, int tm, int tn)
 {
     const int per_tile = tm * tn / 2048;           // workgroups
     const int tail_tile = static_cast<int>(blockIdx.x) / per_tile;
-    const int begin = tail_tile * a.stages, end = begin + a.stages;
-    const int g0 = begin / a.tail_run, g1 = (end - 1) / a.tail_run;
-    if (g0 == g1) return;                          // one workgroup had the whole tile
     const int id = (static_cast<int>(blockIdx.x) % per_tile) * 256 + threadIdx.x;
     const int tile_row = id / (tn / 8), tile_col = (id % (tn / 8)) * 8;
     int64_t row, col;
@@ -841,11 +838,11 @@ __global__ __launch_bounds__(256) void ag_linear_join_kernel(LinearGemmArgs a, i
     col += tile_col;
     if (row >= a.I || col >= a.J) return;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int64_t part = static_cast<int64_t>(a.tiles_i * a.tiles_j - a.full_tiles) * (tm * tn);
+    const float* from = a.partial + static_cast<int64_t>(tail_tile) * (tm * tn) + tile_row * tn + tile_col;
 #pragma unroll 4
-    for (int q = g0; q <= g1; ++q) {
-        const bool starts = q * a.tail_run <= begin;      // the piece that holds the first step
-        const f32x4* src = reinterpret_cast<const f32x4*>(a.partial + (static_cast<int64_t>(q) * 2 + (starts ? 1 : 0)) * (tm * tn) +
-                                                          tile_row * tn + tile_col);
+    for (int q = 0; q < a.splits; ++q, from += part) {
+        const f32x4* src = reinterpret_cast<const f32x4*>(from);
         const f32x4 lo = src[0], hi = src[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -1062,7 +1059,7 @@ hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int t
     case kLinearTile256x128: fn = bf16 ? pick_form<true, Cfg256x128>(form, a.epi.act) : pick_form<false, Cfg256x128>(form, a.epi.act); break;
     default: break;
     }
-    if (fn == nullptr || programs < 1 || programs < a.tail_groups || a.stages < 1 || a.tail_run < 1) return hipErrorInvalidValue;
+    if (fn == nullptr || programs < 1 || a.stages < 1 || a.splits < 1 || a.split_stages < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(Cfg256::NT), 0, stream, a);
     return hipGetLastError();
 }
@@ -1142,7 +1139,7 @@ hipError_t launch_linear_grads(const LinearGemmArgs& dx, const LinearGemmArgs& d
 {
     const int64_t db_programs = db.db ? (db.N + 31) / 32 : 0;
     const int64_t grid = dx_programs + dw_programs + db_programs;
-    if (dx_programs < 1 || dw_programs < 1 || grid > 0x7fffffff || dx.tail_groups != 0 || dw.tail_groups != 0)
+    if (dx_programs < 1 || dw_programs < 1 || grid > 0x7fffffff || dx.splits != 1 || dw.splits != 1)
         return hipErrorInvalidValue;
     static_assert(Cfg128::NT == 256, "the bias gradient takes 256 threads");
     hipLaunchKernelGGL((bf16 ? ag_linear_grads_kernel<true, Cfg128> : ag_linear_grads_kernel<false, Cfg128>),

@@ -109,7 +109,7 @@ struct Product {
     int form = ag::kFormNT, tile = ag::kLinearTile128;
     int64_t I = 0, J = 0, R = 0;
     int64_t tiles_i = 0, tiles_j = 0, stages = 0;
-    int64_t full_tiles = 0, tail_groups = 0, tail_run = 0, programs = 0;
+    int64_t full_tiles = 0, splits = 1, split_stages = 1, programs = 0;
     bool join = false;           // some tail tile is cut
     double us = 0;               // estimated
     uint64_t partial_bytes = 0;
@@ -134,16 +134,16 @@ void whole_tiles(Product* p, int tile)
     p->tiles_i = (p->I + tm - 1) / tm;
     p->tiles_j = (p->J + tn - 1) / tn;
     p->full_tiles = p->programs = p->tiles_i * p->tiles_j;
-    p->tail_groups = 0;
-    p->tail_run = 1;
+    p->splits = 1;
+    p->split_stages = p->stages;
     p->join = false;
     p->partial_bytes = 0;
     p->us = p->stages * kKinds[tile].step_us[p->form] + kKinds[tile].fixed_us;
 }
 
 // Tile and cut with the shortest estimated time.  Whole rounds of tiles on all CUs go one to a workgroup; the
-// rest either too (one more round), or its steps are shared out evenly over G workgroups.  A cut adds the
-// partial tiles' traffic and a second launch.
+// rest (or that and the last round) either too, or its reductions are cut into parts.  A cut adds the partial
+// tiles' traffic and a second launch.
 ag_status_t choose(Product* p, int cus)
 {
     constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
@@ -158,7 +158,7 @@ ag_status_t choose(Product* p, int cus)
         const int64_t tiles = ti * tj, rounds = tiles / cus;
         const double step_us = kKinds[tile].step_us[p->form];
         const double tile_us = p->stages * step_us + kKinds[tile].fixed_us;
-        auto consider = [&](int64_t full, int64_t groups, int64_t run, bool join, double us) {
+        auto consider = [&](int64_t full, int64_t splits, int64_t run, double us) {
             if (found && us >= best) return;
             found = true;
             best = p->us = us;
@@ -166,26 +166,24 @@ ag_status_t choose(Product* p, int cus)
             p->tiles_i = ti;
             p->tiles_j = tj;
             p->full_tiles = full;
-            p->tail_groups = groups;
-            p->tail_run = run;
-            p->programs = std::max(groups, std::min<int64_t>(full, cus));
-            p->join = join;
-            p->partial_bytes = join ? up256(static_cast<uint64_t>(groups) * 2 * tm * tn * 4) : 0;
+            p->splits = splits;
+            p->split_stages = run;
+            p->join = splits > 1;
+            p->programs = std::min<int64_t>(cus, std::max(full, (tiles - full) * splits));
+            p->partial_bytes = splits > 1 ? up256(static_cast<uint64_t>(tiles - full) * splits * tm * tn * 4) : 0;
         };
-        consider(tiles, 0, 1, false, static_cast<double>((tiles + cus - 1) / cus) * tile_us);
+        consider(tiles, 1, p->stages, static_cast<double>((tiles + cus - 1) / cus) * tile_us);
         for (int64_t keep = rounds; keep >= std::max<int64_t>(0, rounds - 1); --keep) {
             const int64_t tail = tiles - keep * cus;
-            if (tail == 0 || tail > 2 * cus || tail * p->stages > 0x3fffffff) continue;
-            for (int part = 4; part >= 1; --part) {
-                const int64_t wanted = std::max<int64_t>(1, cus * part / 4);
-                const int64_t run = std::max<int64_t>(4, (tail * p->stages + wanted - 1) / wanted);
-                const int64_t groups = (tail * p->stages + run - 1) / run;
-                if (run >= p->stages && keep == rounds) continue;       // nothing is cut to gain by
-                const double pieces = static_cast<double>(std::min<int64_t>(2 * groups, tail + groups));
-                const double bytes = pieces * tm * tn * 4;
-                const double us = keep * tile_us + run * step_us + 2 * kKinds[tile].fixed_us + kJoinUs +
-                                  2 * bytes / kBytesPerUs;
-                consider(keep * cus, groups, run, true, us);
+            if (tail == 0) continue;
+            for (int64_t s = 2; s <= std::min<int64_t>(32, p->stages / 2); ++s) {
+                const int64_t run = (p->stages + s - 1) / s, splits = (p->stages + run - 1) / run;
+                if (splits != s) continue;
+                const double bytes = static_cast<double>(tail) * splits * tm * tn * 4;
+                if (bytes > 512e6) break;
+                const double parts = static_cast<double>((tail * splits + cus - 1) / cus);
+                consider(keep * cus, splits, run,
+                         keep * tile_us + parts * (run * step_us + kKinds[tile].fixed_us) + kJoinUs + 2 * bytes / kBytesPerUs);
             }
         }
     }
@@ -202,6 +200,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
         out->tile_n = 16;
         out->tile_k = 128;
         out->full_tiles = out->n_programs = static_cast<int32_t>((p.J + 15) / 16);
+        out->splits = 1;
         return;
     }
     int threads;
@@ -209,6 +208,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
     ag::linear_tile_shape(p.tile, &out->tile_m, &out->tile_n, &threads);
     out->tile_k = 64;
     out->full_tiles = static_cast<int32_t>(p.full_tiles);
+    out->splits = static_cast<int32_t>(p.splits);
     out->n_programs = static_cast<int32_t>(p.programs);
     out->packed = (pack_a ? 1 : 0) | (pack_b ? 2 : 0);
 }
@@ -254,8 +254,8 @@ ag::LinearGemmArgs gemm_args(const Product& p, const uint16_t* A, int64_t lda, c
     a.tiles_j = static_cast<int32_t>(p.tiles_j);
     a.stages = static_cast<int32_t>(p.stages);
     a.full_tiles = static_cast<int32_t>(p.full_tiles);
-    a.tail_groups = static_cast<int32_t>(p.tail_groups);
-    a.tail_run = static_cast<int32_t>(p.tail_run);
+    a.splits = static_cast<int32_t>(p.splits);
+    a.split_stages = static_cast<int32_t>(p.split_stages);
     a.partial = partial;
     a.epi = epi;
     return a;
@@ -328,7 +328,10 @@ ag_status_t plan_forward(const ag_linear_args_t* a, int cus, Forward* f)
     p.I = M;
     p.J = N;
     p.R = K;
-    p.stream = M <= ag::kLinearStreamRows;
+    // Few rows of x: w is what there is to move, and is streamed.  Above 16 rows every workgroup reads that much more
+    // of x, and from about 8M weights on tiles with cut reductions are faster: bf16, N x K 1024 x 1024, 32 rows 5.5
+    // against 12.1 us; 3584 x 8192, 32 rows 26.2 against 20.3 (16 rows: 18.7 streamed).
+    p.stream = M <= 16 || (M <= ag::kLinearStreamRows && N * K < (int64_t{1} << 23));
     if (!p.stream) {
         if ((s = choose(&p, cus)) != AG_OK) return s;
         f->ox = Operand{f->x.at, f->x.ld, M, K};

@@ -526,10 +526,10 @@ typedef struct ag_linear_args {
 typedef struct ag_product_plan {
     int32_t variant;      /* 0 = not computed, 1 = row streaming (few rows of x), 2 = tiles */
     int32_t tile_m, tile_n, tile_k;
-    int32_t full_tiles;   /* tiles that one workgroup computes whole; the steps of the others are shared out evenly, */
-    int32_t n_programs;   /*   and a second kernel joins the pieces.  n_programs: persistent workgroups */
+    int32_t full_tiles;   /* tiles that one workgroup computes whole */
+    int32_t splits;       /* parts that the others' reductions are cut into; a second kernel joins them */
+    int32_t n_programs;   /* persistent workgroups */
     int32_t packed;       /* bit 0 / 1: first / second operand copied to aligned rows first */
-    int32_t reserved;
 } ag_product_plan_t;
 
 typedef struct ag_linear_plan {
