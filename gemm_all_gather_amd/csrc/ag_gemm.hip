@@ -44,9 +44,19 @@
 #include <type_traits>
 
 #include "ag_internal.h"
-#include "ag_mfma.h"
+
+#define AG_LDS __attribute__((address_space(3)))
 
 namespace ag {
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kRawBufferWord3 = 0x00020000;
 // Wave rows of the 2-column wave grid (4: eight waves, two per SIMD).
 #ifndef AG_GEMM_WGM
 #define AG_GEMM_WGM 4
@@ -55,6 +65,54 @@ namespace ag {
 #ifndef AG_GEMM_STORE_AUX
 #define AG_GEMM_STORE_AUX 2
 #endif
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(uint64_t base, uint64_t records)
+{
+    const uint32_t r = records < 0x7fffffffull ? static_cast<uint32_t>(records) : 0x7fffffffu;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), static_cast<short>(0),
+                                             static_cast<int>(r), kRawBufferWord3);
+}
+
+// s_waitcnt with only the vector-memory counter limited (gfx9 encoding).
+template <int N>
+__device__ inline void wait_vmcnt()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+__device__ inline void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+// s_waitcnt with only the LDS/scalar counter limited (at most N outstanding).
+template <int N>
+__device__ inline void wait_lgkmcnt()
+{
+    static_assert(N >= 0 && N < 16, "lgkmcnt is 4 bits");
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4) | (N << 8));
+}
+
+template <bool BF16> struct Mfma;
+template <> struct Mfma<false> {
+    using V = f16x8;
+    static __device__ f32x4 run(V a, V b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ uint32_t pack(float x, float y)
+    {
+        const _Float16 hx = static_cast<_Float16>(x), hy = static_cast<_Float16>(y);
+        return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hx)) |
+               (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hy)) << 16);
+    }
+};
+template <> struct Mfma<true> {
+    using V = bf16x8;
+    static __device__ f32x4 run(V a, V b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+    static __device__ uint32_t pack(float x, float y)
+    {
+        const __bf16 hx = static_cast<__bf16>(x), hy = static_cast<__bf16>(y);
+        return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hx)) |
+               (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hy)) << 16);
+    }
+};
+
+}  // namespace
 
 // Tile configuration.  Named namespace: a kernel template instantiated with a
 // type of internal linkage gets no host-side launch handle.
