@@ -174,6 +174,30 @@ def test_adamw_read_states():
             assert_close(got[1:-1].double().cpu().numpy(), want, 2 * U32 * np.abs(want) + TINY["f32"], f"tensor {i}")
 
 
+def test_adamw_beyond_32_bit_offsets():
+    """A tensor of more than 2^31 elements: its last block."""
+    require_gpu()
+    n, last = 2 ** 31 + 5000, 136       # 5000 = 19 blocks and 136 elements
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros_like(p)
+    blocks = -(-n // BLOCK)
+    m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.zeros(blocks, device="cuda"), torch.zeros(blocks, device="cuda")
+    g[-last:] = torch.randn(last, device="cuda").bfloat16()
+    opt = ag.AdamW([p], [g], [m], [v], exp_avg_scales=[ms], exp_avg_sq_scales=[vs])
+    log("adamw beyond 2^31 elements")
+    opt.step(1, **HYPER, seed=11)
+    torch.cuda.synchronize()
+    g64 = g[-last:].double().cpu().numpy()
+    p1, m1, v1 = adamw_oracle(np.zeros(last), g64, np.zeros(last), np.zeros(last), 1, HYPER["lr"], HYPER["beta1"],
+                              HYPER["beta2"], HYPER["eps"], HYPER["weight_decay"])
+    cm, sm, cv, sv = adamw8_codes_oracle(m1, v1, blocks - 1, 11)
+    assert np.array_equal(m[-last:].double().cpu().numpy(), cm) and np.array_equal(v[-last:].double().cpu().numpy(), cv)
+    assert ms[-1].item() == sm[0] and vs[-1].item() == sv[0]
+    assert_close(p[-last:].double().cpu().numpy(), p1, rounded_bound(p1, 32 * U32 * np.abs(p1), "bf16"), "p")
+    assert not p[:-last].any() and not m[:-last].any() and not vs[:-1].any()
+
+
 def test_adamw_8bit_nothing_live_meets_a_zero_denominator():
     """Gradients a million times smaller than their block's largest still move by at most a few times lr."""
     require_gpu()

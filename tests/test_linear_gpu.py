@@ -168,6 +168,37 @@ def test_linear_on_another_stream_twice_the_same(M):
     assert torch.equal(first, f.y.buffer.view(torch.int16))
 
 
+def test_linear_offsets_beyond_32_bits():
+    """x of 2^31 elements and more: its last rows, through the tiles and as the reduction of dw."""
+    require_gpu()
+    M, N, K = 262200, 40, 8200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = (torch.randn(N, K, generator=g, device="cuda") / K ** 0.5).bfloat16()
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert M * K > 2 ** 31
+    args = dict(x=x, w=w, y=y, M=M, N=N, K=K, dtype="bf16")
+    log("linear beyond 2^31 elements")
+    ag.linear(**args, workspace=workspace(ag.plan_linear(**args)))
+    torch.cuda.synchronize()
+    for first in (0, 131000, 261900, M - 7):
+        xs = x[first:first + 7].double().cpu().numpy()
+        want = xs @ w.double().cpu().numpy().T
+        bound = rounded_bound(want, product_bound(xs, w.double().cpu().numpy(), K), "bf16")
+        assert_close(y[first:first + 7].double().cpu().numpy(), want, bound, f"rows from {first}")
+    # dw of a gradient that is zero but in the last rows is their product alone
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dy[-5:] = torch.randn(5, N, generator=g, device="cuda").bfloat16()
+    dw = torch.empty(N, K, dtype=torch.float32, device="cuda")
+    args = dict(dy=dy, x=x, w=None, M=M, N=N, K=K, dtype="bf16", dw=dw, dw_dtype="f32")
+    log("linear_backward beyond 2^31 elements")
+    ag.linear_backward(**args, workspace=workspace(ag.plan_linear_backward(**args)))
+    torch.cuda.synchronize()
+    d, xs = dy[-5:].double().cpu().numpy(), x[-5:].double().cpu().numpy()
+    assert_close(dw.double().cpu().numpy(), d.T @ xs, product_bound(d.T, xs.T, 5) + 1e-30, "dw")
+
+
 # ------------------------------------------------------------------ gradients
 
 class Backward:
