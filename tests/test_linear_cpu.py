@@ -13,6 +13,7 @@ import torch
 from gemm_all_gather_amd import binding as ag
 from oracle.linear_oracle import (BLOCK, act_oracle, adamw8_codes_oracle, adamw_oracle, decode_oracle,
                                   linear_backward_oracle, linear_oracle, random_bits_oracle, slope_oracle)
+from tests.linear_util import HUGE, LARGE
 
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
 A = 1 << 44         # a device address; matrices lie 1 GiB apart
@@ -127,6 +128,25 @@ def test_plan_linear_backward_counts_work_and_workspace():
     none = ag.plan_linear_backward(**dict(BACKWARD, act="none", z=None, db=None, dw=None, x=None))
     assert none.product_dw.variant == 0 and none.flops == 2.0 * 1000 * 3584 * 8192
     assert none.launches == (2 if none.workspace_bytes else 1)
+
+
+def test_the_gpu_tests_sizes_reach_every_product_kernel():
+    """Tiles, layouts, whole and cut reductions, and the small layers' gradients in one launch (256 CUs)."""
+    seen = set()
+    for M, N, K in LARGE + HUGE:
+        sizes = dict(M=M, N=N, K=K)
+        f = ag.plan_linear(**dict(FORWARD, **sizes)).product
+        b = ag.plan_linear_backward(**dict(BACKWARD, **sizes))
+        for form, q in (("y", f), ("dx", b.product), ("dw", b.product_dw)):
+            seen.add((form, q.tile_m, q.tile_n))
+            seen.add((form, "cut" if q.splits > 1 else "whole"))
+            if q.splits > 1 and q.full_tiles:
+                seen.add((form, "whole rounds, then cut"))
+        seen.add(("launches", b.launches))
+    for form in ("y", "dx", "dw"):
+        for want in ((256, 256), (128, 128), (256, 128), ("cut",), ("whole",), ("whole rounds, then cut",)):
+            assert (form, *want) in seen, (form, want)
+    assert ("launches", 2) in seen
 
 
 def test_launches_without_a_device_report_hip_errors():

@@ -14,7 +14,7 @@ import torch
 from gemm_all_gather_amd import binding as ag
 from oracle.linear_oracle import act_oracle, linear_backward_oracle, linear_oracle, slope_oracle
 from tests.gpu_util import log, require_gpu
-from tests.linear_util import (ACT_ERROR, HALF_STEP, U32, Matrix, TORCH, assert_close, product_bound, random_matrix,
+from tests.linear_util import (ACT_ERROR, HALF_STEP, HUGE, LARGE, U32, Matrix, TORCH, assert_close, product_bound, random_matrix,
                                rounded_bound)
 
 pytestmark = pytest.mark.gpu
@@ -97,8 +97,6 @@ def test_linear_epilogue_parts(M, act):
                 f.check(what)
 
 
-# 256-row tiles, split reductions, several tiles either way
-LARGE = [(33, 600, 4100), (130, 520, 3000), (1000, 1030, 2050), (1100, 2300, 200), (2048, 1024, 512), (700, 700, 8192)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
@@ -112,6 +110,17 @@ def test_linear_larger_sizes(M, N, K):
         log(f"  tile {p.product.tile_m}x{p.product.tile_n} full {p.product.full_tiles} of {p.product.n_programs} programs packed {p.product.packed}")
         f.run()
         f.check(what)
+
+
+def test_linear_more_tiles_than_cus():
+    """Whole rounds of tiles, and the others' reductions cut."""
+    require_gpu()
+    M, N, K = HUGE[0]
+    f = Forward(M, N, K, "bf16", "silu", z=False)
+    p = ag.plan_linear(**f.args()).product
+    log(f"linear {M}x{N}x{K}: tile {p.tile_m}x{p.tile_n} full {p.full_tiles} splits {p.splits}")
+    f.run()
+    f.check(f"linear {M}x{N}x{K}")
 
 
 @pytest.mark.parametrize("M", [0, 1, 40])
@@ -293,6 +302,15 @@ def test_linear_backward_larger_sizes(M, N, K):
         b = Backward(M, N, K, dtype, "gelu", pad=pad)
         b.run()
         b.check(what)
+
+
+@pytest.mark.parametrize("M,N,K", HUGE)
+def test_linear_backward_more_tiles_than_cus(M, N, K):
+    require_gpu()
+    b = Backward(M, N, K, "f16", "none", "f32", accumulate=True)
+    log(f"linear_backward {M}x{N}x{K}")
+    b.run()
+    b.check(f"linear_backward {M}x{N}x{K}")
 
 
 def test_linear_backward_each_gradient_alone():
