@@ -21,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libag.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["ag_host.cpp", "ag_copy.hip", "ag_gemm.hip", "ag_util.hip", "ag_linear_host.cpp", "ag_linear.hip",
+           "ag_linear_forward_f16.hip", "ag_linear_forward_bf16.hip", "ag_linear_grads_f16.hip",
+           "ag_linear_grads_bf16.hip",
            "ag_adamw_host.cpp", "ag_adamw.hip"]
 ARCH = "gfx950"
 

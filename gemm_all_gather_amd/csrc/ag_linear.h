@@ -31,6 +31,8 @@ struct LinearGemmArgs {
     int32_t full_tiles;         // tiles that one workgroup computes whole, the first of the order
     int32_t splits;             // parts of the other tiles' reductions, split_stages steps each (the last may be shorter)
     int32_t split_stages;
+    int32_t heavy;              // > 0: whole tiles, common_rounds rounds on all workgroups and the rest on those from
+    int32_t common_rounds;      //   number `heavy` on
     float* partial;             // fp32 tile (part, tail tile)
     LinearEpilogue epi;
 };
@@ -39,6 +41,13 @@ enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1, kLinearTile256x128 = 2
 enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
 
 hipError_t launch_linear_gemm(const LinearGemmArgs& a, int bf16, int form, int tile, int programs, hipStream_t stream);
+// The tiled kernels, by type (each in a source of its own); null where there is none.
+using LinearGemmFn = void (*)(LinearGemmArgs);
+LinearGemmFn linear_forward_f16(int act, int tile);
+LinearGemmFn linear_forward_bf16(int act, int tile);
+LinearGemmFn linear_gradient_f16(int form, int tile);
+LinearGemmFn linear_gradient_bf16(int form, int tile);
+
 // Joins the parts of the cut tiles in order and applies the epilogue.
 hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream);
 
@@ -79,7 +88,18 @@ struct LinearBiasGradArgs {
 };
 hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream);
 
-// dx, dw and (db.db set) db in one launch of 128 x 128 tiles, without tails.
+using LinearInTurnFn = void (*)(LinearGemmArgs, LinearGemmArgs, LinearBiasGradArgs);
+LinearInTurnFn linear_in_turn_f16(bool dx_first);
+LinearInTurnFn linear_in_turn_bf16(bool dx_first);
+using LinearSideBySideFn = void (*)(LinearGemmArgs, LinearGemmArgs, int, int, LinearBiasGradArgs);
+LinearSideBySideFn linear_side_by_side_f16();
+LinearSideBySideFn linear_side_by_side_bf16();
+
+// dx, dw and (db.db set) db in turn on `programs` workgroups, in 256 x 256 tiles, none cut.
+hipError_t launch_linear_grads_in_turn(const LinearGemmArgs& dx, const LinearGemmArgs& dw, bool dx_first, int programs,
+                                       const LinearBiasGradArgs& db, int bf16, hipStream_t stream);
+
+// dx, dw and (db.db set) db in one launch of 128 x 128 tiles, none cut.
 hipError_t launch_linear_grads(const LinearGemmArgs& dx, const LinearGemmArgs& dw, int dx_programs, int dw_programs,
                                const LinearBiasGradArgs& db, int bf16, hipStream_t stream);
 

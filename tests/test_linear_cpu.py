@@ -5,6 +5,7 @@ import os
 import re
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
@@ -343,16 +344,22 @@ def linear_asm(tmp_path_factory):
         pytest.skip("hipcc not available")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     csrc = os.path.join(root, "gemm_all_gather_amd", "csrc")
-    out = str(tmp_path_factory.mktemp("isa") / "linear.s")
-    subprocess.run([hipcc, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
-                    "-packed-fp32-ops", f"-I{csrc}", f"-I{os.path.join(root, 'include')}", "--cuda-device-only", "-S",
-                    "-o", out, os.path.join(csrc, "ag_linear.hip")], check=True, capture_output=True)
-    return open(out).read()
+    tmp = tmp_path_factory.mktemp("isa")
+
+    def compile_one(name):
+        out = str(tmp / (name + ".s"))
+        subprocess.run([hipcc, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
+                        "-packed-fp32-ops", f"-I{csrc}", f"-I{os.path.join(root, 'include')}", "--cuda-device-only",
+                        "-S", "-o", out, os.path.join(csrc, name + ".hip")], check=True, capture_output=True)
+        return open(out).read()
+
+    with ThreadPoolExecutor(2) as pool:
+        return "\n".join(pool.map(compile_one, ("ag_linear_forward_bf16", "ag_linear_grads_bf16")))
 
 
 def test_product_kernels_wait_for_fragments_and_never_spill(linear_asm):
-    kernels = re.findall(r"^(_Z\S*ag_linear_gemm_kernel\S*):", linear_asm, re.M)
-    assert len(kernels) >= 12
+    kernels = re.findall(r"^(_Z\S*ag_linear_(?:gemm|grads)\S*):", linear_asm, re.M)
+    assert len(kernels) == 15 + 6 + 3     # 5 activations, 2 gradients in 3 tiles; in turn either way, side by side
     for k in kernels:
         start = linear_asm.index(f"\n{k}:")
         lines = [ln.split(";", 1)[0].strip() for ln in linear_asm[start:linear_asm.index("s_endpgm", start)].splitlines()]
