@@ -477,7 +477,8 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         if (x.full_tiles <= 0x7fffff && w.full_tiles <= 0x7fffff) {
             const bool dx_first = x.us >= w.us;
             const double us = dx_first ? in_turn(x, &w, cus) : in_turn(w, &x, cus);
-            if (us < 0.85 * (b->px.us + b->pw.us)) {
+            const double apart = b->px.us + b->pw.us + 4.0 * ((want_db ? 1 : 0) + b->px.launches() + b->pw.launches() - 1);
+            if (us < 0.87 * apart) {
                 b->in_turn = true;
                 b->dx_first = dx_first;
                 x.programs = w.programs = cus;

@@ -17,8 +17,8 @@ ACT_ERROR = 2.0 ** -19
 
 # M, N, K of the larger products.  Between them they reach every tile in every layout, whole and cut.
 LARGE = [(33, 600, 4100), (130, 520, 3000), (1000, 1030, 2050), (1100, 2300, 200), (2048, 1024, 512), (700, 700, 8192),
-         (2100, 2300, 520), (600, 1100, 8300), (8300, 1100, 600)]
-HUGE = [(4352, 4000, 4096), (4000, 4352, 4100)]
+         (2100, 2300, 520), (600, 1100, 8300), (8300, 1100, 600), (1100, 8300, 600)]
+HUGE = [(4352, 4000, 4096), (4000, 4352, 4100), (4608, 4096, 1200)]
 
 
 class Matrix:

@@ -138,16 +138,19 @@ def test_the_gpu_tests_sizes_reach_every_product_kernel():
         sizes = dict(M=M, N=N, K=K)
         f = ag.plan_linear(**dict(FORWARD, **sizes)).product
         b = ag.plan_linear_backward(**dict(BACKWARD, **sizes))
-        for form, q in (("y", f), ("dx", b.product), ("dw", b.product_dw)):
+        one = b.launches == 2 and b.product.tile_m != 0 and b.product_dw.tile_m != 0    # after the slope kernel
+        if one:
+            seen.add(("in one launch", b.product.tile_m, N >= M))       # which of 256-row tiles' dx and dw goes first
+        for form, q in (("y", f),) if one else (("y", f), ("dx", b.product), ("dw", b.product_dw)):
             seen.add((form, q.tile_m, q.tile_n))
             seen.add((form, "cut" if q.splits > 1 else "whole"))
             if q.splits > 1 and q.full_tiles:
                 seen.add((form, "whole rounds, then cut"))
-        seen.add(("launches", b.launches))
     for form in ("y", "dx", "dw"):
         for want in ((256, 256), (128, 128), (256, 128), ("cut",), ("whole",), ("whole rounds, then cut",)):
             assert (form, *want) in seen, (form, want)
-    assert ("launches", 2) in seen
+    for want in ((128, True), (256, False), (256, True)):
+        assert ("in one launch", *want) in seen, want
 
 
 def test_launches_without_a_device_report_hip_errors():
@@ -309,22 +312,48 @@ def _registers(operand):
 
 
 def unwaited_uses(lines):
-    """Instructions that touch a register which an LDS read before them may still be writing.
+    """Instructions that touch a register which an LDS read before them, on some path, may still be writing.
 
-    Straight-line: a read stays in flight until a wait for the LDS counter to reach zero.
+    A read stays in flight until a wait for the LDS counter to reach zero; what is in flight flows along
+    branches and into labels.
     """
-    flying, found = {}, []
-    for ln in lines:
-        if ln.startswith("s_waitcnt") and "lgkmcnt(0)" in ln:
-            flying.clear()
-            continue
-        parts = re.split(r"[\s,]+", ln)
-        used = set().union(*(_registers(p) for p in parts[1:])) if len(parts) > 1 else set()
-        if used & set(flying):
-            found.append(ln)
-        if ln.startswith(("ds_read_b128", "ds_read_b64_tr_b16")):
-            for r in _registers(parts[1]):
-                flying[r] = ln
+    starts = sorted({0} | {i for i, ln in enumerate(lines) if ln.endswith(":")} |
+                    {i + 1 for i, ln in enumerate(lines) if re.match(r"s_(cbranch|branch|endpgm)", ln)})
+    blocks = [(i, j) for i, j in zip(starts, starts[1:] + [len(lines)]) if i < j]
+    label = {lines[i][:-1]: k for k, (i, _) in enumerate(blocks) if lines[i].endswith(":")}
+    after = []
+    for k, (_, j) in enumerate(blocks):
+        last = lines[j - 1]
+        m = re.match(r"s_c?branch\S*\s+(\S+)", last)
+        to = [label[m.group(1)]] if m and m.group(1) in label else []
+        if not re.match(r"s_(branch|endpgm)", last) and k + 1 < len(blocks):
+            to.append(k + 1)
+        after.append(to)
+
+    def walk(k, flying, found):
+        flying = set(flying)
+        for ln in lines[blocks[k][0]:blocks[k][1]]:
+            if ln.startswith("s_waitcnt") and "lgkmcnt(0)" in ln:
+                flying.clear()
+                continue
+            parts = re.split(r"[\s,]+", ln)
+            if flying and any(_registers(q) & flying for q in parts[1:]):
+                found.append(ln)
+            if ln.startswith(("ds_read_b128", "ds_read_b64_tr_b16")):
+                flying |= _registers(parts[1])
+        return flying
+
+    entry, todo = [set() for _ in blocks], list(range(len(blocks)))
+    while todo:
+        k = todo.pop()
+        out = walk(k, entry[k], [])
+        for n in after[k]:
+            if not out <= entry[n]:
+                entry[n] |= out
+                todo.append(n)
+    found = []
+    for k in range(len(blocks)):
+        walk(k, entry[k], found)
     return found
 
 
@@ -335,6 +364,9 @@ def test_unwaited_uses_sees_a_missing_wait():
     assert unwaited_uses(read + ["v_mov_b32_e32 v30, v9"]) == ["v_mov_b32_e32 v30, v9"]
     assert unwaited_uses(read + ["s_waitcnt lgkmcnt(0)", use]) == []
     assert unwaited_uses(read + ["v_add_u32_e32 v1, v2, v3"]) == []
+    # around a loop's back edge, and not past a branch that is always taken
+    assert use in unwaited_uses([".L1:", use] + read + ["s_cbranch_scc1 .L1", "s_endpgm"])
+    assert unwaited_uses(read + ["s_branch .L2", ".L1:", use, ".L2:", "s_waitcnt lgkmcnt(0)", "s_endpgm"]) == []
 
 
 @pytest.fixture(scope="module")
@@ -362,11 +394,10 @@ def test_product_kernels_wait_for_fragments_and_never_spill(linear_asm):
     assert len(kernels) == 15 + 6 + 3     # 5 activations, 2 gradients in 3 tiles; in turn either way, side by side
     for k in kernels:
         start = linear_asm.index(f"\n{k}:")
-        lines = [ln.split(";", 1)[0].strip() for ln in linear_asm[start:linear_asm.index("s_endpgm", start)].splitlines()]
-        lines = [ln for ln in lines if ln and not ln.endswith(":")]
+        lines = [ln.split(";", 1)[0].strip() for ln in linear_asm[start:linear_asm.index(".section", start)].splitlines()]
+        lines = [ln for ln in lines if ln]
         assert sum(ln.startswith("v_mfma") for ln in lines) >= 32, k
-        # the epilogue's own LDS reads are the compiler's; the loop's end with the last product
-        last = max(i for i, ln in enumerate(lines) if ln.startswith("v_mfma"))
-        assert not unwaited_uses(lines[:last + 1]), (k, unwaited_uses(lines[:last + 1])[:3])
+        assert sum(ln.startswith("ds_read") for ln in lines) >= 16, k
+        assert not unwaited_uses(lines), (k, unwaited_uses(lines)[:3])
         meta = re.search(r"\.amdhsa_kernel " + re.escape(k) + r"\n(.*?)\.end_amdhsa_kernel", linear_asm, re.S).group(1)
         assert re.search(r"private_segment_fixed_size 0\n", meta), k
