@@ -22,27 +22,32 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
 struct __attribute__((packed, aligned(4))) Any16f { u32x4 v; };
 struct __attribute__((packed, aligned(1))) Any8 { u32x2 v; };
+// The table's addresses are global memory, which the compiler cannot know of a pointer read from memory (it
+// would take the slower flat accesses, which count as LDS accesses too).
+#define AG_GLOBAL __attribute__((address_space(1)))
+template <class T> using Global = AG_GLOBAL T*;
+template <class T, class P> __device__ __forceinline__ Global<T> global(P* p) { return (Global<T>)(p); }
 
 template <int DT> struct Type;      // ag_dtype_t
 template <> struct Type<AG_F32> {
     using T = float;
-    static __device__ __forceinline__ void load(float (&x)[8], const float* p)
+    static __device__ __forceinline__ void load(float (&x)[8], Global<const float> p)
     {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const u32x4 t = reinterpret_cast<const Any16f*>(p + 4 * h)->v;
+            const u32x4 t = ((Global<const Any16f>)(p + 4 * h))->v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[4 * h + e] = __uint_as_float(t[e]);
         }
     }
-    static __device__ __forceinline__ void store(float* p, const float (&x)[8])
+    static __device__ __forceinline__ void store(Global<float> p, const float (&x)[8])
     {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             u32x4 t;
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[e] = __float_as_uint(x[4 * h + e]);
-            reinterpret_cast<Any16f*>(p + 4 * h)->v = t;
+            ((Global<Any16f>)(p + 4 * h))->v = t;
         }
     }
     static __device__ __forceinline__ float get(float v) { return v; }
@@ -60,19 +65,19 @@ template <bool BF16> struct Half {
         if constexpr (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
         else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
     }
-    static __device__ __forceinline__ void load(float (&x)[8], const uint16_t* p)
+    static __device__ __forceinline__ void load(float (&x)[8], Global<const uint16_t> p)
     {
-        const u32x4 t = reinterpret_cast<const Any16*>(p)->v;
+        const u32x4 t = ((Global<const Any16>)p)->v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = get(static_cast<uint16_t>(t[e / 2] >> (16 * (e & 1))));
     }
-    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[8])
+    static __device__ __forceinline__ void store(Global<uint16_t> p, const float (&x)[8])
     {
         u32x4 t;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             t[e] = static_cast<uint32_t>(put(x[2 * e])) | (static_cast<uint32_t>(put(x[2 * e + 1])) << 16);
-        reinterpret_cast<Any16*>(p)->v = t;
+        ((Global<Any16>)p)->v = t;
     }
 };
 template <> struct Type<AG_F16> : Half<false> {};
@@ -81,7 +86,7 @@ template <> struct Type<AG_BF16> : Half<true> {};
 template <int DT>
 __device__ __forceinline__ void load8(float (&x)[8], const void* base, int64_t at, int n)
 {
-    const typename Type<DT>::T* p = static_cast<const typename Type<DT>::T*>(base) + at;
+    const Global<const typename Type<DT>::T> p = global<const typename Type<DT>::T>(base) + at;
     if (n >= 8) {
         Type<DT>::load(x, p);
     } else {
@@ -92,7 +97,7 @@ __device__ __forceinline__ void load8(float (&x)[8], const void* base, int64_t a
 template <int DT>
 __device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[8], int n)
 {
-    typename Type<DT>::T* p = static_cast<typename Type<DT>::T*>(base) + at;
+    const Global<typename Type<DT>::T> p = global<typename Type<DT>::T>(base) + at;
     if (n >= 8) {
         Type<DT>::store(p, x);
     } else {
@@ -103,8 +108,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[
 }
 __device__ __forceinline__ uint64_t load_codes(const void* base, int64_t at, int n)
 {
-    const uint8_t* p = static_cast<const uint8_t*>(base) + at;
-    if (n >= 8) return __builtin_bit_cast(uint64_t, reinterpret_cast<const Any8*>(p)->v);
+    const Global<const uint8_t> p = global<const uint8_t>(base) + at;
+    if (n >= 8) return __builtin_bit_cast(uint64_t, ((Global<const Any8>)p)->v);
     uint64_t c = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -113,9 +118,9 @@ __device__ __forceinline__ uint64_t load_codes(const void* base, int64_t at, int
 }
 __device__ __forceinline__ void store_codes(void* base, int64_t at, uint64_t c, int n)
 {
-    uint8_t* p = static_cast<uint8_t*>(base) + at;
+    const Global<uint8_t> p = global<uint8_t>(base) + at;
     if (n >= 8) {
-        reinterpret_cast<Any8*>(p)->v = __builtin_bit_cast(u32x2, c);
+        ((Global<Any8>)p)->v = __builtin_bit_cast(u32x2, c);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -144,18 +149,25 @@ __device__ __forceinline__ AdamwScalars scalars(const AdamwArgs& a)
     return s;
 }
 
-// sqrt to 1 ulp; the instruction takes no subnormal numbers, so small arguments are scaled by 2^96 before it.
-__device__ __forceinline__ float root(float x)
+// The updates of 8 elements, square roots and quotients by the instructions' 1 ulp: 2^-21 of the step, below the
+// parameter's own rounding.  The root instruction takes no subnormal numbers: against an eps of 1e-12 and more
+// what it loses (below 1e-19) is nothing; with a smaller eps small arguments are scaled by 2^96 first.
+__device__ __forceinline__ void update(float (&p)[8], const float (&m)[8], const float (&v)[8], const AdamwScalars& s)
 {
-    const bool small = x < 1e-30f;
-    const float r = __builtin_amdgcn_sqrtf(small ? x * 0x1p96f : x);
-    return small ? r * 0x1p-48f : r;
-}
-
-// The quotient by the reciprocal instruction (1 ulp): its error is 2^-22 of the step, below the parameter's own rounding.
-__device__ __forceinline__ float update(float p, float m, float v, const AdamwScalars& s)
-{
-    return p * s.decay - s.rate * m * __builtin_amdgcn_rcpf(root(v * s.inv_bias2) + s.eps);
+    if (s.eps >= 1e-12f) {   // uniform
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            p[e] = p[e] * s.decay - s.rate * m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e] * s.inv_bias2) + s.eps);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = v[e] * s.inv_bias2;
+            const bool small = x < 1e-30f;
+            float r = __builtin_amdgcn_sqrtf(small ? x * 0x1p96f : x);
+            r = small ? r * 0x1p-48f : r;
+            p[e] = p[e] * s.decay - s.rate * m[e] / (r + s.eps);
+        }
+    }
 }
 
 // 32 random bits of the state element at place i (counted over all tensors' blocks): multiply and xor-shift
@@ -256,18 +268,18 @@ __global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
             for (int e = 0; e < 8; ++e) {
                 m[e] = s.b1 * m[e] + s.one_minus_b1 * g[e];
                 v[e] = s.b2 * v[e] + s.one_minus_b2 * g[e] * g[e];
-                p[e] = update(p[e], m[e], v[e], s);
             }
+            update(p, m, v, s);
             store8<AG_F32>(t.exp_avg, at, m, n);
             store8<AG_F32>(t.exp_avg_sq, at, v, n);
         } else {
             const int64_t block = at / AG_ADAMW_BLOCK;
             const bool block_live = block * AG_ADAMW_BLOCK < t.n;
             const uint64_t mc = load_codes(t.exp_avg, n ? at : 0, n), vc = load_codes(t.exp_avg_sq, n ? at : 0, n);
-            const double ms = block_live ? t.exp_avg_scale[block] * kCodeM : 0.0;
-            const double vs = block_live ? t.exp_avg_sq_scale[block] * kCodeV : 0.0;
+            const double ms = block_live ? global<const float>(t.exp_avg_scale)[block] * kCodeM : 0.0;
+            const double vs = block_live ? global<const float>(t.exp_avg_sq_scale)[block] * kCodeV : 0.0;
             double m[8], v[8];
-            float ma[8], vf[8];
+            float mf[8], vf[8];
             uint32_t mmax = 0, vmax = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -277,14 +289,13 @@ __global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
                 const double cv2 = static_cast<double>(cv * cv);
                 m[e] = blend(a.beta1, static_cast<double>(cm * fabsf(cm)) * ms, a.one_minus_beta1 * g[e]);
                 v[e] = blend(a.beta2, cv2 * cv2 * vs, a.one_minus_beta2 * g[e] * g[e]);
-                const float mf = static_cast<float>(m[e]);
-                ma[e] = fabsf(mf);
+                mf[e] = static_cast<float>(m[e]);
                 vf[e] = static_cast<float>(v[e]);
-                const uint32_t mb = __float_as_uint(ma[e]), vb = __float_as_uint(vf[e]) & 0x7fffffffu;
+                const uint32_t mb = __float_as_uint(mf[e]) & 0x7fffffffu, vb = __float_as_uint(vf[e]) & 0x7fffffffu;
                 mmax = mmax > mb ? mmax : mb;
                 vmax = vmax > vb ? vmax : vb;
-                p[e] = update(p[e], mf, vf[e], s);
             }
+            update(p, mf, vf, s);
             mmax = block_max(mmax);
             vmax = block_max(vmax);
             // a block that holds an infinity or a NaN reads back as NaN: all codes 0, the maximum NaN
@@ -296,48 +307,47 @@ __global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
             const float vi = vfine && vS > 1e-30f ? __builtin_amdgcn_rcpf(vS) : 0.f;
             const bool mtiny = mfine && mmax != 0 && mi == 0.f, vtiny = vfine && vmax != 0 && vi == 0.f;
             float km[8], kv[8], um[8], uv[8];
-            uint32_t open = 0;      // codes to decide: bits 0-7 first moments, 8-15 second
+            bool near_m[8], near_v[8], any = false;     // codes for decide()
             const uint64_t place = (static_cast<uint64_t>(t.first_block) * AG_ADAMW_BLOCK) + static_cast<uint64_t>(at);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                um[e] = uv[e] = 0.5f;
-                if (a.stochastic) {   // uniform
+            for (int e = 0; e < 8; ++e) um[e] = uv[e] = 0.5f;
+            if (a.stochastic) {   // uniform
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
                     const uint32_t bits = random_bits(s.seed, place + e);
                     um[e] = static_cast<float>(2 * (bits & 0xffffu) + 1) * (1.f / 131072.f);
                     uv[e] = static_cast<float>(2 * (bits >> 16) + 1) * (1.f / 131072.f);
                 }
-                bool near;
-                km[e] = guess<2>(ma[e], mi, um[e], near);
-                open |= near ? 1u << e : 0u;
-                kv[e] = guess<4>(vf[e], vi, uv[e], near);
-                open |= near ? 256u << e : 0u;
             }
-            if (mtiny) open |= 0xffu;
-            if (vtiny) open |= 0xff00u;
-            if (!mfine || mmax == 0) open &= ~0xffu;
-            if (!vfine || vmax == 0) open &= ~0xff00u;
-            if (__any(open != 0)) {
+            const bool mlive = mfine && mmax != 0, vlive = vfine && vmax != 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                km[e] = guess<2>(fabsf(mf[e]), mi, um[e], near_m[e]);
+                kv[e] = guess<4>(vf[e], vi, uv[e], near_v[e]);
+                any |= near_m[e] | near_v[e];
+            }
+            if (__any(any | mtiny | vtiny)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (open & (1u << e)) km[e] = decide<2>(fabs(m[e]), mS, um[e]);
-                    if (open & (256u << e)) kv[e] = decide<4>(v[e], vS, uv[e]);
+                    if ((near_m[e] | mtiny) & mlive) km[e] = decide<2>(fabs(m[e]), mS, um[e]);
+                    if ((near_v[e] | vtiny) & vlive) kv[e] = decide<4>(v[e], vS, uv[e]);
                 }
             }
             uint32_t mo[2] = {0, 0}, vo[2] = {0, 0};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                int cm = mfine ? static_cast<int>(km[e]) : 0;
-                int cv = vfine ? static_cast<int>(kv[e]) : 0;
-                if (vfine && v[e] > 0.0 && cv < 1) cv = 1;
-                if (m[e] < 0.0) cm = -cm;
+                kv[e] = v[e] > 0.0 ? fmaxf(kv[e], 1.f) : kv[e];
+                const int cm = static_cast<int>(copysignf(km[e], mf[e])), cv = static_cast<int>(kv[e]);
                 mo[e / 4] |= (static_cast<uint32_t>(cm) & 0xffu) << (8 * (e % 4));
                 vo[e / 4] |= static_cast<uint32_t>(cv) << (8 * (e % 4));
             }
+            if (!mfine) mo[0] = mo[1] = 0;
+            if (!vfine) vo[0] = vo[1] = 0;
             store_codes(t.exp_avg, at, mo[0] | static_cast<uint64_t>(mo[1]) << 32, n);
             store_codes(t.exp_avg_sq, at, vo[0] | static_cast<uint64_t>(vo[1]) << 32, n);
             if (block_live && (threadIdx.x & 31) == 0) {
-                t.exp_avg_scale[block] = mS;
-                t.exp_avg_sq_scale[block] = vS;
+                global<float>(t.exp_avg_scale)[block] = mS;
+                global<float>(t.exp_avg_sq_scale)[block] = vS;
             }
         }
         if constexpr (MASTER) store8<AG_F32>(t.master, at, p, n);
@@ -361,8 +371,8 @@ __global__ __launch_bounds__(256) void ag_adamw_read_kernel(AdamwReadArgs a)
     if (left <= 0) return;
     const int n = static_cast<int>(left > 8 ? 8 : left);
     const uint64_t mc = load_codes(t.exp_avg, at, n), vc = load_codes(t.exp_avg_sq, at, n);
-    const double ms = t.exp_avg_scale[at / AG_ADAMW_BLOCK] * kCodeM;
-    const double vs = t.exp_avg_sq_scale[at / AG_ADAMW_BLOCK] * kCodeV;
+    const double ms = global<const float>(t.exp_avg_scale)[at / AG_ADAMW_BLOCK] * kCodeM;
+    const double vs = global<const float>(t.exp_avg_sq_scale)[at / AG_ADAMW_BLOCK] * kCodeV;
     float m[8], v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
