@@ -232,13 +232,16 @@ struct Cfg {
     static constexpr int LDS = SA * A_BYTES + SB * B_BYTES;
     static constexpr int LA = TM / 32, LB = TN / 32;       // loads of a wave per stage
     static constexpr int READ_STEP = PRODUCTS / (2 * (BM + BN)) > 0 ? PRODUCTS / (2 * (BM + BN)) : 1;   // products per read
-    static constexpr int LOAD_STEP = PRODUCTS / (LA + LB); // products per load
-    // Loads still in flight when the next stage has landed.  Each stage issues A's SA stages on and B's SB on, the
-    // sooner needed first, so those after the next stage's are whole groups and, with unequal rings, the other half.
+    // One operand's slot is refilled in the half that follows its last read, the other's (of the deeper ring, B's
+    // of equal ones) in the half after that, the first of the next stage.
+    static constexpr bool LATE_A = SA > SB;
+    static constexpr int STEP_A = PRODUCTS / LA, STEP_B = PRODUCTS / LB;   // products per load
+    // Loads still in flight when the next stage has landed: whole groups after it and, with unequal rings, the
+    // late operand's loads of its own group.
     static constexpr int S = SA < SB ? SA : SB;
     static constexpr int AHEAD = (S - 2) * (LA + LB) + (SA < SB ? LB : SB < SA ? LA : 0);
     static_assert((BM & (BM - 1)) == 0 && (BN & (BN - 1)) == 0, "transposed fragments address blocks by XOR");
-    static_assert(READ_STEP * (BM + BN) <= PRODUCTS && LOAD_STEP >= 1, "reads and loads fit between the products");
+    static_assert(READ_STEP * (BM + BN) <= PRODUCTS && STEP_A >= 1 && STEP_B >= 1, "reads and loads fit between the products");
     static_assert(S >= 2 && SA - SB <= 1 && SB - SA <= 1, "AHEAD counts one extra stage at most");
     static_assert(SA * LA + SB * LB - LA - LB < 64, "vmcnt is 6 bits");
     static_assert(LDS <= 160 * 1024, "gfx950 has 160 KiB of LDS");
@@ -577,21 +580,34 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
     };
     const uint32_t lds_a = lds_address(ring), lds_b = lds_address(ring_b);
 
-    // prologue: all slots on their way, the first stage landed and its first fragments read
+    // One operand's refill of a slot, spread over a half's products: i-th of them.
+    auto refill_a = [&](const typename PartA::At& t, int slot, int i) {
+        if (i % C::STEP_A == C::STEP_A - 1 && i / C::STEP_A < C::LA) pa.load(t, ring + slot * C::A_BYTES + wave * 1024, i / C::STEP_A);
+    };
+    auto refill_b = [&](const typename PartB::At& t, int slot, int i) {
+        if (i % C::STEP_B == C::STEP_B - 1 && i / C::STEP_B < C::LB) pb.load(t, ring_b + slot * C::B_BYTES + wave * 1024, i / C::STEP_B);
+    };
+
+    // prologue: all slots on their way but the late operand's last (the first stage's first half fills it), the first
+    // stage landed and its first fragments read
 #pragma unroll
     for (int q = 0; q < max(C::SA, C::SB); ++q) {
-        if (q < C::SA) {
+        if (q < C::SA - (C::LATE_A ? 1 : 0)) {
             const typename PartA::At la = take_a();
 #pragma unroll
             for (int j = 0; j < C::LA; ++j) pa.load(la, ring + q * C::A_BYTES + wave * 1024, j);
         }
-        if (q < C::SB) {
+        if (q < C::SB - (C::LATE_A ? 0 : 1)) {
             const typename PartB::At lb = take_b();
 #pragma unroll
             for (int j = 0; j < C::LB; ++j) pb.load(lb, ring_b + q * C::B_BYTES + wave * 1024, j);
         }
     }
-    wait_vmcnt<C::SA * C::LA + C::SB * C::LB - C::LA - C::LB>();
+    typename PartA::At la{};
+    typename PartB::At lb{};
+    if constexpr (C::LATE_A) la = take_a();
+    else lb = take_b();
+    wait_vmcnt<C::SA * C::LA + C::SB * C::LB - C::LA - C::LB - (C::LATE_A ? C::LA : C::LB)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     Piece w = piece_of(a, program, programs, 0);
@@ -603,6 +619,7 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
     __builtin_amdgcn_sched_barrier(0);
 
     int sa = 0, sb = 0;         // slots of the stage
+    int late = C::LATE_A ? C::SA - 1 : C::SB - 1;   // slot that the late operand fills next
     for (int q = 0; w.count > 0;) {
         const Piece next = piece_of(a, program, programs, q + 1);
         // whether the stage after the piece's last is a tile's last one too
@@ -622,9 +639,10 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
         // A stage is two halves of BM x BN products each.  Between the first half's products the second half's
         // fragments are read; then this wave's reads of the stage's slots are complete and the next stage has
         // landed, and one barrier makes both true for all waves.  Between the second half's products the next
-        // stage's first fragments are read and the two slots are refilled with stages SA and SB further on, one
-        // load every few products: a wave is held at a load until the CU takes it (about one 1 KiB instruction
-        // per 22 cycles per CU), so loads in a row would leave the matrix pipe idle.  The order is pinned by
+        // stage's first fragments are read.  The stage's two slots are refilled with stages SA and SB further on, one
+        // operand's between the second half's products, the other's between the next stage's first half's: a
+        // wave is held at a load until the CU takes it (about one 1 KiB instruction per 22 cycles per CU, 1408
+        // cycles for a 256 x 256 tile's stage of 2048), so they have to lie evenly.  The order is pinned by
         // scheduling barriers (scalar and address arithmetic may cross them); the fragment reads are
         // waited for as a whole before the half that uses them.
 #pragma unroll 1
@@ -635,11 +653,13 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
 #pragma unroll
             for (int i = 0; i < C::PRODUCTS; ++i) {
                 if (i % C::READ_STEP == 0 && i / C::READ_STEP < BM + BN) read(1, here_a, here_b, 1, i / C::READ_STEP);
+                if constexpr (C::LATE_A) refill_a(la, late, i);
+                else refill_b(lb, late, i);
                 mfma<BF16>(acc[i / BN][i % BN], fb[0][i % BN], fa[0][i / BN]);
                 __builtin_amdgcn_sched_barrier(0x6);
             }
-            const typename PartA::At la = take_a();
-            const typename PartB::At lb = take_b();
+            la = take_a();
+            lb = take_b();
             __builtin_amdgcn_sched_barrier(0);
             wait_lgkmcnt0();
             wait_vmcnt<C::AHEAD>();
@@ -649,17 +669,15 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
 #pragma unroll
             for (int i = 0; i < C::PRODUCTS; ++i) {
                 if (i % C::READ_STEP == 0 && i / C::READ_STEP < BM + BN) read(0, there_a, there_b, 0, i / C::READ_STEP);
-                if (i % C::LOAD_STEP == C::LOAD_STEP - 1 && i / C::LOAD_STEP < C::LA + C::LB) {
-                    const int j = C::SB < C::SA ? (i / C::LOAD_STEP + C::LA) % (C::LA + C::LB) : i / C::LOAD_STEP;   // B's first
-                    if (j < C::LA) pa.load(la, ring + sa * C::A_BYTES + wave * 1024, j);
-                    else pb.load(lb, ring_b + sb * C::B_BYTES + wave * 1024, j - C::LA);
-                }
+                if constexpr (C::LATE_A) refill_b(lb, sb, i);
+                else refill_a(la, sa, i);
                 mfma<BF16>(acc[i / BN][i % BN], fb[1][i % BN], fa[1][i / BN]);
                 __builtin_amdgcn_sched_barrier(0x6);
             }
             __builtin_amdgcn_sched_barrier(0);
             wait_lgkmcnt0();
             __builtin_amdgcn_sched_barrier(0);
+            late = C::LATE_A ? sa : sb;
             sa = next_a;
             sb = next_b;
         }
