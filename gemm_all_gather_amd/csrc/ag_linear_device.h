@@ -339,7 +339,7 @@ struct Part {
     }
 };
 
-// Fragments of NB 16-row (16-column) blocks for a 32-wide step of the stage.  Lane l receives row
+// Fragments of 16-row (16-column) blocks for a 32-wide step of the stage.  Lane l receives row
 // l & 15 of a block, r = 8 (l >> 4) .. + 7 of the step, from either layout.  The reads are inline assembly:
 // the compiler cannot tell them from the LDS-direct loads still landing in the other slot and would
 // wait for those; every read is followed by wait_lgkmcnt0() before its use.
@@ -845,6 +845,16 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_kernel(LinearGemmArg
     else bias_grad_body(db, p - dx_programs - dw_programs, reinterpret_cast<float*>(ring));
 }
 
+// Measured, with one launch's start, epilogue and join:
+//   256 x 256  16384 x 3584 x 8192 NT with gelu_tanh and z, bf16, 680 to 709 us, 1.36 to 1.41 PFLOP/s (a library product
+//              of the same operands without epilogue 753); its gradients NN 659 and TN 687.  The matrix pipe is
+//              busy 73% of the cycles at the 1.8 GHz that the card's power limit leaves (zero operands 17 to 20% faster).
+//   256 x 128  1024 x 8192 x 3584 NN (dx; 256 tiles) 58 us, 1.04 PFLOP/s.
+//   128 x 128  1024 x 3584 x 8192 NT with gelu and residual (224 tiles) 72 us, 0.84 PFLOP/s (the library 70 without
+//              either); without both, after a long warm-up, 60.  A stage takes 1060 cycles or more of 512 in the
+//              matrix pipe.  Not the fragments' latency holds it: reading them a stage before their use, with one
+//              stage less on its way, measured the same (34.8 and 35.0 us for 1024 x 4096 x 4096).  All three tiles draw
+//              12 to 15 TB/s from L2, which is what bounds the smaller two.
 // 256 x 256: a wave's 128 x 128 sub-tile keeps LDS reads (128 KiB a stage) and the rings' refill (64 KiB) below the
 // matrix pipe's 2048 cycles a stage at 128 bytes per cycle; its accumulators take 256 registers.
 // 256 x 128 (1152 LDS cycles against 1024) and 128 x 128 (768 against 512): for products with fewer tiles.

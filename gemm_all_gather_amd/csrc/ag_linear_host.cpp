@@ -468,8 +468,9 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         }
     }
     // Otherwise both in turn, where that saves a good part of a round: 1000 x 4100 x 4100, dw added up in fp32, 179
-    // us in launches of their own, 151 in turn.  (Long products are held by power: idle CUs at a round's end let
-    // the others run faster, and 16384 x 3584 x 8192 measured 1505 against 1501.)
+    // us in launches of their own, 151 in turn (127 since a stage's loads lie over both its halves).  Long products are
+    // held by power: idle CUs at a round's end let the others run faster, and 16384 x 3584 x 8192 measured 1505 in
+    // turn against 1501.
     if (b->px.on && b->pw.on && !b->together) {
         Product x = b->px, w = b->pw;
         whole_tiles(&x, ag::kLinearTile256);

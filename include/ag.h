@@ -486,9 +486,10 @@ ag_status_t ag_plan_gemm_all_gather_ex(const ag_heap_geometry_t* geom, int W, in
  * dtype     AG_F16 or AG_BF16, shared by all of them (AG_F32 -> AG_ERR_UNSUPPORTED)
  * M, N, K   any size from 0 (K = 0: y = act(bias) + residual)
  * ld*       row strides in elements; 0 = dense (K or N); any value >= the row
- * Pointers need only their element's alignment.  Operands of the product whose
- * rows are not 4-byte aligned are copied to the workspace first (M above 32);
- * rows of less than 2^20 elements apart (AG_ERR_UNSUPPORTED otherwise).
+ * Pointers need only their element's alignment.  Operands of a tiled product
+ * whose rows are not 4-byte aligned are copied to the workspace first (the
+ * plan's `packed`; few rows of x need no tiles and no copy).  Row strides are
+ * at most 2^20 elements (AG_ERR_UNSUPPORTED otherwise).
  * Outputs must not overlap inputs or each other (but y and residual, above).
  * What lies between a matrix's rows (ld > row) is never written and never has
  * an effect; nothing is read before a matrix's first element or after the
@@ -640,8 +641,8 @@ ag_status_t ag_adamw_destroy(ag_adamw_t* optimizer);
 typedef struct ag_adamw_hyper {
     double lr, beta1, beta2, eps, weight_decay, grad_scale;
     int64_t step;                 /* >= 1: the number of this step */
-    const int64_t* dev_step;      /* optional device scalars, read by the kernel instead of the host's value: */
-    const float* dev_lr;          /*   a captured graph's step then follows them from replay to replay */
+    const int64_t* dev_step;      /* optional device scalars, read by the kernel instead of the host's value (a */
+    const float* dev_lr;          /*   step >= 1): a captured graph's step then follows them from replay to replay */
     const float* dev_grad_scale;  /*   (multiplied with grad_scale: a clipping factor) */
     uint64_t seed;                /* stochastic rounding's seed: another one for every step */
     int32_t stochastic;           /* 1: stochastic rounding of 8-bit states, seed + *dev_step where there is one */
