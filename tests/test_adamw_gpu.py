@@ -214,6 +214,23 @@ def test_adamw_8bit_nothing_live_meets_a_zero_denominator():
     assert (t.f64("v", 0) >= 1).all()
 
 
+@pytest.mark.parametrize("eps", [1e-8, 1e-12, 9e-13, 1e-20])
+@pytest.mark.parametrize("state", [32, 8])
+def test_adamw_tiny_gradients_and_eps(state, eps):
+    """Second moments from 1e-36 (normal in fp32) to 1e-30, whose roots lie far below the larger eps and far above the smallest."""
+    require_gpu()
+    t = Tensors([1000, 9], "f32", "f32", state, False)
+    g = np.random.default_rng(5)
+    for step in (1, 2):
+        for x in t.parts["g"]:
+            n = x.numel()
+            x.copy_(torch.from_numpy(g.choice([-1.0, 1.0], n) * 10.0 ** g.uniform(-17, -14, n)))
+        before = t.before()
+        log(f"adamw tiny gradients, state {state} eps {eps} step {step}")
+        t.optimizer.step(step, 1e-2, 0.9, 0.99, eps, 0.1)
+        t.check(before, step, f"adamw tiny gradients, state {state} eps {eps} step {step}", eps=eps)
+
+
 def test_adamw_non_finite_gradients():
     """A NaN or an infinity reaches its own parameter, and its whole block of an 8-bit state; nothing else."""
     require_gpu()
