@@ -20,6 +20,15 @@ struct LinearEpilogue {
     int32_t reserved;
 };
 
+// db(n) (+)= sum over parts of sums(part, n).
+struct LinearBiasGradArgs {
+    const float* sums;
+    void* db;
+    int64_t parts, N;
+    int32_t kind;               // of db: 0 f16, 1 bf16, 2 f32
+    int32_t accumulate;
+};
+
 // out(i, j) = epilogue(sum_r A(i, r) B(j, r)).
 struct LinearGemmArgs {
     const uint16_t* A;          // element (i, r) at A[i*lda + r], or A[r*lda + i] (transposed kernels)
@@ -35,6 +44,7 @@ struct LinearGemmArgs {
     int32_t common_rounds;      //   number `heavy` on
     float* partial;             // fp32 tile (part, tail tile)
     LinearEpilogue epi;
+    LinearBiasGradArgs db;      // gradient kernels: the bias gradient's sum on the side (db.db null: none)
 };
 
 enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1, kLinearTile256x128 = 2, kLinearTiles = 3 };
@@ -78,14 +88,6 @@ struct LinearSlopeArgs {
     int32_t rows;               // of one workgroup and partial column sum
 };
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
-// db(n) (+)= sum over parts of sums(part, n).
-struct LinearBiasGradArgs {
-    const float* sums;
-    void* db;
-    int64_t parts, N;
-    int32_t kind;               // of db: 0 f16, 1 bf16, 2 f32
-    int32_t accumulate;
-};
 hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream);
 
 using LinearInTurnFn = void (*)(LinearGemmArgs, LinearGemmArgs, LinearBiasGradArgs);

@@ -773,13 +773,6 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
     wait_vmcnt<0>();   // loads past the last stage write LDS: they end with the workgroup
 }
 
-template <bool BF16, int FORM, int ACT, class C>
-__global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
-{
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
-    gemm_body<BF16, FORM, ACT, C>(a, blockIdx.x, gridDim.x, ring);
-}
-
 // Sums the partial column sums of 32 columns: 8 row lanes, then a fixed order through LDS (8 x 33 floats).
 __device__ __forceinline__ void bias_grad_body(const LinearBiasGradArgs& a, int block, float* part)
 {
@@ -807,6 +800,25 @@ __device__ __forceinline__ void bias_grad_body(const LinearBiasGradArgs& a, int 
     }
 }
 
+// The bias gradient's column groups after a product's tiles, on the workgroups with the fewest tiles first: a launch of
+// its own takes 4 to 5 us (and a gap) for 1.5 us of work.
+__device__ __forceinline__ void bias_grads_after(const LinearBiasGradArgs& db, int program, int programs, uint8_t* ring)
+{
+    if (!db.db) return;
+    for (int block = programs - 1 - program; block < (db.N + 31) / 32; block += programs) {
+        __syncthreads();
+        bias_grad_body(db, block, reinterpret_cast<float*>(ring));
+    }
+}
+
+template <bool BF16, int FORM, int ACT, class C>
+__global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
+    gemm_body<BF16, FORM, ACT, C>(a, blockIdx.x, gridDim.x, ring);
+    if constexpr (FORM != kFormNT) bias_grads_after(a.db, blockIdx.x, gridDim.x, ring);
+}
+
 // dx, dw and the bias gradient's sum one after the other on every workgroup: the product with the longer tiles first,
 // and those workgroups that have fewer of its tiles take more of the other's.  Two launches round up to
 // whole rounds twice (dw 3584 x 8192 of 16384 rows: 448 tiles on 256 CUs, 1.75 rounds).
@@ -824,12 +836,7 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_in_turn_kernel(Linea
         __syncthreads();
         gemm_body<BF16, kFormNN, AG_ACT_NONE, C>(dx, p, n, ring);
     }
-    if (db.db) {
-        for (int block = p; block < (db.N + 31) / 32; block += n) {
-            __syncthreads();
-            bias_grad_body(db, block, reinterpret_cast<float*>(ring));
-        }
-    }
+    bias_grads_after(db, p, n, ring);
 }
 
 // dx, dw and the bias gradient's sum in one launch, for layers whose tiles together leave CUs free: workgroups

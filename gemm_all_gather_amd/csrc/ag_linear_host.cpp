@@ -379,6 +379,7 @@ struct Backward {
     bool slope = false, store_dz = false;
     bool together = false;      // dx, dw and db in one launch, side by side
     bool in_turn = false, dx_first = false;   // or one after the other
+    bool db_alone = false;      // db in a launch of its own; else beside a product
     uint64_t dz_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
     int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
@@ -478,7 +479,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         if (x.full_tiles <= 0x7fffff && w.full_tiles <= 0x7fffff) {
             const bool dx_first = x.us >= w.us;
             const double us = dx_first ? in_turn(x, &w, cus) : in_turn(w, &x, cus);
-            const double apart = b->px.us + b->pw.us + 4.0 * ((want_db ? 1 : 0) + b->px.launches() + b->pw.launches() - 1);
+            const double apart = b->px.us + b->pw.us + (want_db ? 2.0 : 0.0) + 4.0 * (b->px.launches() + b->pw.launches() - 1);
             if (us < 0.87 * apart) {
                 b->in_turn = true;
                 b->dx_first = dx_first;
@@ -490,7 +491,8 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
     }
     b->partial_offset = used;
     b->workspace = used + std::max(b->px.partial_bytes, b->pw.partial_bytes);
-    b->launches = (b->slope ? 1 : 0) + (b->together || b->in_turn ? 1 : (want_db ? 1 : 0) + b->px.launches() + b->pw.launches()) +
+    b->db_alone = want_db && !b->px.on && !b->pw.on;
+    b->launches = (b->slope ? 1 : 0) + (b->together || b->in_turn ? 1 : (b->db_alone ? 1 : 0) + b->px.launches() + b->pw.launches()) +
                   (b->ow.pack ? 1 : 0) + (b->ox.pack ? 1 : 0);
     return AG_OK;
 }
@@ -670,10 +672,11 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         const hipError_t e = ag::launch_linear_grads_in_turn(dx, dw, b.dx_first, static_cast<int>(b.px.programs), db, bf16, stream);
         return e == hipSuccess ? ok() : fail_hip(e, "linear gradients");
     }
-    if (want_db) {
+    if (b.db_alone) {
         const hipError_t e = ag::launch_linear_bias_grad(db, stream);
         if (e != hipSuccess) return fail_hip(e, "linear bias gradient");
     }
+    (b.pw.on ? dw : dx).db = db;    // beside the product that comes last
     if (b.px.on && (s = run_product(b.px, dx, bf16, stream)) != AG_OK) return s;
     if (b.pw.on && (s = run_product(b.pw, dw, bf16, stream)) != AG_OK) return s;
     return ok();
