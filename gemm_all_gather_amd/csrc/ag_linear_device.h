@@ -801,7 +801,7 @@ __device__ __forceinline__ void bias_grad_body(const LinearBiasGradArgs& a, int 
 }
 
 // The bias gradient's column groups after a product's tiles, on the workgroups with the fewest tiles first: a launch of
-// its own takes 4 to 5 us (and a gap) for 1.5 us of work.
+// its own takes 4 to 5 us and a gap (all gradients of 1024 x 3584 x 8192 with it 132 to 137 us, so 126).
 __device__ __forceinline__ void bias_grads_after(const LinearBiasGradArgs& db, int program, int programs, uint8_t* ring)
 {
     if (!db.db) return;
