@@ -76,11 +76,12 @@ hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, int cus, hi
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
                               int64_t cols, hipStream_t stream);
 
-// dz = dy * act'(z), rounded, and the column sums of the unrounded dz over row blocks.
+// dz = dy * act'(z), rounded, what the rounding leaves, and the column sums of the unrounded dz over row blocks.
 struct LinearSlopeArgs {
     const uint16_t* dy;
     const uint16_t* z;          // null when act is none
     uint16_t* dz;               // null: not stored
+    uint16_t* dz_rest;          // dz's second term, dz - (its rounded value), rounded; or null
     float* sums;                // ceil(M / rows) rows of N, or null
     int64_t lddy, ldz, lddz;
     int64_t M, N;

@@ -214,6 +214,15 @@ __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
                 apply_slope(v, z, a.act);
             }
             if (a.dz) store_16<BF16>(a.dz + row * a.lddz + col, v, n);
+            if (a.dz_rest) {
+                float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float kept = to_f32<BF16>(from_f32<BF16>(v[e]));
+                    rest[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
+                }
+                store_16<BF16>(a.dz_rest + row * a.lddz + col, rest, n);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += v[e];
         }

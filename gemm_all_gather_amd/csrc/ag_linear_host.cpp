@@ -375,12 +375,13 @@ ag_status_t plan_forward(const ag_linear_args_t* a, int cus, Forward* f)
 struct Backward {
     Mat dy, z, x, w, dx, dw, db;
     Product px, pw;
-    Operand ox, ow, odz;
+    Product rest;               // dw of dz's second term, before pw
+    Operand ox, ow;
     bool slope = false, store_dz = false;
     bool together = false;      // dx, dw and db in one launch, side by side
     bool in_turn = false, dx_first = false;   // or one after the other
     bool db_alone = false;      // db in a launch of its own; else beside a product
-    uint64_t dz_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
+    uint64_t dz_offset = 0, dz_rest_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
     int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
 };
@@ -429,6 +430,16 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         b->dz_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
     }
+    // A weight gradient in fp32 takes dz in two 16-bit terms and so two products: with one it would carry the error
+    // of a 16-bit gradient (2-norm relative to dw's 1.7e-3 in bf16, 2.1e-4 in fp16; with two 2.5e-6 and 3.5e-7, as
+    // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 us against 1468 of a
+    // bf16 dw, of 1024 rows 236 against 125.  dx and a 16-bit dw take one term: their own rounding is as large (2.3e-3
+    // in all against 1.7e-3), and two would double the time of both products.  relu's dz needs no rounding.
+    const bool two_terms = b->store_dz && want_dw && act && a->act != AG_ACT_RELU && a->dw_dtype == AG_F32;
+    if (two_terms) {
+        b->dz_rest_offset = used;
+        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
+    }
     if (want_db) {
         b->parts = (M + b->rows - 1) / b->rows;
         b->sums_offset = used;
@@ -455,6 +466,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         if ((s = choose(&b->pw, cus)) != AG_OK) return s;
         b->ox = Operand{b->x.at, b->x.ld, M, K};
         place(&b->ox, &used);
+        if (two_terms) b->rest = b->pw;
     }
     // Both products' 128 x 128 tiles on CUs of their own: one launch for what follows dz.
     if (b->px.on && b->pw.on) {
@@ -490,10 +502,10 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         }
     }
     b->partial_offset = used;
-    b->workspace = used + std::max(b->px.partial_bytes, b->pw.partial_bytes);
+    b->workspace = used + std::max({b->px.partial_bytes, b->pw.partial_bytes, b->rest.partial_bytes});
     b->db_alone = want_db && !b->px.on && !b->pw.on;
     b->launches = (b->slope ? 1 : 0) + (b->together || b->in_turn ? 1 : (b->db_alone ? 1 : 0) + b->px.launches() + b->pw.launches()) +
-                  (b->ow.pack ? 1 : 0) + (b->ox.pack ? 1 : 0);
+                  b->rest.launches() + (b->ow.pack ? 1 : 0) + (b->ox.pack ? 1 : 0);
     return AG_OK;
 }
 
@@ -618,6 +630,7 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         a.dy = static_cast<const uint16_t*>(args->dy);
         a.z = args->act != AG_ACT_NONE ? static_cast<const uint16_t*>(args->z) : nullptr;
         a.dz = b.store_dz ? reinterpret_cast<uint16_t*>(ws + b.dz_offset) : nullptr;
+        a.dz_rest = b.rest.on ? reinterpret_cast<uint16_t*>(ws + b.dz_rest_offset) : nullptr;
         a.sums = want_db ? sums : nullptr;
         a.lddy = b.dy.ld;
         a.ldz = b.z.ld;
@@ -661,6 +674,11 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         e.ldo = b.dw.ld;
         e.out_f32 = args->dw_dtype == AG_F32;
         e.accumulate = args->accumulate;
+        if (b.rest.on) {    // the small term first, on the earlier gradient if there is one; the other adds to it
+            const uint16_t* dz_rest = reinterpret_cast<const uint16_t*>(ws + b.dz_rest_offset);
+            if ((s = run_product(b.rest, gemm_args(b.rest, dz_rest, lddz, X, ldx, e, partial), bf16, stream)) != AG_OK) return s;
+            e.accumulate = 1;
+        }
         dw = gemm_args(b.pw, dz, lddz, X, ldx, e, partial);
     }
     if (b.together) {

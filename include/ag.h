@@ -560,7 +560,9 @@ ag_status_t ag_plan_linear(const ag_linear_args_t* args, int num_cus, ag_linear_
  * (the residual's gradient is dy itself).  Sums are fp32; dx has the
  * operands' dtype, dw and db have dw_dtype: the operands' dtype or AG_F32.
  * With an activation, dz is rounded once to dtype, the type its products'
- * matrix instructions take; db sums the unrounded dz.  z is the pre-activation
+ * matrix instructions take, for dx and for a dw of that type; a dw in AG_F32
+ * takes dz in two terms of dtype (the rounded one and what it leaves, rounded)
+ * and so two products.  db sums the unrounded dz.  z is the pre-activation
  * that ag_linear stored; it may be NULL when act is AG_ACT_NONE.  dx, dw and
  * db may each be NULL (not computed); accumulate adds to dw and db in fp32
  * before the one rounding.  x is read only for dw, w only for dx; either may
