@@ -504,39 +504,40 @@ def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=No
 class AdamW:
     """ag_adamw: a device table of tensors, made once; ``step`` updates all of them in one launch.
 
-    Lists of device tensors of equal lengths, each contiguous; 8-bit states are int8 and uint8 tensors with their
-    fp32 block maxima in exp_avg_scales and exp_avg_sq_scales.  The tensors are kept alive here and must keep
-    their addresses (clear gradients in place).
+    Lists (or other iterables) of device tensors, equally many, each contiguous; 8-bit states are int8 and uint8
+    tensors with their fp32 block maxima in exp_avg_scales and exp_avg_sq_scales.  The tensors are kept alive here,
+    whatever becomes of the lists, and must keep their addresses (clear gradients in place).
     """
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, masters=None, exp_avg_scales=None,
                  exp_avg_sq_scales=None):
         import torch
-        lists = [params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, masters]
-        params = list(params)
+        # tuples of the tensors: the caller's lists may change while the device table holds these addresses
+        parts = [part if part is None else tuple(part) for part in
+                 (params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, masters)]
+        params, grads, exp_avgs = parts[:3]
         count = len(params)
+        if any(part is not None and len(part) != count for part in parts):
+            raise ValueError("the lists of tensors differ in length")
         state8 = count > 0 and exp_avgs[0].dtype == torch.int8
         wanted = [None, None, torch.int8 if state8 else torch.float32, torch.uint8 if state8 else torch.float32,
                   torch.float32, torch.float32, torch.float32]
-        for part, dtype in zip(lists, wanted):
+        for i, (part, dtype) in enumerate(zip(parts, wanted)):
             if part is None:
                 continue
-            if len(part) != count:
-                raise ValueError("the lists of tensors differ in length")
             for t, p in zip(part, params):
-                need = -(-p.numel() // AG_ADAMW_BLOCK) if part is exp_avg_scales or part is exp_avg_sq_scales \
-                    else p.numel()
+                need = -(-p.numel() // AG_ADAMW_BLOCK) if i in (4, 5) else p.numel()     # block maxima
                 if not t.is_contiguous() or t.numel() != need or t.dtype != (dtype or part[0].dtype):
                     raise ValueError(f"a tensor is not contiguous, not of {need} elements or not {dtype or part[0].dtype}")
         table = (AdamwTensor * max(1, count))()
         for i, p in enumerate(params):
-            table[i] = AdamwTensor(*(_ptr(part[i]) if part is not None else 0 for part in lists), p.numel())
+            table[i] = AdamwTensor(*(_ptr(part[i]) if part is not None else 0 for part in parts), p.numel())
         h = ctypes.c_void_p()
         _check(lib().ag_adamw_create(table, count, _dtype(params[0].dtype) if count else AG_F32,
                                      _dtype(grads[0].dtype) if count else AG_F32, 8 if state8 else 32,
                                      ctypes.byref(h)), "ag_adamw_create")
         self._h = h
-        self._keepalive = lists
+        self._keepalive = parts
         self._count = count
 
     def destroy(self) -> None:
