@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from operator import attrgetter
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -538,7 +539,7 @@ class AdamW:
                                      ctypes.byref(h)), "ag_adamw_create")
         self._h = h
         self._keepalive = parts
-        self._count = count
+        self._sizes = [p.numel() for p in params]
 
     def destroy(self) -> None:
         if self._h is not None and self._h.value:
@@ -568,9 +569,23 @@ class AdamW:
                        _ptr(dev_grad_scale), 0 if seed is None else seed, 0 if seed is None else 1)
         _check(lib().ag_adamw_step(self.handle, ctypes.byref(y), _stream(stream)), "ag_adamw_step")
 
-    def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:
-        """The fp32 values of 8-bit states, into two lists of fp32 tensors (ag_adamw_read_states)."""
-        m, v = ((_vp * max(1, self._count))(*(_ptr(t) for t in part)) for part in (exp_avgs, exp_avg_sqs))
-        if len(exp_avgs) != self._count or len(exp_avg_sqs) != self._count:
+    def _outputs(self, part):
+        """The addresses of one fp32 output per tensor, each checked (by whole lists: there may be hundreds a call)."""
+        import torch
+        if len(part) != len(self._sizes):
             raise ValueError("the lists of tensors differ in length")
+        tensors, sizes = part, self._sizes
+        if int in set(map(type, part)):     # addresses among them
+            which = [i for i, t in enumerate(part) if not isinstance(t, int)]
+            tensors, sizes = [part[i] for i in which], [sizes[i] for i in which]
+        T = torch.Tensor
+        if (list(map(T.numel, tensors)) != sizes or not all(map(T.is_contiguous, tensors)) or
+                set(map(attrgetter("dtype"), tensors)) - {torch.float32}):
+            raise ValueError("an output is not contiguous, not of its parameter's elements or not fp32")
+        return (_vp * max(1, len(part)))(*map(T.data_ptr if tensors is part else _ptr, part))
+
+    def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:
+        """The fp32 values of 8-bit states, into two lists of fp32 tensors, contiguous and of each parameter's
+        elements (or device addresses of as many floats) (ag_adamw_read_states)."""
+        m, v = (self._outputs(tuple(part)) for part in (exp_avgs, exp_avg_sqs))
         _check(lib().ag_adamw_read_states(self.handle, m, v, _stream(stream)), "ag_adamw_read_states")

@@ -17,7 +17,7 @@ class Recorder:
         self.table, self.steps, self.reads = [], [], []
 
     def ag_adamw_create(self, table, count, param, grad, bits, out):
-        self.table = [table[i].param for i in range(count)]
+        self.table = [table[i].param or 0 for i in range(count)]
         ctypes.cast(out, ctypes.POINTER(ctypes.c_void_p))[0] = 1 << 40
         return ag.AG_OK
 
@@ -27,31 +27,15 @@ class Recorder:
         return ag.AG_OK
 
     def ag_adamw_read_states(self, handle, m, v, stream):
-        self.reads.append((list(m), list(v)))
+        self.reads.append(tuple([p or 0 for p in part] for part in (m, v)))      # ctypes gives None for 0
         return ag.AG_OK
 
     def ag_adamw_destroy(self, handle):
         return ag.AG_OK
 
 
-class DeviceTensor:
-    """What the handle asks of a tensor in device memory."""
-
-    is_cuda, device = True, torch.device("cuda", 0)
-    made = 0
-
-    def __init__(self, n, dtype=torch.float32, contiguous=True):
-        DeviceTensor.made += 1
-        self.n, self.dtype, self.contiguous, self.at = n, dtype, contiguous, (1 << 44) + (DeviceTensor.made << 30)
-
-    def numel(self):
-        return self.n
-
-    def is_contiguous(self):
-        return self.contiguous
-
-    def data_ptr(self):
-        return self.at
+def tensor(n, dtype=torch.float32):
+    return torch.zeros(n, dtype=dtype)
 
 
 @pytest.fixture
@@ -66,13 +50,13 @@ SIZES = [5, 300, 0, 256]
 
 
 def lists(state8=False, param=torch.bfloat16, master=False):
-    d = {"params": [DeviceTensor(n, param) for n in SIZES], "grads": [DeviceTensor(n, param) for n in SIZES],
-         "exp_avgs": [DeviceTensor(n, torch.int8 if state8 else torch.float32) for n in SIZES],
-         "exp_avg_sqs": [DeviceTensor(n, torch.uint8 if state8 else torch.float32) for n in SIZES]}
+    d = {"params": [tensor(n, param) for n in SIZES], "grads": [tensor(n, param) for n in SIZES],
+         "exp_avgs": [tensor(n, torch.int8 if state8 else torch.float32) for n in SIZES],
+         "exp_avg_sqs": [tensor(n, torch.uint8 if state8 else torch.float32) for n in SIZES]}
     if master:
-        d["masters"] = [DeviceTensor(n) for n in SIZES]
+        d["masters"] = [tensor(n) for n in SIZES]
     if state8:
-        d["exp_avg_scales"], d["exp_avg_sq_scales"] = ([DeviceTensor(-(-n // 256)) for n in SIZES] for _ in range(2))
+        d["exp_avg_scales"], d["exp_avg_sq_scales"] = ([tensor(-(-n // 256)) for n in SIZES] for _ in range(2))
     return d
 
 
@@ -95,7 +79,7 @@ def test_tensors_outlive_the_callers_lists(library):
 def test_lists_may_be_any_iterables(library):
     d = lists(True, master=True)
     opt = ag.AdamW(**{k: iter(part) for k, part in d.items()})
-    assert library.table == [t.at for t in d["params"]]
+    assert library.table == [t.data_ptr() for t in d["params"]]
     opt.destroy()
 
 
@@ -108,3 +92,45 @@ def test_lists_of_other_lengths_are_refused(library):
         d[k] = []
         with pytest.raises(ValueError):
             ag.AdamW(**d)
+
+
+# ------------------------------------------------------------------ outputs of read_states
+
+def outputs():
+    return [[tensor(n) for n in SIZES] for _ in range(2)]
+
+
+def test_read_states_takes_whole_contiguous_fp32_outputs(library):
+    opt = ag.AdamW(**lists(True))
+    m, v = outputs()
+    opt.read_states(m, iter(v))
+    assert library.reads == [([t.data_ptr() for t in m], [t.data_ptr() for t in v])]
+    addresses = [[t.data_ptr() for t in part] for part in (m, v)]        # addresses go through as they are
+    opt.read_states(*addresses)
+    assert library.reads[1] == library.reads[0]
+    opt.destroy()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("bad", [lambda: tensor(299), lambda: tensor(301), lambda: tensor(300, torch.float16),
+                                 lambda: tensor(300, torch.float64), lambda: tensor(600)[::2]])
+def test_read_states_refuses_outputs_it_would_write_past(library, bad, which):
+    opt = ag.AdamW(**lists(True))
+    out = outputs()
+    out[which][1] = bad()
+    with pytest.raises(ValueError):
+        opt.read_states(*out)
+    assert not library.reads
+    opt.destroy()
+
+
+def test_read_states_refuses_lists_of_other_lengths(library):
+    opt = ag.AdamW(**lists(True))
+    for k in (0, 1):
+        for change in (lambda t: t[:-1], lambda t: t + [tensor(1)], lambda t: []):
+            out = outputs()
+            out[k] = change(out[k])
+            with pytest.raises(ValueError):
+                opt.read_states(*out)
+    assert not library.reads
+    opt.destroy()
