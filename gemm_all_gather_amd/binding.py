@@ -502,6 +502,16 @@ def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=No
     _check(lib().ag_linear_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_backward")
 
 
+def _scalar(x, name, dtype) -> int:
+    """Address of a device scalar: None, an address, or a tensor whose first element the kernel reads."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    import torch
+    if x.dtype != getattr(torch, dtype) or x.numel() < 1:
+        raise ValueError(f"{name} is not a tensor of one {dtype}")
+    return int(x.data_ptr())
+
+
 class AdamW:
     """ag_adamw: a device table of tensors, made once; ``step`` updates all of them in one launch.
 
@@ -564,9 +574,13 @@ class AdamW:
 
     def step(self, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0, seed=None,
              dev_step=None, dev_lr=None, dev_grad_scale=None, stream=None) -> None:
-        """One AdamW step; a seed (8-bit states) turns stochastic rounding on (ag_adamw_step)."""
-        y = AdamwHyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step, _ptr(dev_step), _ptr(dev_lr),
-                       _ptr(dev_grad_scale), 0 if seed is None else seed, 0 if seed is None else 1)
+        """One AdamW step; a seed (8-bit states) turns stochastic rounding on (ag_adamw_step).
+
+        dev_step (int64), dev_lr and dev_grad_scale (fp32) are one-element device tensors or device addresses.
+        """
+        y = AdamwHyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step, _scalar(dev_step, "dev_step", "int64"),
+                       _scalar(dev_lr, "dev_lr", "float32"), _scalar(dev_grad_scale, "dev_grad_scale", "float32"),
+                       0 if seed is None else seed, 0 if seed is None else 1)
         _check(lib().ag_adamw_step(self.handle, ctypes.byref(y), _stream(stream)), "ag_adamw_step")
 
     def _outputs(self, part):

@@ -134,3 +134,29 @@ def test_read_states_refuses_lists_of_other_lengths(library):
                 opt.read_states(*out)
     assert not library.reads
     opt.destroy()
+
+
+# ------------------------------------------------------------------ device scalars of a step
+
+def test_step_takes_device_scalars_of_their_types(library):
+    opt = ag.AdamW(**lists())
+    step, lr, scale = torch.ones(1, dtype=torch.int64), torch.ones(()), torch.ones(3)[1:2]
+    opt.step(1, 1e-3, dev_step=step, dev_lr=lr, dev_grad_scale=scale)
+    opt.step(1, 1e-3, dev_step=1 << 44, dev_lr=2 << 44)                  # addresses go through as they are
+    opt.step(1, 1e-3)
+    assert library.steps == [(step.data_ptr(), lr.data_ptr(), scale.data_ptr()), (1 << 44, 2 << 44, None), (None, None, None)]
+    opt.destroy()
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("dev_step", torch.ones(1, dtype=torch.int32)), ("dev_step", torch.ones(1)), ("dev_step", torch.ones(0, dtype=torch.int64)),
+    ("dev_lr", torch.ones(1, dtype=torch.float64)), ("dev_lr", torch.ones(1, dtype=torch.bfloat16)), ("dev_lr", torch.ones(0)),
+    ("dev_grad_scale", torch.ones(1, dtype=torch.float64)), ("dev_grad_scale", torch.ones(1, dtype=torch.int64)),
+    ("dev_grad_scale", torch.ones(0)),
+])
+def test_step_refuses_device_scalars_it_would_misread(library, name, bad):
+    opt = ag.AdamW(**lists())
+    with pytest.raises(ValueError, match=name):
+        opt.step(1, 1e-3, **{name: bad})
+    assert not library.steps
+    opt.destroy()
