@@ -502,6 +502,13 @@ def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=No
     _check(lib().ag_linear_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_backward")
 
 
+def _reachable(tensors) -> bool:
+    """Whether kernels can reach the tensors' elements: device memory, or pinned host memory."""
+    import torch
+    return min(map(torch.Tensor.get_device, tensors), default=0) >= 0 or \
+        all(t.is_cuda or t.numel() == 0 or t.is_pinned() for t in tensors)
+
+
 def _scalar(x, name, dtype) -> int:
     """Address of a device scalar: None, an address, or a tensor whose first element the kernel reads."""
     if x is None or isinstance(x, int):
@@ -509,6 +516,8 @@ def _scalar(x, name, dtype) -> int:
     import torch
     if x.dtype != getattr(torch, dtype) or x.numel() < 1:
         raise ValueError(f"{name} is not a tensor of one {dtype}")
+    if not _reachable([x]):
+        raise ValueError(f"{name} lies in host memory that is not pinned")
     return int(x.data_ptr())
 
 
@@ -540,6 +549,8 @@ class AdamW:
                 need = -(-p.numel() // AG_ADAMW_BLOCK) if i in (4, 5) else p.numel()     # block maxima
                 if not t.is_contiguous() or t.numel() != need or t.dtype != (dtype or part[0].dtype):
                     raise ValueError(f"a tensor is not contiguous, not of {need} elements or not {dtype or part[0].dtype}")
+            if not _reachable(part):
+                raise ValueError("a tensor lies in host memory that is not pinned")
         table = (AdamwTensor * max(1, count))()
         for i, p in enumerate(params):
             table[i] = AdamwTensor(*(_ptr(part[i]) if part is not None else 0 for part in parts), p.numel())
@@ -596,6 +607,8 @@ class AdamW:
         if (list(map(T.numel, tensors)) != sizes or not all(map(T.is_contiguous, tensors)) or
                 set(map(attrgetter("dtype"), tensors)) - {torch.float32}):
             raise ValueError("an output is not contiguous, not of its parameter's elements or not fp32")
+        if not _reachable(tensors):
+            raise ValueError("an output lies in host memory that is not pinned")
         return (_vp * max(1, len(part)))(*map(T.data_ptr if tensors is part else _ptr, part))
 
     def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:

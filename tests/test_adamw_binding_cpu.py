@@ -41,6 +41,7 @@ def tensor(n, dtype=torch.float32):
 @pytest.fixture
 def library(monkeypatch):
     r = Recorder()
+    monkeypatch.setattr(ag, "_reachable", lambda tensors: True, raising=False)      # its tensors lie in host memory here
     monkeypatch.setattr(ag, "lib", lambda: r)
     monkeypatch.setattr(ag, "_lib", r)
     return r
@@ -160,3 +161,45 @@ def test_step_refuses_device_scalars_it_would_misread(library, name, bad):
         opt.step(1, 1e-3, **{name: bad})
     assert not library.steps
     opt.destroy()
+
+
+# ------------------------------------------------------------------ memory that kernels cannot reach
+
+@pytest.fixture
+def strict(library, monkeypatch):
+    monkeypatch.undo()                      # the real check of where tensors lie
+    r = Recorder()
+    monkeypatch.setattr(ag, "lib", lambda: r)
+    monkeypatch.setattr(ag, "_lib", r)
+    return r
+
+
+def test_tensors_in_pageable_host_memory_are_refused(strict):
+    with pytest.raises(ValueError, match="host memory"):
+        ag.AdamW(**lists(True, master=True))
+    assert not strict.table
+    # tensors without elements have no memory to reach
+    opt = ag.AdamW(*([torch.zeros(0)] for _ in range(4)))
+    with pytest.raises(ValueError, match="host memory"):
+        opt.step(1, 1e-3, dev_lr=torch.ones(1))
+    assert not strict.steps
+    opt.destroy()
+
+
+def test_read_states_refuses_host_outputs(library, monkeypatch):
+    opt = ag.AdamW(**lists(True))
+    monkeypatch.setattr(ag, "_reachable", lambda tensors: False)
+    with pytest.raises(ValueError, match="host memory"):
+        opt.read_states(*outputs())
+    assert not library.reads
+    opt.destroy()
+
+
+def test_reachable_memory():
+    class Pinned(torch.Tensor):
+        def is_pinned(self):
+            return True
+
+    host, pinned = torch.zeros(3), torch.zeros(3).as_subclass(Pinned)
+    assert ag._reachable([]) and ag._reachable([torch.zeros(0)]) and ag._reachable([pinned])
+    assert not ag._reachable([host]) and not ag._reachable([pinned, host]) and not ag._reachable([torch.zeros(3, device="meta")])
