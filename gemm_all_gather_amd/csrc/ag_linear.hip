@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256) void ag_linear_pack_kernel(const uint16_t* src
 // 256 columns.  One pass over dy and z, bound by HBM: 16384 x 3584, gelu_tanh (352 MB): 69 us, 5.1 TB/s, a copy's
 // rate.  A kernel of its own because dz is an operand of both products; in their loads the slope would be computed
 // once per tile row and column (14 and 32 times), and they take operands to LDS without passing registers.
-template <bool BF16>
+template <bool BF16, bool REST>
 __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
 {
     __shared__ float part[8][264];
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
                 apply_slope(v, z, a.act);
             }
             if (a.dz) store_16<BF16>(a.dz + row * a.lddz + col, v, n);
-            if (a.dz_rest) {
+            if constexpr (REST) {
                 float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -326,7 +326,9 @@ hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t s
 {
     dim3 grid;
     if (a.rows < 1 || !grid_of((a.N + 255) / 256 * ((a.M + a.rows - 1) / a.rows), 1, &grid)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(bf16 ? ag_linear_slope_kernel<true> : ag_linear_slope_kernel<false>, grid, dim3(256), 0, stream, a);
+    auto fn = a.dz_rest ? (bf16 ? ag_linear_slope_kernel<true, true> : ag_linear_slope_kernel<false, true>)
+                        : (bf16 ? ag_linear_slope_kernel<true, false> : ag_linear_slope_kernel<false, false>);
+    hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
