@@ -145,10 +145,10 @@ __device__ __forceinline__ void apply_slope(float (&v)[8], const float (&z)[8], 
     case AG_ACT_GELU_TANH:   // with s = sigmoid(2u): s + z s (1 - s) 2u'
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float s = sigmoid(2.f * kGeluK * z[e] * (1.f + kGeluC * z[e] * z[e]));
-            // s (1 - s) is 0 from |z| of 10 or so on; the factors beside it stay finite (z^2 overflows at 1.8e19)
-            const float c = fminf(fmaxf(z[e], -32.f), 32.f), cc = c * c;
-            v[e] *= s + c * s * (1.f - s) * (2.f * kGeluK * (1.f + 3.f * kGeluC * cc));
+            // z^2 overflows from |z| = 1.8e19 on, where s (1 - s) is 0: the factor beside it has to stay finite
+            const float zz = fminf(z[e] * z[e], 1e30f);
+            const float s = sigmoid(2.f * kGeluK * z[e] * (1.f + kGeluC * zz));
+            v[e] *= s + z[e] * s * (1.f - s) * (2.f * kGeluK * (1.f + 3.f * kGeluC * zz));
         }
         break;
     case AG_ACT_SILU:
