@@ -607,8 +607,8 @@ ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int n
  * 8-bit states: blocks of AG_ADAMW_BLOCK consecutive elements of a tensor
  * share one fp32 maximum S per state.  A code c stands for
  *   m = sign(c) (|c|/127)^2 S   (int8)       v = (c/255)^4 S   (uint8),
- * so that m and sqrt(v) reach down to the same 1.6e-5 of their block's
- * largest.  A value's code is floor(t + u), t its place on that scale and
+ * so that an m reaches down to 6.2e-5 of its block's largest (to nearest,
+ * below 1.6e-5 it is 0) and a sqrt(v) to 1.5e-5.  A value's code is floor(t + u), t its place on that scale and
  * u = 1/2 (nearest), or with stochastic rounding a number in (0,1) that a
  * counter hash makes from the seed and the element's place: updates far
  * smaller than a code's step then count on average instead of never.  v > 0
@@ -637,7 +637,7 @@ typedef struct ag_adamw_tensor {
  * synchronising call); 1 <= count <= 2^20, below 2^40 elements in all. */
 ag_status_t ag_adamw_create(const ag_adamw_tensor_t* tensors, int64_t count, ag_dtype_t param_dtype,
                             ag_dtype_t grad_dtype, int state_bits, ag_adamw_t** out);
-/* The step that uses the table must have completed. */
+/* The steps that use the table must have completed, and no captured graph that holds one may run any more. */
 ag_status_t ag_adamw_destroy(ag_adamw_t* optimizer);
 
 typedef struct ag_adamw_hyper {
