@@ -35,7 +35,7 @@ struct AdamwScalars {
     uint64_t seed;                          // mixed
 };
 
-// A seed's 64 bits spread over all of them.
+// A seed's 64 bits spread over all of them: a step of SplitMix64 (Steele, Lea and Flood 2014), with its constants.
 __host__ __device__ inline uint64_t adamw_mix_seed(uint64_t z)
 {
     z += 0x9E3779B97F4A7C15ull;

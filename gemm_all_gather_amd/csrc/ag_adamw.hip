@@ -6,8 +6,9 @@
 //
 // 32-bit states are bound by HBM: 117 million bf16 parameters with master weights (28 bytes each) take 623 us, 5.3 TB/s,
 // a large copy's rate.  8-bit states (10 bytes each; 228 us at that rate) are bound by the vector pipe: about 72
-// instructions an element, 5.5 of them square roots and reciprocals and 15 in fp64, 356 us.  The states are blended
-// in fp64 and doubtful codes decided there, so that the codes are those of exact arithmetic.  By the instructions'
+// instructions an element, 5.5 of them square roots and reciprocals and 15 in fp64, 345 to 356 us.  The states are blended
+// in fp64 and doubtful codes decided there, so that the codes are those of exact arithmetic (a blend in fp32 with its
+// error added to what counts as doubtful would give the same codes; it is not built).  By the instructions'
 // cycles 36% go into the blend and the update, 35% into the two codes, 29% into stochastic rounding's random bits.
 
 #include <hip/hip_runtime.h>
@@ -176,9 +177,10 @@ __device__ __forceinline__ void update(float (&p)[8], const float (&m)[8], const
     }
 }
 
-// 32 random bits of the state element at place i (counted over all tensors' blocks): multiply and xor-shift
-// rounds.  The seed comes in mixed (adamw_mix_seed), half before and half between the rounds, so that seeds that
-// count up give unrelated bits at every place.
+// 32 random bits of the state element at place i (counted over all tensors' blocks): the two multiply and xor-shift
+// rounds of a 32-bit mixer that Wellons found by search in 2018, with its multipliers and shifts.  The seed comes in
+// mixed (adamw_mix_seed), half before and half between the rounds, so that seeds that count up give unrelated bits at
+// every place.
 __device__ __forceinline__ uint32_t random_bits(uint64_t mixed_seed, uint64_t i)
 {
     uint32_t x = static_cast<uint32_t>(i) ^ (static_cast<uint32_t>(mixed_seed) + static_cast<uint32_t>(i >> 32) * 0x9E3779B1u);

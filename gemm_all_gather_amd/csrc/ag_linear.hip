@@ -187,9 +187,10 @@ __global__ __launch_bounds__(256) void ag_linear_pack_kernel(const uint16_t* src
 
 // dz = dy act'(z), rounded to the products' type, and the column sums of the unrounded dz over a.rows rows (summed on
 // by bias_grad_body: two levels in a fixed order, no atomics).  32 column groups of 8 x 8 row lanes; a workgroup takes
-// 256 columns.  One pass over dy and z, bound by HBM: 16384 x 3584, gelu_tanh (352 MB): 69 us, 5.1 TB/s, a copy's
+// 256 columns.  One pass over dy and z, bound by HBM: 16384 x 3584, gelu_tanh (352 MB): 69 to 71 us, 5.0 TB/s, a copy's
 // rate.  A kernel of its own because dz is an operand of both products; in their loads the slope would be computed
-// once per tile row and column (14 and 32 times), and they take operands to LDS without passing registers.
+// once per tile row and column (14 and 32 times), and they take operands to LDS without passing registers.  REST: dz's
+// second term too, as an instantiation of its own (a branch cost the other calls up to 1 us).
 template <bool BF16, bool REST>
 __global__ __launch_bounds__(256) void ag_linear_slope_kernel(LinearSlopeArgs a)
 {

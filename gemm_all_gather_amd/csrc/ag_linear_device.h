@@ -857,13 +857,15 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_kernel(LinearGemmArg
 // Measured, with one launch's start, epilogue and join:
 //   256 x 256  16384 x 3584 x 8192 NT with gelu_tanh and z, bf16, 680 to 709 us, 1.36 to 1.41 PFLOP/s (a library product
 //              of the same operands without epilogue 753); its gradients NN 659 and TN 687.  The matrix pipe is
-//              busy 73% of the cycles at the 1.8 GHz that the card's power limit leaves (zero operands 17 to 20% faster).
+//              busy 72 to 74% of the cycles at the 1.8 GHz that the card's power limit leaves (zero operands 17 to 20% faster).
 //   256 x 128  1024 x 8192 x 3584 NN (dx; 256 tiles) 58 us, 1.04 PFLOP/s.
 //   128 x 128  1024 x 3584 x 8192 NT with gelu and residual (224 tiles) 72 us, 0.84 PFLOP/s (the library 70 without
 //              either); without both, after a long warm-up, 60.  A stage takes 1060 cycles or more of 512 in the
 //              matrix pipe.  Not the fragments' latency holds it: reading them a stage before their use, with one
-//              stage less on its way, measured the same (34.8 and 35.0 us for 1024 x 4096 x 4096).  All three tiles draw
-//              12 to 15 TB/s from L2, which is what bounds the smaller two.
+//              stage less on its way, measured the same (34.8 and 35.0 us for 1024 x 4096 x 4096).
+// What holds the smaller two is not known.  A 128 x 128 stage needs 704 cycles of a CU's load intake, 768 of LDS and 512
+// of the matrix pipe, and takes 1060 to 1420 (181 750 cycles over the 128 stages of 1024 x 3584 x 8192); a 256 x 128 one
+// 1056, 1152 and 1024, and takes about 2300 (0.98 to 1.02 us).  All three tiles draw 12 to 15 TB/s from L2.
 // 256 x 256: a wave's 128 x 128 sub-tile keeps LDS reads (128 KiB a stage) and the rings' refill (64 KiB) below the
 // matrix pipe's 2048 cycles a stage at 128 bytes per cycle; its accumulators take 256 registers.
 // 256 x 128 (1152 LDS cycles against 1024) and 128 x 128 (768 against 512): for products with fewer tiles.

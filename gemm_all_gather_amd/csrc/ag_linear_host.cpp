@@ -117,7 +117,8 @@ struct Product {
     int launches() const { return !on ? 0 : join ? 2 : 1; }
 };
 
-// What a workgroup's 64-wide step measured in long products on all CUs.
+// What a workgroup's 64-wide step measured in long products on all CUs (before a stage's loads lay over both its halves,
+// which took 3% off the 256 x 256 ones).
 struct Kind {
     double step_us[3], fixed_us;     // a 64-wide step by form (NT, NN, TN); a launch's start and epilogue
 };
@@ -432,9 +433,9 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
     }
     // A weight gradient in fp32 takes dz in two 16-bit terms and so two products: with one it would carry the error
     // of a 16-bit gradient (2-norm relative to dw's 1.7e-3 in bf16, 2.1e-4 in fp16; with two 2.5e-6 and 3.5e-7, as
-    // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 us against 1468 of a
-    // bf16 dw, of 1024 rows 236 against 125.  dx and a 16-bit dw take one term: their own rounding is as large (2.3e-3
-    // in all against 1.7e-3), and two would double the time of both products.  relu's dz needs no rounding.
+    // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 to 2290 us against 1468
+    // to 1490 of a bf16 dw, of 1024 rows 231 against 122.  dx and a 16-bit dw take one term: their own rounding is as
+    // large (2.3e-3 in all against 1.7e-3), and two would double the time of both products.  relu's dz needs no rounding.
     const bool two_terms = b->store_dz && want_dw && act && a->act != AG_ACT_RELU && a->dw_dtype == AG_F32;
     if (two_terms) {
         b->dz_rest_offset = used;
@@ -481,7 +482,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         }
     }
     // Otherwise both in turn, where that saves a good part of a round: 1000 x 4100 x 4100, dw added up in fp32, 179
-    // us in launches of their own, 151 in turn (127 since a stage's loads lie over both its halves).  Long products are
+    // us in launches of their own, 151 in turn (125 since a stage's loads lie over both its halves).  Long products are
     // held by power: idle CUs at a round's end let the others run faster, and 16384 x 3584 x 8192 measured 1505 in
     // turn against 1501.
     if (b->px.on && b->pw.on && !b->together) {
