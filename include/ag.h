@@ -614,7 +614,8 @@ ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int n
  * smaller than a code's step then count on average instead of never.  v > 0
  * never rounds to the code 0, so no live first moment meets a zero
  * denominator.  All-zero codes and scales are the zero state.  A NaN or an
- * infinity makes its whole block's state NaN (the parameters: its element).
+ * infinity (also a v past fp32's largest, from gradients of about 1e20 on)
+ * makes its whole block's state NaN (the parameters: its element).
  * ------------------------------------------------------------------------ */
 #define AG_ADAMW_BLOCK 256
 
