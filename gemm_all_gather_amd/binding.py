@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from operator import attrgetter
 from typing import Optional
 
@@ -609,7 +610,8 @@ class AdamW:
             raise ValueError("an output is not contiguous, not of its parameter's elements or not fp32")
         if not _reachable(tensors):
             raise ValueError("an output lies in host memory that is not pinned")
-        return (_vp * max(1, len(part)))(*map(T.data_ptr if tensors is part else _ptr, part))
+        at = array("Q", map(T.data_ptr if tensors is part else _ptr, part))
+        return (_vp * len(at)).from_buffer(at) if at else (_vp * 1)()
 
     def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:
         """The fp32 values of 8-bit states, into two lists of fp32 tensors, contiguous and of each parameter's
