@@ -562,6 +562,9 @@ class AdamW:
         self._h = h
         self._keepalive = parts
         self._sizes = [p.numel() for p in params]
+        T = torch.Tensor
+        self._reads = T.numel, T.is_contiguous, attrgetter("dtype"), T.get_device, T.data_ptr, {torch.float32}
+        self._pointers = _vp * count
 
     def destroy(self) -> None:
         if self._h is not None and self._h.value:
@@ -595,26 +598,27 @@ class AdamW:
                        0 if seed is None else seed, 0 if seed is None else 1)
         _check(lib().ag_adamw_step(self.handle, ctypes.byref(y), _stream(stream)), "ag_adamw_step")
 
-    def _outputs(self, part):
-        """The addresses of one fp32 output per tensor, each checked (by whole lists: there may be hundreds a call)."""
-        import torch
-        if len(part) != len(self._sizes):
-            raise ValueError("the lists of tensors differ in length")
-        tensors, sizes = part, self._sizes
-        if int in set(map(type, part)):     # addresses among them
-            which = [i for i, t in enumerate(part) if not isinstance(t, int)]
-            tensors, sizes = [part[i] for i in which], [sizes[i] for i in which]
-        T = torch.Tensor
-        if (list(map(T.numel, tensors)) != sizes or not all(map(T.is_contiguous, tensors)) or
-                set(map(attrgetter("dtype"), tensors)) - {torch.float32}):
+    def _addresses(self, outputs):
+        """The outputs' addresses, each tensor checked first (by whole lists: there may be hundreds a call)."""
+        if int in set(map(type, outputs)):      # addresses among them are taken as they are
+            at = [t if isinstance(t, int) else self._addresses_of([t], [n])[0] for t, n in zip(outputs, self._sizes * 2)]
+            return array("Q", at)
+        return self._addresses_of(outputs, self._sizes * 2)
+
+    def _addresses_of(self, tensors, sizes):
+        numel, contiguous, dtype, device, data_ptr, fp32 = self._reads
+        if list(map(numel, tensors)) != sizes or not all(map(contiguous, tensors)) or not fp32.issuperset(map(dtype, tensors)):
             raise ValueError("an output is not contiguous, not of its parameter's elements or not fp32")
-        if not _reachable(tensors):
+        if min(map(device, tensors), default=0) < 0 and not _reachable(tensors):
             raise ValueError("an output lies in host memory that is not pinned")
-        at = array("Q", map(T.data_ptr if tensors is part else _ptr, part))
-        return (_vp * len(at)).from_buffer(at) if at else (_vp * 1)()
+        return array("Q", map(data_ptr, tensors))
 
     def read_states(self, exp_avgs, exp_avg_sqs, stream=None) -> None:
         """The fp32 values of 8-bit states, into two lists of fp32 tensors, contiguous and of each parameter's
         elements (or device addresses of as many floats) (ag_adamw_read_states)."""
-        m, v = (self._outputs(tuple(part)) for part in (exp_avgs, exp_avg_sqs))
+        m, v, n = tuple(exp_avgs), tuple(exp_avg_sqs), len(self._sizes)
+        if len(m) != n or len(v) != n:
+            raise ValueError("the lists of tensors differ in length")
+        at = self._addresses(m + v)
+        m, v = self._pointers.from_buffer(at), self._pointers.from_buffer(at, n * at.itemsize)
         _check(lib().ag_adamw_read_states(self.handle, m, v, _stream(stream)), "ag_adamw_read_states")

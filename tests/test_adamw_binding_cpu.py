@@ -203,3 +203,16 @@ def test_reachable_memory():
     host, pinned = torch.zeros(3), torch.zeros(3).as_subclass(Pinned)
     assert ag._reachable([]) and ag._reachable([torch.zeros(0)]) and ag._reachable([pinned])
     assert not ag._reachable([host]) and not ag._reachable([pinned, host]) and not ag._reachable([torch.zeros(3, device="meta")])
+
+
+def test_read_states_takes_addresses_among_tensors(library):
+    opt = ag.AdamW(**lists(True))
+    m, v = outputs()
+    want = [t.data_ptr() for t in m], [t.data_ptr() for t in v]
+    m[1], v[3] = want[0][1], want[1][3]
+    opt.read_states(m, v)
+    assert library.reads == [want]
+    m[0] = tensor(4)
+    with pytest.raises(ValueError):
+        opt.read_states(m, v)
+    opt.destroy()
