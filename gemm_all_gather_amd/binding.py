@@ -108,6 +108,29 @@ class LinearPlan(ctypes.Structure):
                 [("flops", ctypes.c_double)] + _fields(ctypes.c_int32, "launches reserved"))
 
 
+class LinearI8Args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "x w x_scale w_scale bias residual y z") +
+                _fields(ctypes.c_int64, "ldx ldw ldr ldy ldz M N K") +
+                _fields(ctypes.c_int32, "dtype act") + [("reserved", ctypes.c_int32 * 6)])
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "x residual weight h y q scale rstd") +
+                _fields(ctypes.c_int64, "ldx ldr ldh ldy ldq M K") + [("eps", ctypes.c_double)] +
+                [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)])
+
+
+class RmsNormBackwardArgs(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "dy h dh weight rstd dx dw") +
+                _fields(ctypes.c_int64, "lddy ldh lddh lddx M K") +
+                _fields(ctypes.c_int32, "dtype dw_dtype accumulate") + [("reserved", ctypes.c_int32 * 5)])
+
+
+class RowsPlan(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_int32, "threads_per_row vectors_per_thread n_programs launches") +
+                _fields(ctypes.c_uint64, "workspace_bytes bytes_read bytes_written"))
+
+
 class AdamwTensor(ctypes.Structure):
     _fields_ = (_fields(ctypes.c_void_p, "param grad exp_avg exp_avg_sq exp_avg_scale exp_avg_sq_scale master") +
                 [("n", ctypes.c_int64)])
@@ -178,6 +201,12 @@ _SIGNATURES = {
     "ag_plan_linear": [ctypes.POINTER(LinearArgs), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _vp, _c_size, _vp],
     "ag_plan_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_quantize_rows": [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp],
+    "ag_dequantize_rows": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp],
+    "ag_rms_norm": [ctypes.POINTER(RmsNormArgs), _vp],
+    "ag_plan_rms_norm": [ctypes.POINTER(RmsNormArgs), _c_int, ctypes.POINTER(RowsPlan)],
+    "ag_rms_norm_backward": [ctypes.POINTER(RmsNormBackwardArgs), _vp, _c_size, _vp],
+    "ag_plan_rms_norm_backward": [ctypes.POINTER(RmsNormBackwardArgs), _c_int, ctypes.POINTER(RowsPlan)],
     "ag_adamw_create": [ctypes.POINTER(AdamwTensor), _c_i64, _c_int, _c_int, _c_int, _HEAP_PP],
     "ag_adamw_destroy": [_vp],
     "ag_adamw_step": [_vp, ctypes.POINTER(AdamwHyper), _vp],
@@ -501,6 +530,80 @@ def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=No
                        accumulate)
     ws, nbytes = _workspace(workspace)
     _check(lib().ag_linear_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_backward")
+
+
+def _operand(x, code, name) -> int:
+    """Address of an operand: None, an address, or a tensor of the type on the current device."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    import torch
+    want = {AG_F16: torch.float16, AG_BF16: torch.bfloat16, AG_F32: torch.float32, "int8": torch.int8}.get(code)
+    if want is not None and x.dtype is not want:
+        raise ValueError(f"{name} is not of {want}")
+    if x.get_device() < 0 or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} does not lie on the current device")
+    return x.data_ptr()
+
+
+def quantize_rows(x, q, scale, M, K, dtype, ldx=0, ldq=0, stream=None) -> None:
+    """Each row of x as int8 codes and one fp32 scale (ag_quantize_rows)."""
+    d = _dtype(dtype)
+    _check(lib().ag_quantize_rows(_operand(x, d, "x"), ldx, _operand(q, "int8", "q"), ldq, _operand(scale, AG_F32, "scale"), M, K,
+                                  d, _stream(stream)), "ag_quantize_rows")
+
+
+def dequantize_rows(q, scale, y, M, K, dtype, ldq=0, ldy=0, stream=None) -> None:
+    """y = q * scale, the values that codes stand for (ag_dequantize_rows)."""
+    d = _dtype(dtype)
+    _check(lib().ag_dequantize_rows(_operand(q, "int8", "q"), ldq, _operand(scale, AG_F32, "scale"), _operand(y, d, "y"), ldy, M,
+                                    K, d, _stream(stream)), "ag_dequantize_rows")
+
+
+def _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq) -> RmsNormArgs:
+    d = _dtype(dtype)
+    return RmsNormArgs(_operand(x, d, "x"), _operand(residual, d, "residual"), _operand(weight, d, "weight"), _operand(h, d, "h"),
+                       _operand(y, d, "y"), _operand(q, "int8", "q"), _operand(scale, AG_F32, "scale"),
+                       _operand(rstd, AG_F32, "rstd"), ldx, ldr, ldh, ldy, ldq, M, K, eps, d)
+
+
+def plan_rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0,
+                  ldr=0, ldh=0, ldy=0, ldq=0, num_cus=0) -> RowsPlan:
+    p = RowsPlan()
+    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
+    _check(lib().ag_plan_rms_norm(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_rms_norm")
+    return p
+
+
+def rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0, ldr=0,
+             ldh=0, ldy=0, ldq=0, stream=None) -> None:
+    """The norm of h = x + residual, into y and, or, the codes q with their scales (ag_rms_norm)."""
+    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
+    _check(lib().ag_rms_norm(ctypes.byref(a), _stream(stream)), "ag_rms_norm")
+
+
+def _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype,
+                        accumulate) -> RmsNormBackwardArgs:
+    d = _dtype(dtype)
+    g = d if dw_dtype is None else _dtype(dw_dtype)
+    return RmsNormBackwardArgs(_operand(dy, d, "dy"), _operand(h, d, "h"), _operand(dh, d, "dh"), _operand(weight, d, "weight"),
+                               _operand(rstd, AG_F32, "rstd"), _operand(dx, d, "dx"), _operand(dw, g, "dw"), lddy, ldh, lddh,
+                               lddx, M, K, d, g, int(accumulate))
+
+
+def plan_rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
+                           dw_dtype=None, accumulate=False, num_cus=0) -> RowsPlan:
+    p = RowsPlan()
+    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
+    _check(lib().ag_plan_rms_norm_backward(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_rms_norm_backward")
+    return p
+
+
+def rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
+                      dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
+    """The norm's gradients dx (with dh, what reaches h otherwise) and dw, those that are given (ag_rms_norm_backward)."""
+    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_rms_norm_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_rms_norm_backward")
 
 
 def _reachable(tensors) -> bool:

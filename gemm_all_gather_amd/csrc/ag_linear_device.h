@@ -15,64 +15,13 @@
 #include "ag.h"
 #include "ag_linear.h"
 #include "ag_mfma.h"
+#include "ag_vec.h"
 
 namespace ag {
 
 // ---------------------------------------------------------------- epilogue
 
 namespace {
-
-template <bool BF16> __device__ __forceinline__ float to_f32(uint16_t v)
-{
-    if constexpr (BF16) return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
-    else return static_cast<float>(__builtin_bit_cast(_Float16, v));
-}
-template <bool BF16> __device__ __forceinline__ uint16_t from_f32(float v)   // to nearest, ties to even
-{
-    if constexpr (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-    else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-}
-
-// Vectors at any alignment of their elements (global accesses need none on gfx950).
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
-
-__device__ __forceinline__ u16x8 load8(const uint16_t* p)
-{
-    return __builtin_bit_cast(u16x8, reinterpret_cast<const Any16*>(p)->v);
-}
-__device__ __forceinline__ void store8(uint16_t* p, u16x8 v)
-{
-    reinterpret_cast<Any16*>(p)->v = __builtin_bit_cast(u32x4, v);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load_f32(float (&v)[8], const uint16_t* p, int n)
-{
-    if (n >= 8) {
-        const u16x8 t = load8(p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = to_f32<BF16>(t[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < n ? to_f32<BF16>(p[e]) : 0.f;
-    }
-}
-template <bool BF16>
-__device__ __forceinline__ void store_16(uint16_t* p, const float (&v)[8], int n)
-{
-    u16x8 t;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = from_f32<BF16>(v[e]);
-    if (n >= 8) {
-        store8(p, t);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n) p[e] = t[e];
-    }
-}
 
 constexpr float kGeluK = 0.79788456080286536f;      // sqrt(2/pi)
 constexpr float kGeluC = 0.044715f;

@@ -1,0 +1,65 @@
+// Internal interface between the host code of the row operators (ag_rows_host.cpp: codes of 8 bits, the
+// root-mean-square norm and its gradients) and their kernels (ag_rows.hip).  Not part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ag {
+
+// One pass over rows: h = x + residual, its norm, and the row in 16 or 8 bits; without `norm` the row itself in 8 bits.
+struct RowsArgs {
+    const void* x;
+    const void* residual;   // or null
+    const void* weight;     // or null
+    void* h;                // or null
+    void* y;                // or null
+    int8_t* q;              // or null
+    float* scale;           // with q
+    float* rstd;            // or null
+    int64_t ldx, ldr, ldh, ldy, ldq;
+    int64_t M;
+    int32_t K;
+    int32_t reserved;
+    double eps;
+};
+
+// How a row is dealt to threads: `threads` of a workgroup with `vectors` of 8 elements each in registers; vectors 0:
+// longer rows, read twice by `threads`.
+struct RowsShape {
+    int threads, vectors;
+    int per_group;          // rows of a workgroup at a time
+};
+RowsShape rows_shape(int64_t K);
+
+// norm with dtype AG_F16 or AG_BF16; without it AG_F32 too.
+hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hipStream_t stream);
+
+// y = q * scale in dtype.  scales_by_two: y = q * (the scale's power of two, by split_scale) in a 16-bit type, exactly.
+struct DequantizeArgs {
+    const int8_t* q;
+    const float* scale;
+    void* y;
+    int64_t ldq, ldy;
+    int64_t M;
+    int32_t K;
+    int32_t by_power;
+};
+hipError_t launch_dequantize(const DequantizeArgs& a, int dtype, hipStream_t stream);
+
+struct NormBackwardArgs {
+    const uint16_t* dy;
+    const uint16_t* h;
+    const uint16_t* dh;         // or null
+    const uint16_t* weight;     // or null
+    const float* rstd;
+    uint16_t* dx;               // or null; may be dh
+    float* sums;                // one row of K floats for each workgroup, or null
+    int64_t lddy, ldh, lddh, lddx;
+    int64_t M;
+    int32_t K;
+    int32_t reserved;
+};
+hipError_t launch_norm_backward(const NormBackwardArgs& a, int bf16, int programs, hipStream_t stream);
+
+}  // namespace ag

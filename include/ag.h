@@ -591,6 +591,117 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
 ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int num_cus, ag_linear_plan_t* plan);
 
 /* ------------------------------------------------------------------------
+ * Rows in 8 bits.  One format serves activations, weights and checkpoints: a
+ * row of K numbers v becomes K codes and one fp32 scale,
+ *
+ *   a = max |v_k|,  q_k = the whole number nearest to 127 v_k / a (ties to
+ *   even),  scale = a / 127,                v_k stands as q_k * scale
+ *
+ * so that |q| <= 127.  The codes are those of exact arithmetic, whatever the
+ * row's size or the kernel that made them.  A row of zeros has zero codes and
+ * scale 0; a NaN or an infinity makes its row's scale NaN and its codes 0.
+ *
+ * x       device, M x K of dtype (AG_F16, AG_BF16 or AG_F32), row stride ldx
+ * q       device, M x K int8, row stride ldq
+ * scale   device, M floats
+ * y       device, M x K of dtype, row stride ldy: q * scale, rounded once
+ * M below 2^31, K up to 2^20; strides as for ag_linear (0 = dense).  Outputs
+ * must not overlap inputs or each other.  One launch each; nothing to do for
+ * M = 0 (K = 0: the scales are 0).
+ * ------------------------------------------------------------------------ */
+ag_status_t ag_quantize_rows(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t M, int64_t K,
+                             ag_dtype_t dtype, void* stream);
+ag_status_t ag_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale, void* y, int64_t ldy, int64_t M,
+                               int64_t K, ag_dtype_t dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm, with the residual's addition before it and an output
+ * in 16 or in 8 bits: what stands between two linear layers.
+ *
+ *   h = x + residual                  (rounded to dtype: the norm is of what is stored)
+ *   rstd = 1 / sqrt(mean of h^2 over the row + eps)
+ *   y = h rstd weight                 (rounded once)
+ *   q, scale: the row h weight in 8 bits as above, its scale times rstd
+ *
+ * x, residual, h, y   device, M x K of dtype (AG_F16 or AG_BF16); residual,
+ *            h and y may be NULL; h may be x or residual itself (same address
+ *            and stride)
+ * weight     device, K of dtype, or NULL (ones)
+ * q, scale   device, M x K int8 and M floats, or both NULL
+ * rstd       device, M floats, or NULL (ag_rms_norm_backward reads it)
+ * eps        > 0, finite
+ * Squares are summed in fp64 and products h weight kept exact (fp32), so that
+ * no size of h overflows; the codes are those of exact arithmetic, wherever
+ * the products lie within fp32's normal numbers.  A row with a product past
+ * fp32's largest has the scale NaN, as one with a NaN or an infinity.
+ * Sizes, strides and overlaps as above.  One launch.
+ * ------------------------------------------------------------------------ */
+typedef struct ag_rms_norm_args {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* h;
+    void* y;
+    int8_t* q;
+    float* scale;
+    float* rstd;
+    int64_t ldx, ldr, ldh, ldy, ldq;
+    int64_t M, K;
+    double eps;
+    int32_t dtype;        /* ag_dtype_t */
+    int32_t reserved[7];  /* must be 0 */
+} ag_rms_norm_args_t;
+
+typedef struct ag_rows_plan {
+    int32_t threads_per_row;       /* of a workgroup */
+    int32_t vectors_per_thread;    /* of 8 elements, kept in registers; 0: the row is read twice */
+    int32_t n_programs;            /* workgroups */
+    int32_t launches;
+    uint64_t workspace_bytes;
+    uint64_t bytes_read;           /* algorithmic: each input once */
+    uint64_t bytes_written;
+} ag_rows_plan_t;
+
+ag_status_t ag_rms_norm(const ag_rms_norm_args_t* args, void* stream);
+ag_status_t ag_plan_rms_norm(const ag_rms_norm_args_t* args, int num_cus, ag_rows_plan_t* plan);
+
+/* Gradients of the norm, from the gradient dy of y and, where h goes on past
+ * the norm (the residual's way), the gradient dh that reaches h there:
+ *
+ *   g = dy weight
+ *   dx = rstd (g - h rstd^2 mean(g h)) + dh     (x's gradient and the residual's alike)
+ *   dw = sum over rows dy h rstd                + dw if accumulate
+ *
+ * dy, h, dh, dx  device, M x K of dtype; dh may be NULL, dx may be dh itself
+ *                (same address and stride); h is what ag_rms_norm normalised
+ * rstd           device, M floats
+ * weight         device, K of dtype, or NULL (ones)
+ * dx, dw         either may be NULL (not computed); dw has dw_dtype: dtype or
+ *                AG_F32
+ * Sums are fp32 (mean(g h): one row's; dw: rows dealt to the workgroups, then
+ * their sums in a fixed order, without atomics).  The workspace is as for
+ * ag_linear.  M = 0 gives a zero dw (or leaves it, with accumulate). */
+typedef struct ag_rms_norm_backward_args {
+    const void* dy;
+    const void* h;
+    const void* dh;
+    const void* weight;
+    const float* rstd;
+    void* dx;
+    void* dw;
+    int64_t lddy, ldh, lddh, lddx;
+    int64_t M, K;
+    int32_t dtype;        /* ag_dtype_t */
+    int32_t dw_dtype;     /* ag_dtype_t */
+    int32_t accumulate;   /* 0 or 1 */
+    int32_t reserved[5];  /* must be 0 */
+} ag_rms_norm_backward_args_t;
+
+ag_status_t ag_rms_norm_backward(const ag_rms_norm_backward_args_t* args, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+ag_status_t ag_plan_rms_norm_backward(const ag_rms_norm_backward_args_t* args, int num_cus, ag_rows_plan_t* plan);
+
+/* ------------------------------------------------------------------------
  * AdamW over many tensors in one launch, with states in 32 or in 8 bits.
  * A handle keeps a device table of the tensors' addresses, made once (as a
  * heap keeps its base table); the tensors must stay where they are while the
