@@ -201,6 +201,8 @@ _SIGNATURES = {
     "ag_plan_linear": [ctypes.POINTER(LinearArgs), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _vp, _c_size, _vp],
     "ag_plan_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_linear_i8": [ctypes.POINTER(LinearI8Args), _vp, _c_size, _vp],
+    "ag_plan_linear_i8": [ctypes.POINTER(LinearI8Args), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_quantize_rows": [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp],
     "ag_dequantize_rows": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp],
     "ag_rms_norm": [ctypes.POINTER(RmsNormArgs), _vp],
@@ -604,6 +606,29 @@ def rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, d
     a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
     ws, nbytes = _workspace(workspace)
     _check(lib().ag_rms_norm_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_rms_norm_backward")
+
+
+def _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz) -> LinearI8Args:
+    d = _dtype(dtype)
+    return LinearI8Args(_operand(x, "int8", "x"), _operand(w, "int8", "w"), _operand(x_scale, AG_F32, "x_scale"),
+                        _operand(w_scale, AG_F32, "w_scale"), _operand(bias, d, "bias"), _operand(residual, d, "residual"),
+                        _operand(y, d, "y"), _operand(z, d, "z"), ldx, ldw, ldr, ldy, ldz, M, N, K, d, _act(act))
+
+
+def plan_linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0,
+                   ldy=0, ldz=0, num_cus=0) -> LinearPlan:
+    p = LinearPlan()
+    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    _check(lib().ag_plan_linear_i8(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_linear_i8")
+    return p
+
+
+def linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0, ldy=0,
+              ldz=0, workspace=None, stream=None) -> None:
+    """y = act(x_scale w_scale (x w^T) + bias) + residual of int8 codes x and w (ag_linear_i8)."""
+    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_linear_i8(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_i8")
 
 
 def _reachable(tensors) -> bool:

@@ -47,6 +47,13 @@ struct LinearGemmArgs {
     LinearBiasGradArgs db;      // gradient kernels: the bias gradient's sum on the side (db.db null: none)
 };
 
+// The same of 8-bit integers (forward only): A and B point to bytes, their strides and R count bytes, stages are 128 wide,
+// and the partial tiles hold int32.
+struct LinearI8GemmArgs : LinearGemmArgs {
+    const float* row_scale;     // of A's rows
+    const float* col_scale;     // of B's rows
+};
+
 enum LinearTile { kLinearTile256 = 0, kLinearTile128 = 1, kLinearTile256x128 = 2, kLinearTiles = 3 };
 enum LinearForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };   // y, dx, dw
 
@@ -57,6 +64,12 @@ LinearGemmFn linear_forward_f16(int act, int tile);
 LinearGemmFn linear_forward_bf16(int act, int tile);
 LinearGemmFn linear_gradient_f16(int form, int tile);
 LinearGemmFn linear_gradient_bf16(int form, int tile);
+
+using LinearI8GemmFn = void (*)(LinearI8GemmArgs);
+LinearI8GemmFn linear_i8_f16(int act, int tile);
+LinearI8GemmFn linear_i8_bf16(int act, int tile);
+hipError_t launch_linear_i8_gemm(const LinearI8GemmArgs& a, int bf16, int tile, int programs, hipStream_t stream);
+hipError_t launch_linear_i8_join(const LinearI8GemmArgs& a, int bf16, int tile, hipStream_t stream);
 
 // Joins the parts of the cut tiles in order and applies the epilogue.
 hipError_t launch_linear_join(const LinearGemmArgs& a, int bf16, int form, int tile, hipStream_t stream);
@@ -71,6 +84,21 @@ struct LinearStreamArgs {
     LinearEpilogue epi;
 };
 hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, int cus, hipStream_t stream);
+
+// The same of 8-bit integers.
+struct LinearI8StreamArgs {
+    const int8_t* x;
+    const int8_t* w;
+    const float* x_scale;
+    const float* w_scale;
+    int64_t ldx, ldw;
+    int64_t M, N, K;
+    LinearEpilogue epi;
+};
+hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cus, hipStream_t stream);
+// Copies rows of bytes to aligned rows (ld_dst a multiple of 16).
+hipError_t launch_linear_i8_pack(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst, int64_t rows, int64_t cols,
+                                 hipStream_t stream);
 
 // Copies rows to aligned rows (ld_dst a multiple of 8).
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,

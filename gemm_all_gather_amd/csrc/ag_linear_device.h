@@ -344,14 +344,31 @@ struct Frags {
     }
 };
 
+// What a product's operands hold: 16-bit floats, or 8-bit integers with a scale for each row of A and of B, whose
+// epilogue works in a 16-bit type all the same.  A stage's 128 bytes of a row are 64 of the one or 128 of the other, and
+// so are the loads, the LDS layout and the fragments' places.
+template <bool BF16_> struct Floats {
+    static constexpr bool BF16 = BF16_, I8 = false;
+    using V = typename Mfma<BF16_>::V;
+    using Args = LinearGemmArgs;
+    static __device__ __forceinline__ int64_t units(int64_t elements) { return elements; }       // of 16 bits
+};
+template <bool BF16_> struct Codes {
+    static constexpr bool BF16 = BF16_, I8 = true;
+    using V = u32x4;
+    using Args = LinearI8GemmArgs;
+    static __device__ __forceinline__ int64_t units(int64_t elements) { return (elements + 1) / 2; }
+};
+
 // c += b a^T with c in accumulation registers.  Inline assembly keeps the 256 accumulators of a 256 x 256 tile in
 // the accumulation half of the register file; left to itself the compiler spread them over both halves and
 // spilled.  It does not see these instructions' write latency: c is used again no sooner than BM * BN of them
 // later, and settle() stands between them and other uses.
-template <bool BF16, class V>
+template <class E, class V>
 __device__ __forceinline__ void mfma(f32x4& c, V b, V a)
 {
-    if constexpr (BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+    if constexpr (E::I8) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));   // c holds int32
+    else if constexpr (E::BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
     else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
 }
 __device__ __forceinline__ void settle()
@@ -450,19 +467,42 @@ struct Walk {
     __device__ __forceinline__ void down() { p += rows16; }
 };
 
-template <bool BF16, int FORM, int ACT, class C>
-__device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, int programs, uint8_t* ring)
+// Sums of 8-bit products (the bits of v), times the scales.
+__device__ __forceinline__ void apply_scales(float (&v)[8], float row, const float (&col)[8])
 {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(__float_as_int(v[e])) * row * col[e];
+}
+__device__ __forceinline__ void load_scales(float (&v)[8], const float* p, int n)
+{
+    if (n >= 8) {
+        const f32x4u lo = *reinterpret_cast<const f32x4u*>(p), hi = *reinterpret_cast<const f32x4u*>(p + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = lo[e];
+            v[4 + e] = hi[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.f;
+    }
+}
+
+template <class E, int FORM, int ACT, class C>
+__device__ __forceinline__ void gemm_body(const typename E::Args& a, int program, int programs, uint8_t* ring)
+{
+    constexpr bool BF16 = E::BF16;
     constexpr bool TA = FORM == kFormTN, TB = FORM != kFormNT;
     constexpr int BM = C::BM, BN = C::BN;
-    using V = typename Mfma<BF16>::V;
+    using V = typename E::V;
     using PartA = Part<C::TM, TA>;
     using PartB = Part<C::TN, TB>;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const uint32_t lda2 = static_cast<uint32_t>(a.lda) * 2u, ldb2 = static_cast<uint32_t>(a.ldb) * 2u;
+    constexpr uint32_t SIZE = E::I8 ? 1 : 2;
+    const uint32_t lda2 = static_cast<uint32_t>(a.lda) * SIZE, ldb2 = static_cast<uint32_t>(a.ldb) * SIZE;
 
     PartA pa;
     PartB pb;
@@ -479,13 +519,13 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
         const Piece w = piece_of(a, program, programs, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::TM, C::TN, &i0, &j0);
-        return PartA::start(a.A, i0, a.I, a.R, lda2, w.first, w.count);
+        return PartA::start(a.A, i0, a.I, E::units(a.R), lda2, w.first, w.count);
     };
     auto start_b = [&](int q) {
         const Piece w = piece_of(a, program, programs, q);
         int64_t i0, j0;
         place_tile(a, w.tile, C::TM, C::TN, &i0, &j0);
-        return PartB::start(a.B, j0, a.J, a.R, ldb2, w.first, w.count);
+        return PartB::start(a.B, j0, a.J, E::units(a.R), ldb2, w.first, w.count);
     };
     int qa = 0, qb = 0;
     typename PartA::Next na = start_a(0);
@@ -506,16 +546,19 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
     auto next_slot = [](int slot, int slots) { return slot + 1 == slots ? 0 : slot + 1; };
     // Where the reduction is no multiple of 64, the last stage of an r-contiguous operand goes on into the next
     // rows: that is set to zero in LDS, once, when a tile's last stage has landed.
-    const bool ragged = !(TA && TB) && (a.R & 63) != 0;
+    constexpr uint32_t IN_STAGE = E::I8 ? 128 : 64, IN_CHUNK = IN_STAGE / 8;       // elements
+    const bool ragged = !(TA && TB) && (a.R & (IN_STAGE - 1)) != 0;
     auto clear_tail = [&](int slot_a, int slot_b) {
-        const uint32_t from = static_cast<uint32_t>(a.R & 63);
+        const uint32_t from = static_cast<uint32_t>(a.R & (IN_STAGE - 1));
         for (int row = tid; row < C::TM + C::TN; row += C::NT) {
             if ((TA && row < C::TM) || (TB && row >= C::TM)) continue;
             uint8_t* line = row < C::TM ? ring + slot_a * C::A_BYTES + row * 128 : ring_b + slot_b * C::B_BYTES + (row - C::TM) * 128;
-            for (uint32_t c = from >> 3; c < 8; ++c) {
+            for (uint32_t c = from / IN_CHUNK; c < 8; ++c) {
                 uint8_t* chunk = line + ((c ^ (static_cast<uint32_t>(row) & 7u)) << 4);   // TM is a multiple of 8
-                if (c * 8 >= from) {
+                if (c * IN_CHUNK >= from) {
                     *reinterpret_cast<u32x4*>(chunk) = u32x4{0u, 0u, 0u, 0u};
+                } else if constexpr (E::I8) {
+                    for (uint32_t e = from & 15u; e < 16; ++e) chunk[e] = 0;
                 } else {
                     for (uint32_t e = from & 7u; e < 8; ++e) reinterpret_cast<uint16_t*>(chunk)[e] = 0;
                 }
@@ -606,7 +649,7 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
                 if (i % C::READ_STEP == 0 && i / C::READ_STEP < BM + BN) read(1, here_a, here_b, 1, i / C::READ_STEP);
                 if constexpr (C::LATE_A) refill_a(la, late, i);
                 else refill_b(lb, late, i);
-                mfma<BF16>(acc[i / BN][i % BN], fb[0][i % BN], fa[0][i / BN]);
+                mfma<E>(acc[i / BN][i % BN], fb[0][i % BN], fa[0][i / BN]);
                 __builtin_amdgcn_sched_barrier(0x6);
             }
             la = take_a();
@@ -622,7 +665,7 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
                 if (i % C::READ_STEP == 0 && i / C::READ_STEP < BM + BN) read(0, there_a, there_b, 0, i / C::READ_STEP);
                 if constexpr (C::LATE_A) refill_b(lb, sb, i);
                 else refill_a(la, sa, i);
-                mfma<BF16>(acc[i / BN][i % BN], fb[1][i % BN], fa[1][i / BN]);
+                mfma<E>(acc[i / BN][i % BN], fb[1][i % BN], fa[1][i / BN]);
                 __builtin_amdgcn_sched_barrier(0x6);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -664,12 +707,20 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
 #pragma unroll
                 for (int b = 0; b < BN / 2; ++b) load_f32<BF16>(bias[b], a.epi.bias + col0 + 32 * b, 8);
             }
+            [[maybe_unused]] float col_scale[E::I8 ? BN / 2 : 1][8];
+            if constexpr (E::I8) {
+#pragma unroll
+                for (int b = 0; b < BN / 2; ++b) load_scales(col_scale[b], a.col_scale + col0 + 32 * b, 8);
+            }
             each<BM>([&](auto row_block) __attribute__((always_inline)) {
                 constexpr int bm = decltype(row_block)::value;
+                [[maybe_unused]] float row_scale = 1.f;
+                if constexpr (E::I8) row_scale = a.row_scale[row0 + 16 * bm];
 #pragma unroll
                 for (int b = 0; b < BN / 2; ++b) {
                     float x[8];
                     widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                    if constexpr (E::I8) apply_scales(x, row_scale, col_scale[b]);
                     if constexpr (FORM == kFormNT) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] += bias[b][e];
@@ -706,6 +757,11 @@ __device__ __forceinline__ void gemm_body(const LinearGemmArgs& a, int program, 
                     const int64_t col = col0 + 32 * b;
                     const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
                     if (row < a.I && n > 0) {
+                        if constexpr (E::I8) {
+                            float col_scale[8];
+                            load_scales(col_scale, a.col_scale + col, n);
+                            apply_scales(x, a.row_scale[row], col_scale);
+                        }
                         if constexpr (FORM == kFormNT) {
                             float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                             if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
@@ -766,8 +822,16 @@ template <bool BF16, int FORM, int ACT, class C>
 __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
-    gemm_body<BF16, FORM, ACT, C>(a, blockIdx.x, gridDim.x, ring);
+    gemm_body<Floats<BF16>, FORM, ACT, C>(a, blockIdx.x, gridDim.x, ring);
     if constexpr (FORM != kFormNT) bias_grads_after(a.db, blockIdx.x, gridDim.x, ring);
+}
+
+// y of 8-bit integers.
+template <bool BF16, int ACT, class C>
+__global__ __launch_bounds__(C::NT, 1) void ag_linear_i8_gemm_kernel(LinearI8GemmArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
+    gemm_body<Codes<BF16>, kFormNT, ACT, C>(a, blockIdx.x, gridDim.x, ring);
 }
 
 // dx, dw and the bias gradient's sum one after the other on every workgroup: the product with the longer tiles first,
@@ -779,13 +843,13 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_in_turn_kernel(Linea
     __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
     const int p = blockIdx.x, n = gridDim.x;
     if constexpr (DX_FIRST) {
-        gemm_body<BF16, kFormNN, AG_ACT_NONE, C>(dx, p, n, ring);
+        gemm_body<Floats<BF16>, kFormNN, AG_ACT_NONE, C>(dx, p, n, ring);
         __syncthreads();
-        gemm_body<BF16, kFormTN, AG_ACT_NONE, C>(dw, p, n, ring);
+        gemm_body<Floats<BF16>, kFormTN, AG_ACT_NONE, C>(dw, p, n, ring);
     } else {
-        gemm_body<BF16, kFormTN, AG_ACT_NONE, C>(dw, p, n, ring);
+        gemm_body<Floats<BF16>, kFormTN, AG_ACT_NONE, C>(dw, p, n, ring);
         __syncthreads();
-        gemm_body<BF16, kFormNN, AG_ACT_NONE, C>(dx, p, n, ring);
+        gemm_body<Floats<BF16>, kFormNN, AG_ACT_NONE, C>(dx, p, n, ring);
     }
     bias_grads_after(db, p, n, ring);
 }
@@ -798,8 +862,8 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_grads_kernel(LinearGemmArg
 {
     __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS];
     const int p = blockIdx.x;
-    if (p < dx_programs) gemm_body<BF16, kFormNN, AG_ACT_NONE, C>(dx, p, dx_programs, ring);
-    else if (p < dx_programs + dw_programs) gemm_body<BF16, kFormTN, AG_ACT_NONE, C>(dw, p - dx_programs, dw_programs, ring);
+    if (p < dx_programs) gemm_body<Floats<BF16>, kFormNN, AG_ACT_NONE, C>(dx, p, dx_programs, ring);
+    else if (p < dx_programs + dw_programs) gemm_body<Floats<BF16>, kFormTN, AG_ACT_NONE, C>(dw, p - dx_programs, dw_programs, ring);
     else bias_grad_body(db, p - dx_programs - dw_programs, reinterpret_cast<float*>(ring));
 }
 

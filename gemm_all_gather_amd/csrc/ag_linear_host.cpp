@@ -32,15 +32,17 @@ ag_status_t check_sizes(int64_t M, int64_t N, int64_t K, int dtype, int act)
 struct Operand {
     uint64_t at;
     int64_t ld, rows, cols;      // as stored
+    int esize = 2;
     bool pack = false;
     uint64_t copy_offset = 0;
-    int64_t copy_ld() const { return (cols + 7) / 8 * 8; }
-    uint64_t copy_bytes() const { return up256(static_cast<uint64_t>(rows) * copy_ld() * 2); }
+    int64_t copy_ld() const { return (cols * esize + 15) / 16 * 16 / esize; }
+    uint64_t copy_bytes() const { return up256(static_cast<uint64_t>(rows) * copy_ld() * esize); }
 };
 
 struct Product {
     bool on = false;
     bool stream = false;
+    bool i8 = false;             // 8-bit integers: stages of 128
     int form = ag::kFormNT, tile = ag::kLinearTile128;
     int64_t I = 0, J = 0, R = 0;
     int64_t tiles_i = 0, tiles_j = 0, stages = 0;
@@ -50,6 +52,7 @@ struct Product {
     double us = 0;               // estimated
     uint64_t partial_bytes = 0;
     int launches() const { return !on ? 0 : join ? 2 : 1; }
+    int64_t stage() const { return i8 ? 128 : 64; }
 };
 
 // What a workgroup's 64-wide step measured in long products on all CUs (before a stage's loads lay over both its halves,
@@ -60,6 +63,8 @@ struct Kind {
 constexpr Kind kKinds[ag::kLinearTiles] = {{{1.42, 1.46, 1.48}, 6.0},     // 256 x 256
                                            {{0.53, 0.60, 0.75}, 4.0},     // 128 x 128
                                            {{1.02, 0.98, 1.00}, 5.0}};    // 256 x 128
+constexpr Kind kKindsI8[ag::kLinearTiles] = {{{1.42, 0, 0}, 6.0}, {{0.53, 0, 0}, 4.0}, {{1.02, 0, 0}, 5.0}};   // 128-wide steps
+const Kind& kind_of(const Product& p, int tile) { return p.i8 ? kKindsI8[tile] : kKinds[tile]; }
 
 // Whole tiles of one kind; us is a tile's time.
 void whole_tiles(Product* p, int tile)
@@ -67,7 +72,7 @@ void whole_tiles(Product* p, int tile)
     int tm, tn, threads;
     ag::linear_tile_shape(tile, &tm, &tn, &threads);
     p->tile = tile;
-    p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
+    p->stages = std::max<int64_t>(1, (p->R + p->stage() - 1) / p->stage());
     p->tiles_i = (p->I + tm - 1) / tm;
     p->tiles_j = (p->J + tn - 1) / tn;
     p->full_tiles = p->programs = p->tiles_i * p->tiles_j;
@@ -76,7 +81,7 @@ void whole_tiles(Product* p, int tile)
     p->heavy = p->common_rounds = 0;
     p->join = false;
     p->partial_bytes = 0;
-    p->us = p->stages * kKinds[tile].step_us[p->form] + kKinds[tile].fixed_us;
+    p->us = p->stages * kind_of(*p, tile).step_us[p->form] + kind_of(*p, tile).fixed_us;
 }
 
 // Tile and cut with the shortest estimated time.  Whole rounds of tiles on all CUs go one to a workgroup; the
@@ -85,7 +90,7 @@ void whole_tiles(Product* p, int tile)
 ag_status_t choose(Product* p, int cus)
 {
     constexpr double kBytesPerUs = 4e6, kJoinUs = 5.0;
-    p->stages = std::max<int64_t>(1, (p->R + 63) / 64);
+    p->stages = std::max<int64_t>(1, (p->R + p->stage() - 1) / p->stage());
     double best = 0;
     bool found = false;
     for (int tile = 0; tile < ag::kLinearTiles; ++tile) {
@@ -94,8 +99,8 @@ ag_status_t choose(Product* p, int cus)
         const int64_t ti = (p->I + tm - 1) / tm, tj = (p->J + tn - 1) / tn;
         if (ti > 0x7fffffff || tj > 0x7fffffff || ti * tj > 0x7fffff00) continue;
         const int64_t tiles = ti * tj, rounds = tiles / cus;
-        const double step_us = kKinds[tile].step_us[p->form];
-        const double tile_us = p->stages * step_us + kKinds[tile].fixed_us;
+        const double step_us = kind_of(*p, tile).step_us[p->form];
+        const double tile_us = p->stages * step_us + kind_of(*p, tile).fixed_us;
         auto consider = [&](int64_t full, int64_t splits, int64_t run, double us) {
             if (found && us >= best) return;
             found = true;
@@ -121,7 +126,7 @@ ag_status_t choose(Product* p, int cus)
                 if (bytes > 512e6) break;
                 const double parts = static_cast<double>((tail * splits + cus - 1) / cus);
                 consider(keep * cus, splits, run,
-                         keep * tile_us + parts * (run * step_us + kKinds[tile].fixed_us) + kJoinUs + 2 * bytes / kBytesPerUs);
+                         keep * tile_us + parts * (run * step_us + kind_of(*p, tile).fixed_us) + kJoinUs + 2 * bytes / kBytesPerUs);
             }
         }
     }
@@ -157,7 +162,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
         out->variant = 1;
         out->tile_m = static_cast<int32_t>((p.I + 15) / 16 * 16);
         out->tile_n = 16;
-        out->tile_k = 128;
+        out->tile_k = static_cast<int32_t>(2 * p.stage());
         out->full_tiles = out->n_programs = static_cast<int32_t>((p.J + 15) / 16);
         out->splits = 1;
         return;
@@ -165,7 +170,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
     int threads;
     out->variant = 2;
     ag::linear_tile_shape(p.tile, &out->tile_m, &out->tile_n, &threads);
-    out->tile_k = 64;
+    out->tile_k = static_cast<int32_t>(p.stage());
     out->full_tiles = static_cast<int32_t>(p.full_tiles);
     out->splits = static_cast<int32_t>(p.splits);
     out->n_programs = static_cast<int32_t>(p.programs);
@@ -175,7 +180,7 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
 // Places the copies and partial sums in the workspace after `used` bytes.
 void place(Operand* o, uint64_t* used)
 {
-    o->pack = o->rows > 0 && o->cols > 0 && (o->at % 4 != 0 || (o->rows > 1 && o->ld % 2 != 0));
+    o->pack = o->rows > 0 && o->cols > 0 && (o->at % 4 != 0 || (o->rows > 1 && o->ld * o->esize % 4 != 0));
     if (!o->pack) return;
     o->copy_offset = *used;
     *used += o->copy_bytes();
@@ -220,6 +225,18 @@ ag::LinearGemmArgs gemm_args(const Product& p, const uint16_t* A, int64_t lda, c
     a.partial = partial;
     a.epi = epi;
     return a;
+}
+
+ag_status_t pack(const Operand& o, void* workspace, hipStream_t stream, const int8_t** at, int64_t* ld)
+{
+    *at = reinterpret_cast<const int8_t*>(o.at);
+    *ld = o.rows > 1 && !o.pack ? o.ld : o.copy_ld();
+    if (!o.pack) return AG_OK;
+    int8_t* dst = static_cast<int8_t*>(workspace) + o.copy_offset;
+    const hipError_t e = ag::launch_linear_i8_pack(*at, o.ld, dst, *ld, o.rows, o.cols, stream);
+    if (e != hipSuccess) return fail_hip(e, "linear operand copy");
+    *at = dst;
+    return AG_OK;
 }
 
 ag_status_t run_product(const Product& p, const ag::LinearGemmArgs& a, int bf16, hipStream_t stream)
@@ -282,6 +299,68 @@ ag_status_t plan_forward(const ag_linear_args_t* a, int cus, Forward* f)
         if ((s = choose(&p, cus)) != AG_OK) return s;
         f->ox = Operand{f->x.at, f->x.ld, M, K};
         f->ow = Operand{f->w.at, f->w.ld, N, K};
+        place(&f->ox, &f->workspace);
+        place(&f->ow, &f->workspace);
+        f->partial_offset = f->workspace;
+        f->workspace += p.partial_bytes;
+    }
+    f->launches = p.launches() + (f->ox.pack ? 1 : 0) + (f->ow.pack ? 1 : 0);
+    return AG_OK;
+}
+
+// ------------------------------------------------------------------ forward, 8-bit integers
+
+struct ForwardI8 {
+    Mat x, w, x_scale, w_scale, bias, residual, y, z;
+    Product product;
+    Operand ox, ow;
+    uint64_t partial_offset = 0, workspace = 0;
+    int launches = 0;
+};
+
+constexpr int64_t kMaxCodes = 131071;   // 131072 products of -128 and -128 are 2^31
+
+ag_status_t plan_forward_i8(const ag_linear_i8_args_t* a, int cus, ForwardI8* f)
+{
+    if (!a) return fail(AG_ERR_INVALID_ARG, "args is NULL");
+    for (int32_t r : a->reserved)
+        if (r != 0) return fail(AG_ERR_INVALID_ARG, "a reserved field is not 0");
+    ag_status_t s = check_sizes(a->M, a->N, a->K, a->dtype, a->act);
+    if (s != AG_OK) return s;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    if (K > kMaxCodes)
+        return fail(AG_ERR_UNSUPPORTED, "K %lld: sums of more than %lld products may leave 32 bits", static_cast<long long>(K),
+                    static_cast<long long>(kMaxCodes));
+    f->x = Mat{"x", addr(a->x), M, K, a->ldx ? a->ldx : K, 1};
+    f->w = Mat{"w", addr(a->w), N, K, a->ldw ? a->ldw : K, 1};
+    f->x_scale = Mat{"x_scale", addr(a->x_scale), 1, M, M, 4};
+    f->w_scale = Mat{"w_scale", addr(a->w_scale), 1, N, N, 4};
+    f->bias = Mat{"bias", addr(a->bias), 1, N, N, 2};
+    f->residual = Mat{"residual", addr(a->residual), M, N, a->ldr ? a->ldr : N, 2};
+    f->y = Mat{"y", addr(a->y), M, N, a->ldy ? a->ldy : N, 2};
+    f->z = Mat{"z", addr(a->z), M, N, a->ldz ? a->ldz : N, 2};
+    const bool some = M > 0 && N > 0;
+    for (const Mat* m : {&f->x, &f->w, &f->x_scale, &f->w_scale, &f->y})
+        if ((s = check_mat(*m, some)) != AG_OK) return s;
+    for (const Mat* m : {&f->bias, &f->residual, &f->z})
+        if ((s = check_mat(*m, false)) != AG_OK) return s;
+    if ((s = check_overlaps({f->x, f->w, f->x_scale, f->w_scale, f->bias}, {f->y, f->z})) != AG_OK) return s;
+    if (share(f->z, f->residual)) return fail(AG_ERR_INVALID_ARG, "z overlaps residual");
+    const bool in_place = f->y.at == f->residual.at && f->y.ld == f->residual.ld;
+    if (!in_place && share(f->y, f->residual)) return fail(AG_ERR_INVALID_ARG, "y overlaps residual without being it");
+    if (!some) return AG_OK;
+
+    Product& p = f->product;
+    p.on = p.i8 = true;
+    p.form = ag::kFormNT;
+    p.I = M;
+    p.J = N;
+    p.R = K;
+    p.stream = M <= 16 || (M <= ag::kLinearStreamRows && N * K < (int64_t{1} << 23));
+    if (!p.stream) {
+        if ((s = choose(&p, cus)) != AG_OK) return s;
+        f->ox = Operand{f->x.at, f->x.ld, M, K, 1};
+        f->ow = Operand{f->w.at, f->w.ld, N, K, 1};
         place(&f->ox, &f->workspace);
         place(&f->ow, &f->workspace);
         f->partial_offset = f->workspace;
@@ -495,6 +574,75 @@ ag_status_t ag_linear(const ag_linear_args_t* args, void* workspace, size_t work
     float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.partial_offset);
     s = run_product(f.product, gemm_args(f.product, A, lda, B, ldb, e, partial), bf16, stream);
     return s == AG_OK ? ok() : s;
+}
+
+ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_linear_plan_t* plan)
+{
+    if (!plan) return fail(AG_ERR_INVALID_ARG, "plan is NULL");
+    if (num_cus < 0) return fail(AG_ERR_INVALID_ARG, "num_cus %d < 0", num_cus);
+    ag_status_t s;
+    if (num_cus == 0 && (s = current_cus(&num_cus)) != AG_OK) return s;
+    ForwardI8 f;
+    if ((s = plan_forward_i8(args, num_cus, &f)) != AG_OK) return s;
+    ag_linear_plan_t p{};
+    report(f.product, f.ox.pack, f.ow.pack, &p.product);
+    const double M = static_cast<double>(args->M), N = static_cast<double>(args->N), K = static_cast<double>(args->K);
+    p.workspace_bytes = f.workspace;
+    if (f.product.on) {
+        p.bytes_read = static_cast<uint64_t>(M * K + N * K + 4 * (M + N) + 2 * ((args->bias ? N : 0) + (args->residual ? M * N : 0)));
+        p.bytes_written = static_cast<uint64_t>(2 * M * N * (args->z ? 2 : 1));
+        p.flops = 2 * M * N * K;
+    }
+    p.launches = f.launches;
+    *plan = p;
+    return ok();
+}
+
+ag_status_t ag_linear_i8(const ag_linear_i8_args_t* args, void* workspace, size_t workspace_bytes, void* stream_)
+{
+    int cus = 0;
+    ForwardI8 f;
+    ag_status_t s = plan_forward_i8(args, 256, &f);
+    if (s != AG_OK) return s;
+    if (!f.product.on) return ok();
+    if ((s = current_cus(&cus)) != AG_OK) return s;
+    if (cus != 256) {
+        f = ForwardI8{};
+        if ((s = plan_forward_i8(args, cus, &f)) != AG_OK) return s;
+    }
+    s = check_workspace(workspace, workspace_bytes, f.workspace, {f.x, f.w, f.x_scale, f.w_scale, f.bias, f.residual, f.y, f.z});
+    if (s != AG_OK) return s;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    const int bf16 = args->dtype == AG_BF16;
+    ag::LinearEpilogue e{};
+    e.bias = static_cast<const uint16_t*>(args->bias);
+    e.residual = static_cast<const uint16_t*>(args->residual);
+    e.z = static_cast<uint16_t*>(args->z);
+    e.out = args->y;
+    e.ldr = f.residual.ld;
+    e.ldz = f.z.ld;
+    e.ldo = f.y.ld;
+    e.act = args->act;
+    if (f.product.stream) {
+        const ag::LinearI8StreamArgs a{args->x, args->w, args->x_scale, args->w_scale, f.x.ld, f.w.ld, args->M, args->N, args->K, e};
+        const hipError_t err = ag::launch_linear_i8_stream(a, bf16, cus, stream);
+        return err == hipSuccess ? ok() : fail_hip(err, "linear stream");
+    }
+    const int8_t *A, *B;
+    int64_t lda, ldb;
+    if ((s = pack(f.ox, workspace, stream, &A, &lda)) != AG_OK) return s;
+    if ((s = pack(f.ow, workspace, stream, &B, &ldb)) != AG_OK) return s;
+    float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.partial_offset);
+    ag::LinearI8GemmArgs a{gemm_args(f.product, reinterpret_cast<const uint16_t*>(A), lda, reinterpret_cast<const uint16_t*>(B), ldb, e,
+                                     partial),
+                           args->x_scale, args->w_scale};
+    hipError_t err = ag::launch_linear_i8_gemm(a, bf16, f.product.tile, static_cast<int>(f.product.programs), stream);
+    if (err != hipSuccess) return fail_hip(err, "linear product");
+    if (f.product.join) {
+        err = ag::launch_linear_i8_join(a, bf16, f.product.tile, stream);
+        if (err != hipSuccess) return fail_hip(err, "linear join");
+    }
+    return ok();
 }
 
 ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int num_cus, ag_linear_plan_t* plan)

@@ -1,0 +1,229 @@
+// Kernels of the linear layer on 8-bit integers beside its tiled products: the join of cut tiles, the row-streaming form
+// for a few rows of x, copies to aligned rows, and the launchers.
+
+#include "ag_linear_device.h"
+
+namespace ag {
+namespace {
+
+// ---------------------------------------------------------------- join of cut tiles
+
+// Adds the parts of a tail tile, 8 consecutive columns per thread: sums of integers, exact in any order; then the epilogue.
+// Bound by memory as the join of 16-bit products.
+template <bool BF16>
+__global__ __launch_bounds__(256) void ag_linear_i8_join_kernel(LinearI8GemmArgs a, int tm, int tn)
+{
+    const int per_tile = tm * tn / 2048;           // workgroups
+    const int tail_tile = static_cast<int>(blockIdx.x) / per_tile;
+    const int id = (static_cast<int>(blockIdx.x) % per_tile) * 256 + threadIdx.x;
+    const int tile_row = id / (tn / 8), tile_col = (id % (tn / 8)) * 8;
+    int64_t row, col;
+    place_tile(a, a.full_tiles + tail_tile, tm, tn, &row, &col);
+    row += tile_row;
+    col += tile_col;
+    if (row >= a.I || col >= a.J) return;
+    uint32_t s[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    const int64_t part = static_cast<int64_t>(a.tiles_i * a.tiles_j - a.full_tiles) * (tm * tn);
+    const float* from = a.partial + static_cast<int64_t>(tail_tile) * (tm * tn) + tile_row * tn + tile_col;
+#pragma unroll 4
+    for (int q = 0; q < a.splits; ++q, from += part) {
+        const u32x4* src = reinterpret_cast<const u32x4*>(from);
+        const u32x4 lo = src[0], hi = src[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] += lo[e];
+            s[4 + e] += hi[e];
+        }
+    }
+    const int n = static_cast<int>(min(int64_t{8}, a.J - col));
+    float v[8], scale[8], bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(s[e]);
+    load_scales(scale, a.col_scale + col, n);
+    apply_scales(v, a.row_scale[row], scale);
+    if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
+    finish_layer<BF16>(v, bias, a.epi, a.epi.act, row, col, n);
+}
+
+// ---------------------------------------------------------------- a few rows of x
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(1))) AnyBytes16 { i32x4 v; };
+
+__device__ __forceinline__ i32x4 load16(const int8_t* p) { return reinterpret_cast<const AnyBytes16*>(p)->v; }
+__device__ __forceinline__ i32x4 load16(const int8_t* p, int64_t left)
+{
+    if (left >= 16) return load16(p);
+    i32x4 t = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < left) t[e >> 2] |= static_cast<int>(static_cast<uint32_t>(static_cast<uint8_t>(p[e])) << (8 * (e & 3)));
+    return t;
+}
+
+// y for up to 16 MB rows of x: the weights are streamed once, straight into matrix-instruction fragments, 16 rows of w per
+// workgroup.  The workgroup's waves share the reduction, 256 wide at a time, and add up through LDS; D rows are rows of
+// w, D columns rows of x.  Bound by the stream of w and the start and end of a launch.
+template <bool BF16, int MB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI8StreamArgs a)
+{
+    __shared__ i32x4 part[WAVES][MB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t row = min(n0 + (lane & 15), a.N - 1);     // rows past N repeat the last one and are not stored
+    const int k_lane = (lane >> 4) * 16;
+    const int8_t* w = a.w + row * a.ldw + k_lane;
+    const int8_t* x[MB];
+    bool live[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const int64_t m = b * 16 + (lane & 15);
+        live[b] = m < a.M;
+        x[b] = a.x + (live[b] ? m : 0) * a.ldx + k_lane;
+    }
+    i32x4 acc[MB];
+    const i32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[b] = zero;
+
+    struct Block {
+        i32x4 w[4], x[MB][4];
+    };
+    auto load = [&](Block& t, int64_t k) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t.w[u] = load16(w + k + u * 64);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                t.x[b][u] = zero;
+                if (live[b]) t.x[b][u] = load16(x[b] + k + u * 64);
+            }
+    };
+    auto multiply = [&](const Block& t) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.w[u], t.x[b][u], acc[b], 0, 0, 0);
+    };
+    // two 256-wide blocks on their way per wave while a third is multiplied
+    constexpr int64_t NEXT = WAVES * 256;
+    const int64_t whole = a.K / 256 * 256;
+    int64_t k = wave * 256;
+    Block even, odd;
+    if (k < whole) load(even, k);
+    for (; k < whole; k += 2 * NEXT) {
+        const bool more = k + NEXT < whole;
+        if (more) load(odd, k + NEXT);
+        multiply(even);
+        if (k + 2 * NEXT < whole) load(even, k + 2 * NEXT);
+        if (more) multiply(odd);
+    }
+    if (whole < a.K && wave == (whole / 256) % WAVES) {   // the last, shorter block
+        k = whole;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t left = a.K - k - u * 64 - k_lane;
+            const i32x4 fw = load16(w + k + u * 64, left);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                const i32x4 fx = live[b] ? load16(x[b] + k + u * 64, left) : zero;
+                acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, fx, acc[b], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[b];
+    __syncthreads();
+    // one thread per row of x and 4 rows of w
+    const int tid = threadIdx.x;
+    if (tid < MB * 64) {
+        const int b = tid >> 6, l = tid & 63;
+        i32x4 s = part[0][b][l];
+#pragma unroll
+        for (int wv = 1; wv < WAVES; ++wv) s += part[wv][b][l];
+        const int64_t m = b * 16 + (l & 15), col = n0 + (l >> 4) * 4;
+        const int n = static_cast<int>(max(int64_t{0}, min(int64_t{4}, a.N - col)));
+        if (m < a.M && n > 0) {
+            float v[8] = {}, scale[8], bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __int_as_float(s[e]);
+            load_scales(scale, a.w_scale + col, n);
+            apply_scales(v, a.x_scale[m], scale);
+            if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
+            finish_layer<BF16>(v, bias, a.epi, a.epi.act, m, col, n);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- rows to aligned rows
+
+// A matrix's rows to rows of 16-byte multiples, for operands that do not start on 4 bytes or have other strides.
+__global__ __launch_bounds__(256) void ag_linear_i8_pack_kernel(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst,
+                                                                int64_t rows, int64_t cols)
+{
+    const int64_t per_row = (cols + 15) / 16;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t row = id / per_row, col = (id - row * per_row) * 16;
+    if (row >= rows) return;
+    *reinterpret_cast<i32x4*>(dst + row * ld_dst + col) = load16(src + row * ld_src + col, cols - col);
+}
+
+using StreamFn = void (*)(LinearI8StreamArgs);
+template <bool BF16, int MB> StreamFn pick_stream(bool wide)
+{
+    return wide ? ag_linear_i8_stream_kernel<BF16, MB, 16> : ag_linear_i8_stream_kernel<BF16, MB, 8>;
+}
+
+bool grid_of(int64_t work, int64_t per, dim3* grid)
+{
+    const int64_t g = (work + per - 1) / per;
+    if (g < 1 || g > 0x7fffffff) return false;
+    *grid = dim3(static_cast<uint32_t>(g));
+    return true;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launchers
+
+hipError_t launch_linear_i8_gemm(const LinearI8GemmArgs& a, int bf16, int tile, int programs, hipStream_t stream)
+{
+    const LinearI8GemmFn fn = bf16 ? linear_i8_bf16(a.epi.act, tile) : linear_i8_f16(a.epi.act, tile);
+    if (fn == nullptr || programs < 1 || a.stages < 1 || a.splits < 1 || a.split_stages < 1) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(Cfg256::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_i8_join(const LinearI8GemmArgs& a, int bf16, int tile, hipStream_t stream)
+{
+    int tm, tn, threads;
+    linear_tile_shape(tile, &tm, &tn, &threads);
+    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j - a.full_tiles;
+    dim3 grid;
+    if (!grid_of(tiles * (tm * tn / 2048), 1, &grid)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((bf16 ? ag_linear_i8_join_kernel<true> : ag_linear_i8_join_kernel<false>), grid, dim3(256), 0, stream, a, tm, tn);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cus, hipStream_t stream)
+{
+    dim3 grid;
+    if (a.M < 1 || a.M > kLinearStreamRows || !grid_of(a.N, 16, &grid)) return hipErrorInvalidValue;
+    const bool wide = static_cast<int64_t>(grid.x) <= cus;
+    const StreamFn fn = a.M <= 16 ? (bf16 ? pick_stream<true, 1>(wide) : pick_stream<false, 1>(wide))
+                                  : (bf16 ? pick_stream<true, 2>(wide) : pick_stream<false, 2>(wide));
+    hipLaunchKernelGGL(fn, grid, dim3(wide ? 1024 : 512), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_i8_pack(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst, int64_t rows, int64_t cols,
+                                 hipStream_t stream)
+{
+    dim3 grid;
+    if (!grid_of(rows * ((cols + 15) / 16), 256, &grid)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ag_linear_i8_pack_kernel, grid, dim3(256), 0, stream, src, ld_src, dst, ld_dst, rows, cols);
+    return hipGetLastError();
+}
+
+}  // namespace ag

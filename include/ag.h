@@ -702,6 +702,37 @@ ag_status_t ag_rms_norm_backward(const ag_rms_norm_backward_args_t* args, void* 
 ag_status_t ag_plan_rms_norm_backward(const ag_rms_norm_backward_args_t* args, int num_cus, ag_rows_plan_t* plan);
 
 /* ------------------------------------------------------------------------
+ * Linear layer on 8-bit integers with a scale for each row of x (token) and
+ * of w (output channel), as ag_quantize_rows or ag_rms_norm make them:
+ *
+ *   z = x_scale[m] w_scale[n] sum_k x(m,k) w(n,k) + bias
+ *   y = act(z) + residual                    (fp32, rounded once to dtype)
+ *
+ * The sums are exact (int32).  x is M x K, w N x K, both int8; K up to 131071
+ * (131072 products of -128 and -128 would leave int32).  bias, residual, y
+ * and z have dtype (AG_F16 or AG_BF16).  Everything else is as for ag_linear;
+ * operands of a tiled product whose rows do not start on 4 bytes are copied.
+ * ------------------------------------------------------------------------ */
+typedef struct ag_linear_i8_args {
+    const int8_t* x;
+    const int8_t* w;
+    const float* x_scale;  /* M */
+    const float* w_scale;  /* N */
+    const void* bias;
+    const void* residual;
+    void* y;
+    void* z;
+    int64_t ldx, ldw, ldr, ldy, ldz;
+    int64_t M, N, K;
+    int32_t dtype;        /* ag_dtype_t */
+    int32_t act;          /* ag_act_t */
+    int32_t reserved[6];  /* must be 0 */
+} ag_linear_i8_args_t;
+
+ag_status_t ag_linear_i8(const ag_linear_i8_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
+ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_linear_plan_t* plan);
+
+/* ------------------------------------------------------------------------
  * AdamW over many tensors in one launch, with states in 32 or in 8 bits.
  * A handle keeps a device table of the tensors' addresses, made once (as a
  * heap keeps its base table); the tensors must stay where they are while the
