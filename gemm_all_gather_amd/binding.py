@@ -201,6 +201,8 @@ _SIGNATURES = {
     "ag_plan_linear": [ctypes.POINTER(LinearArgs), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _vp, _c_size, _vp],
     "ag_plan_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_linear_backward_q8": [ctypes.POINTER(LinearBackwardArgs), _vp, _vp, _vp, _c_size, _vp],
+    "ag_plan_linear_backward_q8": [ctypes.POINTER(LinearBackwardArgs), _vp, _vp, _c_int, ctypes.POINTER(LinearPlan)],
     "ag_linear_i8": [ctypes.POINTER(LinearI8Args), _vp, _c_size, _vp],
     "ag_plan_linear_i8": [ctypes.POINTER(LinearI8Args), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_quantize_rows": [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp],
@@ -559,6 +561,36 @@ def dequantize_rows(q, scale, y, M, K, dtype, ldq=0, ldy=0, stream=None) -> None
     d = _dtype(dtype)
     _check(lib().ag_dequantize_rows(_operand(q, "int8", "q"), ldq, _operand(scale, AG_F32, "scale"), _operand(y, d, "y"), ldy, M,
                                     K, d, _stream(stream)), "ag_dequantize_rows")
+
+
+def _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw, dw_dtype,
+                      accumulate):
+    d = _dtype(dtype)
+    g = d if dw_dtype is None else _dtype(dw_dtype)
+    a = LinearBackwardArgs(_operand(dy, d, "dy"), _operand(z, d if z_scale is None else "int8", "z"),
+                           _operand(x, d if x_scale is None else "int8", "x"), _operand(w, d, "w"), _operand(dx, d, "dx"),
+                           _operand(dw, g, "dw"), _operand(db, g, "db"), lddy, ldz, ldx, ldw, lddx, lddw, M, N, K, d, _act(act), g,
+                           int(accumulate))
+    return a, _operand(x_scale, AG_F32, "x_scale"), _operand(z_scale, AG_F32, "z_scale")
+
+
+def plan_linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", z=None, z_scale=None, dx=None, dw=None, db=None,
+                            lddy=0, ldx=0, ldw=0, ldz=0, lddx=0, lddw=0, dw_dtype=None, accumulate=False, num_cus=0) -> LinearPlan:
+    p = LinearPlan()
+    a, xs, zs = _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw,
+                                  dw_dtype, accumulate)
+    _check(lib().ag_plan_linear_backward_q8(ctypes.byref(a), xs, zs, num_cus, ctypes.byref(p)), "ag_plan_linear_backward_q8")
+    return p
+
+
+def linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", z=None, z_scale=None, dx=None, dw=None, db=None, lddy=0,
+                       ldx=0, ldw=0, ldz=0, lddx=0, lddw=0, dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
+    """linear_backward from activations kept in 8 bits: x holds codes where x_scale is given, z where z_scale is
+    (ag_linear_backward_q8)."""
+    a, xs, zs = _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw,
+                                  dw_dtype, accumulate)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_linear_backward_q8(ctypes.byref(a), xs, zs, ws, nbytes, _stream(stream)), "ag_linear_backward_q8")
 
 
 def _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq) -> RmsNormArgs:

@@ -117,6 +117,14 @@ struct LinearSlopeArgs {
     int32_t rows;               // of one workgroup and partial column sum
 };
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
+// The same from activations in 8 bits: z holds codes where z_scale is not null, and dz_fold, where x_scale is not null, receives
+// dz times the scale's factor in [1/2, 1) (split_scale), rounded; dz_rest is then what that rounding leaves.
+struct LinearSlopeQ8Args : LinearSlopeArgs {
+    const float* x_scale;
+    const float* z_scale;
+    uint16_t* dz_fold;
+};
+hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, int bf16, hipStream_t stream);
 hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream);
 
 using LinearInTurnFn = void (*)(LinearGemmArgs, LinearGemmArgs, LinearBiasGradArgs);

@@ -9,6 +9,7 @@
 #include "ag.h"
 #include "ag_linear.h"
 #include "ag_matrix.h"
+#include "ag_rows.h"
 #include "ag_status.h"
 
 namespace {
@@ -373,20 +374,22 @@ ag_status_t plan_forward_i8(const ag_linear_i8_args_t* a, int cus, ForwardI8* f)
 // ------------------------------------------------------------------ backward
 
 struct Backward {
-    Mat dy, z, x, w, dx, dw, db;
+    Mat dy, z, x, w, dx, dw, db, x_scale, z_scale;
     Product px, pw;
     Product rest;               // dw of dz's second term, before pw
     Operand ox, ow;
     bool slope = false, store_dz = false;
+    bool fold = false;          // dw takes dz times its row's x_scale (but for a power of two), dx takes dz
     bool together = false;      // dx, dw and db in one launch, side by side
     bool in_turn = false, dx_first = false;   // or one after the other
     bool db_alone = false;      // db in a launch of its own; else beside a product
-    uint64_t dz_offset = 0, dz_rest_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
+    uint64_t dz_offset = 0, dz_fold_offset = 0, dz_rest_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
     int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
 };
 
-ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward* b)
+// x_scale, z_scale: x and z are 8-bit codes where they are not null.
+ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_scale, const float* z_scale, int cus, Backward* b)
 {
     if (!a) return fail(AG_ERR_INVALID_ARG, "args is NULL");
     for (int32_t r : a->reserved)
@@ -399,9 +402,11 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
     const int64_t M = a->M, N = a->N, K = a->K;
     const int g = a->dw_dtype == AG_F32 ? 4 : 2;
     b->dy = Mat{"dy", addr(a->dy), M, N, a->lddy ? a->lddy : N, 2};
-    b->z = Mat{"z", addr(a->z), M, N, a->ldz ? a->ldz : N, 2};
-    b->x = Mat{"x", addr(a->x), M, K, a->ldx ? a->ldx : K, 2};
+    b->z = Mat{"z", addr(a->z), M, N, a->ldz ? a->ldz : N, z_scale ? 1 : 2};
+    b->x = Mat{"x", addr(a->x), M, K, a->ldx ? a->ldx : K, x_scale ? 1 : 2};
     b->w = Mat{"w", addr(a->w), N, K, a->ldw ? a->ldw : K, 2};
+    b->x_scale = Mat{"x_scale", addr(x_scale), 1, M, M, 4};
+    b->z_scale = Mat{"z_scale", addr(z_scale), 1, M, M, 4};
     b->dx = Mat{"dx", addr(a->dx), M, K, a->lddx ? a->lddx : K, 2};
     b->dw = Mat{"dw", addr(a->dw), N, K, a->lddw ? a->lddw : K, g};
     b->db = Mat{"db", addr(a->db), 1, N, N, g};
@@ -411,17 +416,18 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
     if ((s = check_mat(b->z, any && a->act != AG_ACT_NONE)) != AG_OK) return s;
     if ((s = check_mat(b->x, want_dw)) != AG_OK) return s;
     if ((s = check_mat(b->w, want_dx)) != AG_OK) return s;
-    for (const Mat* m : {&b->dx, &b->dw, &b->db})
+    for (const Mat* m : {&b->dx, &b->dw, &b->db, &b->x_scale, &b->z_scale})
         if ((s = check_mat(*m, false)) != AG_OK) return s;
-    if ((s = check_overlaps({b->dy, b->z, b->x, b->w}, {b->dx, b->dw, b->db})) != AG_OK) return s;
+    if ((s = check_overlaps({b->dy, b->z, b->x, b->w, b->x_scale, b->z_scale}, {b->dx, b->dw, b->db})) != AG_OK) return s;
     if (!any) return AG_OK;
 
     const bool act = a->act != AG_ACT_NONE;
     uint64_t used = 0;
     if (M > 0 && N > 0) {
         const bool aligned = b->dy.at % 4 == 0 && (M == 1 || b->dy.ld % 2 == 0);
-        b->store_dz = (want_dx || want_dw) && (act || !aligned);
-        b->slope = b->store_dz || want_db;
+        b->fold = want_dw && x_scale;
+        b->store_dz = (want_dx || (want_dw && !b->fold)) && (act || !aligned);
+        b->slope = b->store_dz || b->fold || want_db;
     }
     b->lddz = (N + 7) / 8 * 8;
     // about 1024 workgroups of 256 columns: enough for every CU, and few partial sums of a long column
@@ -430,12 +436,17 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         b->dz_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
     }
+    if (b->fold) {
+        b->dz_fold_offset = used;
+        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
+    }
     // A weight gradient in fp32 takes dz in two 16-bit terms and so two products: with one it would carry the error
     // of a 16-bit gradient (2-norm relative to dw's 1.7e-3 in bf16, 2.1e-4 in fp16; with two 2.5e-6 and 3.5e-7, as
     // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 to 2290 us against 1468
     // to 1490 of a bf16 dw, of 1024 rows 231 against 122.  dx and a 16-bit dw take one term: their own rounding is as
     // large (2.3e-3 in all against 1.7e-3), and two would double the time of both products.  relu's dz needs no rounding.
-    const bool two_terms = b->store_dz && want_dw && act && a->act != AG_ACT_RELU && a->dw_dtype == AG_F32;
+    // With a row's scale in it, every dz does.
+    const bool two_terms = want_dw && a->dw_dtype == AG_F32 && (b->fold || (b->store_dz && act && a->act != AG_ACT_RELU));
     if (two_terms) {
         b->dz_rest_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
@@ -465,7 +476,13 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, int cus, Backward*
         b->pw.R = M;
         if ((s = choose(&b->pw, cus)) != AG_OK) return s;
         b->ox = Operand{b->x.at, b->x.ld, M, K};
-        place(&b->ox, &used);
+        if (b->fold) {      // the codes times the scales' powers of two, in 16 bits
+            b->ox.pack = true;
+            b->ox.copy_offset = used;
+            used += b->ox.copy_bytes();
+        } else {
+            place(&b->ox, &used);
+        }
         if (two_terms) b->rest = b->pw;
     }
     // Both products' 128 x 128 tiles on CUs of their own: one launch for what follows dz.
@@ -645,14 +662,15 @@ ag_status_t ag_linear_i8(const ag_linear_i8_args_t* args, void* workspace, size_
     return ok();
 }
 
-ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int num_cus, ag_linear_plan_t* plan)
+ag_status_t ag_plan_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
+                                       int num_cus, ag_linear_plan_t* plan)
 {
     if (!plan) return fail(AG_ERR_INVALID_ARG, "plan is NULL");
     if (num_cus < 0) return fail(AG_ERR_INVALID_ARG, "num_cus %d < 0", num_cus);
     ag_status_t s;
     if (num_cus == 0 && (s = current_cus(&num_cus)) != AG_OK) return s;
     Backward b;
-    if ((s = plan_backward(args, num_cus, &b)) != AG_OK) return s;
+    if ((s = plan_backward(args, x_scale, z_scale, num_cus, &b)) != AG_OK) return s;
     ag_linear_plan_t p{};
     report(b.px, false, b.ow.pack, &p.product);
     report(b.pw, false, b.ox.pack, &p.product_dw);
@@ -661,7 +679,8 @@ ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int n
     const int g = args->dw_dtype == AG_F32 ? 4 : 2;
     if (dx || dw || db) {
         const double grads = ((dw ? N * K : 0) + (db ? N : 0)) * g;
-        p.bytes_read = static_cast<uint64_t>(2 * (M * N * (args->act != AG_ACT_NONE ? 2 : 1) + (dw ? M * K : 0) + (dx ? N * K : 0)) +
+        p.bytes_read = static_cast<uint64_t>(2 * M * N + (args->act != AG_ACT_NONE ? b.z.esize * M * N + (z_scale ? 4 * M : 0) : 0) +
+                                             (dw ? b.x.esize * M * K + (x_scale ? 4 * M : 0) : 0) + 2 * (dx ? N * K : 0) +
                                              (args->accumulate ? grads : 0));
         p.bytes_written = static_cast<uint64_t>(2 * (dx ? M * K : 0) + grads);
         p.flops = 2 * M * N * K * ((dx ? 1 : 0) + (dw ? 1 : 0));
@@ -672,30 +691,42 @@ ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int n
     return ok();
 }
 
-ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* workspace, size_t workspace_bytes, void* stream_)
+ag_status_t ag_plan_linear_backward(const ag_linear_backward_args_t* args, int num_cus, ag_linear_plan_t* plan)
+{
+    return ag_plan_linear_backward_q8(args, nullptr, nullptr, num_cus, plan);
+}
+
+ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return ag_linear_backward_q8(args, nullptr, nullptr, workspace, workspace_bytes, stream);
+}
+
+ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
+                                  void* workspace, size_t workspace_bytes, void* stream_)
 {
     int cus = 0;
     Backward b;
-    ag_status_t s = plan_backward(args, 256, &b);
+    ag_status_t s = plan_backward(args, x_scale, z_scale, 256, &b);
     if (s != AG_OK) return s;
     if (b.launches == 0) return ok();
     if ((s = current_cus(&cus)) != AG_OK) return s;
     if (cus != 256) {
         b = Backward{};
-        if ((s = plan_backward(args, cus, &b)) != AG_OK) return s;
+        if ((s = plan_backward(args, x_scale, z_scale, cus, &b)) != AG_OK) return s;
     }
-    s = check_workspace(workspace, workspace_bytes, b.workspace, {b.dy, b.z, b.x, b.w, b.dx, b.dw, b.db});
+    s = check_workspace(workspace, workspace_bytes, b.workspace, {b.dy, b.z, b.x, b.w, b.dx, b.dw, b.db, b.x_scale, b.z_scale});
     if (s != AG_OK) return s;
     const hipStream_t stream = static_cast<hipStream_t>(stream_);
     const int bf16 = args->dtype == AG_BF16;
     char* ws = static_cast<char*>(workspace);
     float* sums = reinterpret_cast<float*>(ws + b.sums_offset);
     float* partial = reinterpret_cast<float*>(ws + b.partial_offset);
+    uint16_t* dz_fold = reinterpret_cast<uint16_t*>(ws + b.dz_fold_offset);
     const bool want_db = !b.db.empty();
     const uint16_t* dz = static_cast<const uint16_t*>(args->dy);
     int64_t lddz = args->M == 1 ? b.lddz : b.dy.ld;     // one row may have any stride
     if (b.slope) {
-        ag::LinearSlopeArgs a{};
+        ag::LinearSlopeQ8Args a{};
         a.dy = static_cast<const uint16_t*>(args->dy);
         a.z = args->act != AG_ACT_NONE ? static_cast<const uint16_t*>(args->z) : nullptr;
         a.dz = b.store_dz ? reinterpret_cast<uint16_t*>(ws + b.dz_offset) : nullptr;
@@ -708,7 +739,10 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         a.N = args->N;
         a.act = args->act;
         a.rows = static_cast<int32_t>(b.rows);
-        const hipError_t e = ag::launch_linear_slope(a, bf16, stream);
+        a.dz_fold = b.fold ? dz_fold : nullptr;
+        a.x_scale = b.fold ? x_scale : nullptr;
+        a.z_scale = a.z ? z_scale : nullptr;
+        const hipError_t e = a.x_scale || a.z_scale ? ag::launch_linear_slope_q8(a, bf16, stream) : ag::launch_linear_slope(a, bf16, stream);
         if (e != hipSuccess) return fail_hip(e, "linear slope");
         if (b.store_dz) {
             dz = a.dz;
@@ -737,7 +771,18 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
     if (b.pw.on) {
         const uint16_t* X;
         int64_t ldx;
-        if ((s = pack(b.ox, workspace, stream, &X, &ldx)) != AG_OK) return s;
+        if (b.fold) {
+            X = reinterpret_cast<const uint16_t*>(ws + b.ox.copy_offset);
+            ldx = b.ox.copy_ld();
+            const ag::DequantizeArgs a{static_cast<const int8_t*>(args->x), x_scale, ws + b.ox.copy_offset, b.x.ld, ldx, args->M,
+                                       static_cast<int32_t>(args->K), 1};
+            const hipError_t e = ag::launch_dequantize(a, args->dtype, stream);
+            if (e != hipSuccess) return fail_hip(e, "linear operand of codes");
+        } else if ((s = pack(b.ox, workspace, stream, &X, &ldx)) != AG_OK) {
+            return s;
+        }
+        const uint16_t* dzw = b.fold ? dz_fold : dz;
+        const int64_t lddzw = b.fold ? b.lddz : lddz;
         ag::LinearEpilogue e{};
         e.out = args->dw;
         e.ldo = b.dw.ld;
@@ -745,10 +790,10 @@ ag_status_t ag_linear_backward(const ag_linear_backward_args_t* args, void* work
         e.accumulate = args->accumulate;
         if (b.rest.on) {    // the small term first, on the earlier gradient if there is one; the other adds to it
             const uint16_t* dz_rest = reinterpret_cast<const uint16_t*>(ws + b.dz_rest_offset);
-            if ((s = run_product(b.rest, gemm_args(b.rest, dz_rest, lddz, X, ldx, e, partial), bf16, stream)) != AG_OK) return s;
+            if ((s = run_product(b.rest, gemm_args(b.rest, dz_rest, b.lddz, X, ldx, e, partial), bf16, stream)) != AG_OK) return s;
             e.accumulate = 1;
         }
-        dw = gemm_args(b.pw, dz, lddz, X, ldx, e, partial);
+        dw = gemm_args(b.pw, dzw, lddzw, X, ldx, e, partial);
     }
     if (b.together) {
         const hipError_t e = ag::launch_linear_grads(dx, dw, static_cast<int>(b.px.programs), static_cast<int>(b.pw.programs), db,

@@ -1,0 +1,97 @@
+// The activation's gradient from activations that were kept in 8 bits.
+
+#include "ag_linear_device.h"
+#include "ag_scale.h"
+
+namespace ag {
+namespace {
+
+// dz = dy act'(z), where z may be codes, rounded for dx; dz times the factor in [1/2, 1) of its row's x_scale, rounded for dw
+// (x's codes times the scale's power of two are exact in 16 bits), with what that rounding leaves; and the column sums
+// of the unrounded dz over a.rows rows.  Threads and sums as in the kernel without codes.
+template <bool BF16, bool REST, bool X8, bool Z8>
+__global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a)
+{
+    __shared__ float part[8][264];
+    const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const uint32_t col_blocks = static_cast<uint32_t>((a.N + 255) / 256);
+    const int64_t bx = blockIdx.x % col_blocks, by = blockIdx.x / col_blocks;
+    const int64_t col = (bx * 32 + c) * 8;
+    const int64_t row0 = by * a.rows;
+    const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.N - col)));
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (n > 0) {
+#pragma unroll 4
+        for (int i = rl; i < a.rows; i += 8) {
+            const int64_t row = row0 + i;
+            if (row >= a.M) break;
+            float v[8];
+            load_f32<BF16>(v, a.dy + row * a.lddy + col, n);
+            if (a.z) {
+                float z[8];
+                if constexpr (Z8) {
+                    const float s = a.z_scale[row];
+                    load_codes(z, reinterpret_cast<const int8_t*>(a.z) + row * a.ldz + col, n);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] *= s;
+                } else {
+                    load_f32<BF16>(z, a.z + row * a.ldz + col, n);
+                }
+                apply_slope(v, z, a.act);
+            }
+            if (a.dz) store_16<BF16>(a.dz + row * a.lddz + col, v, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += v[e];
+            if constexpr (X8) {
+                float power, rest;
+                split_scale<BF16>(a.x_scale[row], &power, &rest);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= rest;
+                store_16<BF16>(a.dz_fold + row * a.lddz + col, v, n);
+            }
+            if constexpr (REST) {
+                float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float kept = to_f32<BF16>(from_f32<BF16>(v[e]));
+                    rest[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
+                }
+                store_16<BF16>(a.dz_rest + row * a.lddz + col, rest, n);
+            }
+        }
+    }
+    if (a.sums) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[rl][c * 8 + e] = sum[e];
+        __syncthreads();
+        const int64_t out = bx * 256 + threadIdx.x;
+        if (out < a.N) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s += part[r][threadIdx.x];
+            a.sums[by * a.N + out] = s;
+        }
+    }
+}
+
+using SlopeFn = void (*)(LinearSlopeQ8Args);
+template <bool BF16, bool REST> SlopeFn pick(bool x8, bool z8)
+{
+    return x8 ? (z8 ? ag_linear_slope_q8_kernel<BF16, REST, true, true> : ag_linear_slope_q8_kernel<BF16, REST, true, false>)
+              : ag_linear_slope_q8_kernel<BF16, REST, false, true>;
+}
+
+}  // namespace
+
+hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, int bf16, hipStream_t stream)
+{
+    const int64_t groups = a.rows < 1 ? 0 : (a.N + 255) / 256 * ((a.M + a.rows - 1) / a.rows);
+    if (groups < 1 || groups > 0x7fffffff || (!a.x_scale && !a.z_scale) || (a.x_scale && !a.dz_fold)) return hipErrorInvalidValue;
+    const bool x8 = a.x_scale != nullptr, z8 = a.z_scale != nullptr;
+    const SlopeFn fn = a.dz_rest ? (bf16 ? pick<true, true>(x8, z8) : pick<false, true>(x8, z8))
+                        : (bf16 ? pick<true, false>(x8, z8) : pick<false, false>(x8, z8));
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace ag

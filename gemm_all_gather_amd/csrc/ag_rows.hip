@@ -12,8 +12,6 @@ namespace {
 
 // ---------------------------------------------------------------- rows and codes
 
-struct __attribute__((packed, aligned(1))) Any8 { u32x2 v; };
-
 // n <= 8 elements from p on, the others 0.
 template <int DTYPE>
 __device__ __forceinline__ void load_row(float (&v)[8], const void* p, int64_t at, int n)
@@ -277,22 +275,10 @@ __global__ __launch_bounds__(256) void ag_dequantize_kernel(DequantizeArgs a)
     for (int half = 0; half < 2; ++half) {
         const int n = a.K - col - 8 * half;
         if (n <= 0) break;
-        uint32_t lo = 0, hi = 0;
-        if (n >= 8) {
-            const u32x2 t = reinterpret_cast<const Any8*>(q + 8 * half)->v;
-            lo = t.x;
-            hi = t.y;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t c = e < n ? static_cast<uint8_t>(q[8 * half + e]) : 0u;
-                if (e < 4) lo |= c << (8 * e);
-                else hi |= c << (8 * (e - 4));
-            }
-        }
         float v[8];
+        load_codes(v, q + 8 * half, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(static_cast<int8_t>((e < 4 ? lo >> (8 * e) : hi >> (8 * (e - 4))) & 255u)) * s;
+        for (int e = 0; e < 8; ++e) v[e] *= s;
         const int64_t at = row * a.ldy + col + 8 * half;
         if constexpr (DTYPE == AG_F32) {
             float* p = static_cast<float*>(a.y) + at;

@@ -732,6 +732,19 @@ typedef struct ag_linear_i8_args {
 ag_status_t ag_linear_i8(const ag_linear_i8_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
 ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_linear_plan_t* plan);
 
+/* ag_linear_backward from activations that were kept in 8 bits: where x_scale
+ * (M floats) is not NULL, args->x holds int8 codes (ldx in codes), and where
+ * z_scale is not NULL, args->z does.  The gradients are those of the values
+ * that the codes stand for.  A row's x_scale goes into its dz before dz's
+ * rounding to dtype, but for its power of two, which goes to the codes and
+ * leaves them exact: dw carries one rounding of dz, as without codes, and
+ * needs no rounded copy of x.  A dw in AG_F32 takes dz in two terms of dtype.
+ * Either scale may be NULL. */
+ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+ag_status_t ag_plan_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
+                                       int num_cus, ag_linear_plan_t* plan);
+
 /* ------------------------------------------------------------------------
  * AdamW over many tensors in one launch, with states in 32 or in 8 bits.
  * A handle keeps a device table of the tensors' addresses, made once (as a
