@@ -14,6 +14,7 @@ import ctypes
 import os
 from array import array
 from operator import attrgetter
+from struct import Struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -201,16 +202,16 @@ _SIGNATURES = {
     "ag_plan_linear": [ctypes.POINTER(LinearArgs), _c_int, ctypes.POINTER(LinearPlan)],
     "ag_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _vp, _c_size, _vp],
     "ag_plan_linear_backward": [ctypes.POINTER(LinearBackwardArgs), _c_int, ctypes.POINTER(LinearPlan)],
-    "ag_linear_backward_q8": [ctypes.POINTER(LinearBackwardArgs), _vp, _vp, _vp, _c_size, _vp],
-    "ag_plan_linear_backward_q8": [ctypes.POINTER(LinearBackwardArgs), _vp, _vp, _c_int, ctypes.POINTER(LinearPlan)],
-    "ag_linear_i8": [ctypes.POINTER(LinearI8Args), _vp, _c_size, _vp],
-    "ag_plan_linear_i8": [ctypes.POINTER(LinearI8Args), _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_linear_backward_q8": [_vp, _vp, _vp, _vp, _c_size, _vp],
+    "ag_plan_linear_backward_q8": [_vp, _vp, _vp, _c_int, ctypes.POINTER(LinearPlan)],
+    "ag_linear_i8": [_vp, _vp, _c_size, _vp],
+    "ag_plan_linear_i8": [_vp, _c_int, ctypes.POINTER(LinearPlan)],
     "ag_quantize_rows": [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp],
     "ag_dequantize_rows": [_vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp],
-    "ag_rms_norm": [ctypes.POINTER(RmsNormArgs), _vp],
-    "ag_plan_rms_norm": [ctypes.POINTER(RmsNormArgs), _c_int, ctypes.POINTER(RowsPlan)],
-    "ag_rms_norm_backward": [ctypes.POINTER(RmsNormBackwardArgs), _vp, _c_size, _vp],
-    "ag_plan_rms_norm_backward": [ctypes.POINTER(RmsNormBackwardArgs), _c_int, ctypes.POINTER(RowsPlan)],
+    "ag_rms_norm": [_vp, _vp],
+    "ag_plan_rms_norm": [_vp, _c_int, ctypes.POINTER(RowsPlan)],
+    "ag_rms_norm_backward": [_vp, _vp, _c_size, _vp],
+    "ag_plan_rms_norm_backward": [_vp, _c_int, ctypes.POINTER(RowsPlan)],
     "ag_adamw_create": [ctypes.POINTER(AdamwTensor), _c_i64, _c_int, _c_int, _c_int, _HEAP_PP],
     "ag_adamw_destroy": [_vp],
     "ag_adamw_step": [_vp, ctypes.POINTER(AdamwHyper), _vp],
@@ -536,42 +537,142 @@ def linear_backward(dy, x, w, M, N, K, dtype, act="none", z=None, dx=None, dw=No
     _check(lib().ag_linear_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_backward")
 
 
-def _operand(x, code, name) -> int:
-    """Address of an operand: None, an address, or a tensor of the type on the current device."""
-    if x is None or isinstance(x, int):
-        return x or 0
+_torch_types: Optional[dict] = None     # ag_dtype_t, and "int8", to torch's types: filled with the first tensor
+_current_device = None
+
+
+def _load_types() -> dict:
+    global _torch_types, _current_device
     import torch
-    want = {AG_F16: torch.float16, AG_BF16: torch.bfloat16, AG_F32: torch.float32, "int8": torch.int8}.get(code)
-    if want is not None and x.dtype is not want:
-        raise ValueError(f"{name} is not of {want}")
-    if x.get_device() < 0 or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} does not lie on the current device")
-    return x.data_ptr()
+    _current_device = torch.cuda.current_device
+    _torch_types = {AG_F16: torch.float16, AG_BF16: torch.bfloat16, AG_F32: torch.float32, "int8": torch.int8}
+    return _torch_types
+
+
+def _addresses(*operands) -> list:
+    """Addresses of operands (what, type, name): None, an address, or a tensor of the type on the current device."""
+    at, device = [], -1
+    for x, code, name in operands:
+        if x is None:
+            at.append(0)
+        elif isinstance(x, int):
+            at.append(x)
+        else:
+            types = _torch_types or _load_types()
+            if x.dtype is not types.get(code, x.dtype):       # a code that is none is the library's to refuse
+                raise ValueError(f"{name} is not of {types[code]}")
+            d = x.get_device()
+            if d != device or d < 0:
+                if d < 0 or d != _current_device():
+                    raise ValueError(f"{name} does not lie on the current device")
+                device = d
+            at.append(x.data_ptr())
+    return at
+
+
+# The arguments' structures as bytes: packing them takes a fifth of the time that ctypes takes to fill one field by field,
+# and a call of one token's norm is bound by the host.
+_NORM = Struct("<8Q7qd8i")
+_NORM_BACKWARD = Struct("<7Q6q8i")
+_I8 = Struct("<8Q8q8i")
+_BACKWARD = Struct("<7Q9q8i")
 
 
 def quantize_rows(x, q, scale, M, K, dtype, ldx=0, ldq=0, stream=None) -> None:
     """Each row of x as int8 codes and one fp32 scale (ag_quantize_rows)."""
     d = _dtype(dtype)
-    _check(lib().ag_quantize_rows(_operand(x, d, "x"), ldx, _operand(q, "int8", "q"), ldq, _operand(scale, AG_F32, "scale"), M, K,
-                                  d, _stream(stream)), "ag_quantize_rows")
+    x, q, scale = _addresses((x, d, "x"), (q, "int8", "q"), (scale, AG_F32, "scale"))
+    _check(lib().ag_quantize_rows(x, ldx, q, ldq, scale, M, K, d, _stream(stream)), "ag_quantize_rows")
 
 
 def dequantize_rows(q, scale, y, M, K, dtype, ldq=0, ldy=0, stream=None) -> None:
     """y = q * scale, the values that codes stand for (ag_dequantize_rows)."""
     d = _dtype(dtype)
-    _check(lib().ag_dequantize_rows(_operand(q, "int8", "q"), ldq, _operand(scale, AG_F32, "scale"), _operand(y, d, "y"), ldy, M,
-                                    K, d, _stream(stream)), "ag_dequantize_rows")
+    q, scale, y = _addresses((q, "int8", "q"), (scale, AG_F32, "scale"), (y, d, "y"))
+    _check(lib().ag_dequantize_rows(q, ldq, scale, y, ldy, M, K, d, _stream(stream)), "ag_dequantize_rows")
+
+
+def _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq) -> bytes:
+    """ag_rms_norm_args_t."""
+    d = _dtype(dtype)
+    at = _addresses((x, d, "x"), (residual, d, "residual"), (weight, d, "weight"), (h, d, "h"), (y, d, "y"), (q, "int8", "q"),
+                    (scale, AG_F32, "scale"), (rstd, AG_F32, "rstd"))
+    return _NORM.pack(*at, ldx, ldr, ldh, ldy, ldq, M, K, eps, d, 0, 0, 0, 0, 0, 0, 0)
+
+
+def plan_rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0,
+                  ldr=0, ldh=0, ldy=0, ldq=0, num_cus=0) -> RowsPlan:
+    p = RowsPlan()
+    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
+    _check(lib().ag_plan_rms_norm(a, num_cus, ctypes.byref(p)), "ag_plan_rms_norm")
+    return p
+
+
+def rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0, ldr=0,
+             ldh=0, ldy=0, ldq=0, stream=None) -> None:
+    """The norm of h = x + residual, into y and, or, the codes q with their scales (ag_rms_norm)."""
+    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
+    _check(lib().ag_rms_norm(a, _stream(stream)), "ag_rms_norm")
+
+
+def _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate) -> bytes:
+    """ag_rms_norm_backward_args_t."""
+    d = _dtype(dtype)
+    g = d if dw_dtype is None else _dtype(dw_dtype)
+    at = _addresses((dy, d, "dy"), (h, d, "h"), (dh, d, "dh"), (weight, d, "weight"), (rstd, AG_F32, "rstd"), (dx, d, "dx"),
+                    (dw, g, "dw"))
+    return _NORM_BACKWARD.pack(*at, lddy, ldh, lddh, lddx, M, K, d, g, int(accumulate), 0, 0, 0, 0, 0)
+
+
+def plan_rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
+                           dw_dtype=None, accumulate=False, num_cus=0) -> RowsPlan:
+    p = RowsPlan()
+    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
+    _check(lib().ag_plan_rms_norm_backward(a, num_cus, ctypes.byref(p)), "ag_plan_rms_norm_backward")
+    return p
+
+
+def rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
+                      dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
+    """The norm's gradients dx (with dh, what reaches h otherwise) and dw, those that are given (ag_rms_norm_backward)."""
+    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_rms_norm_backward(a, ws, nbytes, _stream(stream)), "ag_rms_norm_backward")
+
+
+def _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz) -> bytes:
+    """ag_linear_i8_args_t."""
+    d = _dtype(dtype)
+    at = _addresses((x, "int8", "x"), (w, "int8", "w"), (x_scale, AG_F32, "x_scale"), (w_scale, AG_F32, "w_scale"), (bias, d, "bias"),
+                    (residual, d, "residual"), (y, d, "y"), (z, d, "z"))
+    return _I8.pack(*at, ldx, ldw, ldr, ldy, ldz, M, N, K, d, _act(act), 0, 0, 0, 0, 0, 0)
+
+
+def plan_linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0,
+                   ldy=0, ldz=0, num_cus=0) -> LinearPlan:
+    p = LinearPlan()
+    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    _check(lib().ag_plan_linear_i8(a, num_cus, ctypes.byref(p)), "ag_plan_linear_i8")
+    return p
+
+
+def linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0, ldy=0,
+              ldz=0, workspace=None, stream=None) -> None:
+    """y = act(x_scale w_scale (x w^T) + bias) + residual of int8 codes x and w (ag_linear_i8)."""
+    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ag_linear_i8(a, ws, nbytes, _stream(stream)), "ag_linear_i8")
 
 
 def _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw, dw_dtype,
                       accumulate):
+    """ag_linear_backward_args_t and the addresses of the scales."""
     d = _dtype(dtype)
     g = d if dw_dtype is None else _dtype(dw_dtype)
-    a = LinearBackwardArgs(_operand(dy, d, "dy"), _operand(z, d if z_scale is None else "int8", "z"),
-                           _operand(x, d if x_scale is None else "int8", "x"), _operand(w, d, "w"), _operand(dx, d, "dx"),
-                           _operand(dw, g, "dw"), _operand(db, g, "db"), lddy, ldz, ldx, ldw, lddx, lddw, M, N, K, d, _act(act), g,
-                           int(accumulate))
-    return a, _operand(x_scale, AG_F32, "x_scale"), _operand(z_scale, AG_F32, "z_scale")
+    *at, xs, zs = _addresses((dy, d, "dy"), (z, d if z_scale is None else "int8", "z"), (x, d if x_scale is None else "int8", "x"),
+                             (w, d, "w"), (dx, d, "dx"), (dw, g, "dw"), (db, g, "db"), (x_scale, AG_F32, "x_scale"),
+                             (z_scale, AG_F32, "z_scale"))
+    return _BACKWARD.pack(*at, lddy, ldz, ldx, ldw, lddx, lddw, M, N, K, d, _act(act), g, int(accumulate), 0, 0, 0, 0), xs, zs
 
 
 def plan_linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", z=None, z_scale=None, dx=None, dw=None, db=None,
@@ -579,7 +680,7 @@ def plan_linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", 
     p = LinearPlan()
     a, xs, zs = _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw,
                                   dw_dtype, accumulate)
-    _check(lib().ag_plan_linear_backward_q8(ctypes.byref(a), xs, zs, num_cus, ctypes.byref(p)), "ag_plan_linear_backward_q8")
+    _check(lib().ag_plan_linear_backward_q8(a, xs, zs, num_cus, ctypes.byref(p)), "ag_plan_linear_backward_q8")
     return p
 
 
@@ -590,77 +691,7 @@ def linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", z=Non
     a, xs, zs = _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw,
                                   dw_dtype, accumulate)
     ws, nbytes = _workspace(workspace)
-    _check(lib().ag_linear_backward_q8(ctypes.byref(a), xs, zs, ws, nbytes, _stream(stream)), "ag_linear_backward_q8")
-
-
-def _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq) -> RmsNormArgs:
-    d = _dtype(dtype)
-    return RmsNormArgs(_operand(x, d, "x"), _operand(residual, d, "residual"), _operand(weight, d, "weight"), _operand(h, d, "h"),
-                       _operand(y, d, "y"), _operand(q, "int8", "q"), _operand(scale, AG_F32, "scale"),
-                       _operand(rstd, AG_F32, "rstd"), ldx, ldr, ldh, ldy, ldq, M, K, eps, d)
-
-
-def plan_rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0,
-                  ldr=0, ldh=0, ldy=0, ldq=0, num_cus=0) -> RowsPlan:
-    p = RowsPlan()
-    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
-    _check(lib().ag_plan_rms_norm(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_rms_norm")
-    return p
-
-
-def rms_norm(x, M, K, dtype, weight=None, residual=None, h=None, y=None, q=None, scale=None, rstd=None, eps=1e-6, ldx=0, ldr=0,
-             ldh=0, ldy=0, ldq=0, stream=None) -> None:
-    """The norm of h = x + residual, into y and, or, the codes q with their scales (ag_rms_norm)."""
-    a = _norm_args(x, M, K, dtype, weight, residual, h, y, q, scale, rstd, eps, ldx, ldr, ldh, ldy, ldq)
-    _check(lib().ag_rms_norm(ctypes.byref(a), _stream(stream)), "ag_rms_norm")
-
-
-def _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype,
-                        accumulate) -> RmsNormBackwardArgs:
-    d = _dtype(dtype)
-    g = d if dw_dtype is None else _dtype(dw_dtype)
-    return RmsNormBackwardArgs(_operand(dy, d, "dy"), _operand(h, d, "h"), _operand(dh, d, "dh"), _operand(weight, d, "weight"),
-                               _operand(rstd, AG_F32, "rstd"), _operand(dx, d, "dx"), _operand(dw, g, "dw"), lddy, ldh, lddh,
-                               lddx, M, K, d, g, int(accumulate))
-
-
-def plan_rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
-                           dw_dtype=None, accumulate=False, num_cus=0) -> RowsPlan:
-    p = RowsPlan()
-    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
-    _check(lib().ag_plan_rms_norm_backward(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_rms_norm_backward")
-    return p
-
-
-def rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, dw=None, lddy=0, ldh=0, lddh=0, lddx=0,
-                      dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
-    """The norm's gradients dx (with dh, what reaches h otherwise) and dw, those that are given (ag_rms_norm_backward)."""
-    a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
-    ws, nbytes = _workspace(workspace)
-    _check(lib().ag_rms_norm_backward(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_rms_norm_backward")
-
-
-def _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz) -> LinearI8Args:
-    d = _dtype(dtype)
-    return LinearI8Args(_operand(x, "int8", "x"), _operand(w, "int8", "w"), _operand(x_scale, AG_F32, "x_scale"),
-                        _operand(w_scale, AG_F32, "w_scale"), _operand(bias, d, "bias"), _operand(residual, d, "residual"),
-                        _operand(y, d, "y"), _operand(z, d, "z"), ldx, ldw, ldr, ldy, ldz, M, N, K, d, _act(act))
-
-
-def plan_linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0,
-                   ldy=0, ldz=0, num_cus=0) -> LinearPlan:
-    p = LinearPlan()
-    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
-    _check(lib().ag_plan_linear_i8(ctypes.byref(a), num_cus, ctypes.byref(p)), "ag_plan_linear_i8")
-    return p
-
-
-def linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, residual=None, z=None, ldx=0, ldw=0, ldr=0, ldy=0,
-              ldz=0, workspace=None, stream=None) -> None:
-    """y = act(x_scale w_scale (x w^T) + bias) + residual of int8 codes x and w (ag_linear_i8)."""
-    a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
-    ws, nbytes = _workspace(workspace)
-    _check(lib().ag_linear_i8(ctypes.byref(a), ws, nbytes, _stream(stream)), "ag_linear_i8")
+    _check(lib().ag_linear_backward_q8(a, xs, zs, ws, nbytes, _stream(stream)), "ag_linear_backward_q8")
 
 
 def _reachable(tensors) -> bool:

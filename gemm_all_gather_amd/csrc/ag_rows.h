@@ -30,7 +30,11 @@ struct RowsShape {
     int threads, vectors;
     int per_group;          // rows of a workgroup at a time
 };
-RowsShape rows_shape(int64_t K);
+RowsShape rows_shape(int64_t K, bool norm);
+RowsShape norm_backward_shape(int64_t K);       // vectors 0: in two passes, launch_norm_backward_long
+
+// A grid's workgroups: with up to 1024 threads each, a launch's threads stay below 2^32.
+constexpr int64_t kMaxRowsPrograms = (int64_t{1} << 22) - 1;
 
 // norm with dtype AG_F16 or AG_BF16; without it AG_F32 too.
 hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hipStream_t stream);
@@ -54,12 +58,27 @@ struct NormBackwardArgs {
     const uint16_t* weight;     // or null
     const float* rstd;
     uint16_t* dx;               // or null; may be dh
-    float* sums;                // one row of K floats for each workgroup, or null
+    float* sums;                // one row of floats for each workgroup, or null
+    float* means;               // M floats, of the two passes over longer rows
+    int64_t ldsums;             // a multiple of 32
     int64_t lddy, ldh, lddh, lddx;
     int64_t M;
     int32_t K;
     int32_t reserved;
 };
+// dw (+)= the sum of `parts` rows of sums.
+struct NormDwArgs {
+    const float* sums;
+    void* dw;
+    int64_t ldsums;
+    int32_t parts;
+    int32_t K;
+    int32_t dtype;              // ag_dtype_t of dw
+    int32_t accumulate;
+};
+hipError_t launch_norm_dw(const NormDwArgs& a, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int bf16, int programs, hipStream_t stream);
+// Longer rows: `batches` of `rows` rows each, and as many rows of sums.
+hipError_t launch_norm_backward_long(const NormBackwardArgs& a, int bf16, int batches, int rows, hipStream_t stream);
 
 }  // namespace ag

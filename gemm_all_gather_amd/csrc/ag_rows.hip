@@ -1,6 +1,8 @@
 // Kernels that take whole rows: a row in 8 bits with its scale, the root-mean-square norm around it, and the norm's
 // gradients.  All are bound by memory, one pass over their operands.
 
+#include <algorithm>
+
 #include "ag_rows.h"
 #include "ag_scale.h"
 #include "ag_vec.h"
@@ -12,27 +14,99 @@ namespace {
 
 // ---------------------------------------------------------------- rows and codes
 
-// n <= 8 elements from p on, the others 0.
-template <int DTYPE>
-__device__ __forceinline__ void load_row(float (&v)[8], const void* p, int64_t at, int n)
+template <int DTYPE> __device__ __forceinline__ const void* row_of(const void* p, int64_t row, int64_t ld)
 {
-    if constexpr (DTYPE == AG_F32) {
-        const float* f = static_cast<const float*>(p) + at;
+    return static_cast<const char*>(p) + row * ld * (DTYPE == AG_F32 ? 4 : 2);
+}
+
+// Eight elements as they lie in memory: loaded early, and taken apart where they are used (a conversion next to its load
+// waits for it, one vector after the other).
+template <int DTYPE> struct Raw {
+    u32x4 v;            // pairs in words: as eight elements the compiler would keep eight registers
+    // The elements of a row of K from col on (TAIL false: K is a multiple of 8), those past its end 0.  A row's last, shorter vector is loaded as its last eight
+    // elements, moved down: one load instead of up to seven.
+    template <bool TAIL> __device__ __forceinline__ void load(const void* row, int col, int K)
+    {
+        const uint16_t* s = static_cast<const uint16_t*>(row);
+        const int n = K - col;
+        v = u32x4{0u, 0u, 0u, 0u};
         if (n >= 8) {
-            const f32x4u lo = *reinterpret_cast<const f32x4u*>(f), hi = *reinterpret_cast<const f32x4u*>(f + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = lo[e];
-                v[4 + e] = hi[e];
+            v = reinterpret_cast<const Any16*>(s + col)->v;
+        } else if (TAIL && n > 0) {
+            uint64_t lo = 0, hi = 0;
+            if (K >= 8) {
+                const u32x4 t = reinterpret_cast<const Any16*>(s + (K - 8))->v;
+                lo = static_cast<uint64_t>(t.y) << 32 | t.x;
+                hi = static_cast<uint64_t>(t.w) << 32 | t.z;
+                const int bits = 16 * (8 - n);      // 16 to 112
+                const bool far = bits >= 64;
+                lo = far ? hi >> (bits - 64) : lo >> bits | hi << (64 - bits);
+                hi = far ? 0 : hi >> bits;
+            } else {
+#pragma unroll 1
+                for (int e = n - 1; e >= 0; --e) {
+                    hi = hi << 16 | lo >> 48;
+                    lo = lo << 16 | s[col + e];
+                }
             }
+            v = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[8])       // rounded
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = static_cast<uint32_t>(from_f32<DTYPE == AG_BF16>(f[2 * e + 1])) << 16 | from_f32<DTYPE == AG_BF16>(f[2 * e]);
+    }
+    __device__ __forceinline__ void store(void* p, int64_t at, int n) const
+    {
+        uint16_t* s = static_cast<uint16_t*>(p) + at;
+        if (n >= 8) {
+            reinterpret_cast<Any16*>(s)->v = v;
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < n ? f[e] : 0.f;
+            for (int e = 0; e < 8; ++e)
+                if (e < n) s[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
         }
-    } else {
-        load_f32<DTYPE == AG_BF16>(v, static_cast<const uint16_t*>(p) + at, n);
     }
-}
+    __device__ __forceinline__ void ones()
+    {
+        const uint32_t one = DTYPE == AG_BF16 ? 0x3f80u : 0x3c00u;
+        v = u32x4{one << 16 | one, one << 16 | one, one << 16 | one, one << 16 | one};
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        u32x4 w = v;
+        asm volatile("" : "+v"(w));     // taken apart here: not at the load, nor once before a loop
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = to_f32<DTYPE == AG_BF16>(static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1))));
+    }
+};
+template <> struct Raw<AG_F32> {
+    f32x4u lo, hi;
+    template <bool TAIL> __device__ __forceinline__ void load(const void* row, int col, int K)
+    {
+        const float* s = static_cast<const float*>(row) + col;
+        const int n = K - col;
+        lo = hi = f32x4u{0.f, 0.f, 0.f, 0.f};
+        if (n >= 8) {
+            lo = *reinterpret_cast<const f32x4u*>(s);
+            hi = *reinterpret_cast<const f32x4u*>(s + 4);
+        } else if (TAIL && n > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) (e < 4 ? lo : hi)[e & 3] = s[e];
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[e] = lo[e];
+            f[4 + e] = hi[e];
+        }
+    }
+};
 
 // A number of codes' steps to the nearest whole number, ties to even, as in exact arithmetic: v and top are exact, t = v
 // (127 / top) in fp32 is off by less than 127 (2^-23 + 2^-47) = 1.6e-5, so only a t within 1e-4 of a half is decided
@@ -68,20 +142,66 @@ __device__ __forceinline__ void store_codes(int8_t* p, const float (&v)[8], uint
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }   // NaN above infinity
 
-// A row's sum of squares and largest magnitude, over G threads; every thread gets both.  One barrier where several waves
-// share a row: the LDS is used in turn (`turn`), so that a wave that is a row ahead does not write what others still read.
-template <int G>
+// x combined with all lanes' of each group of G <= 64, in every lane: rotations within rows of 16 lanes, then swaps of rows and
+// of halves, none of which goes through LDS.
+template <int D> __device__ __forceinline__ uint32_t rotated(uint32_t x)      // within 16 lanes, by D
+{
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x120 + D, 0xf, 0xf, true));
+}
+template <int D, class T> __device__ __forceinline__ T rotated_as(T x)
+{
+    if constexpr (sizeof(T) == 8) {
+        u32x2 w = __builtin_bit_cast(u32x2, x);
+        w.x = rotated<D>(w.x);
+        w.y = rotated<D>(w.y);
+        return __builtin_bit_cast(T, w);
+    } else {
+        return __builtin_bit_cast(T, rotated<D>(__builtin_bit_cast(uint32_t, x)));
+    }
+}
+// Both rows of a pair (SIZE 16), both halves (32): each lane gets its own side's and the other side's, in the lanes' order.
+template <int SIZE> __device__ __forceinline__ u32x2 swapped(uint32_t x)
+{
+    if constexpr (SIZE == 16) return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, x, false, false));
+    else return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(x, x, false, false));
+}
+template <int SIZE, class T, class F> __device__ __forceinline__ T across(T x, F f)
+{
+    if constexpr (sizeof(T) == 8) {
+        const u32x2 w = __builtin_bit_cast(u32x2, x), lo = swapped<SIZE>(w.x), hi = swapped<SIZE>(w.y);
+        return f(__builtin_bit_cast(T, u32x2{lo.x, hi.x}), __builtin_bit_cast(T, u32x2{lo.y, hi.y}));
+    } else {
+        const u32x2 w = swapped<SIZE>(__builtin_bit_cast(uint32_t, x));
+        const uint32_t one = w.x, other = w.y;      // a bit cast of a vector's element takes its first one
+        return f(__builtin_bit_cast(T, one), __builtin_bit_cast(T, other));
+    }
+}
+template <int G, class T, class F> __device__ __forceinline__ T combine(T x, F f)
+{
+    static_assert(G == 16 || G == 64, "whole rows or whole waves");
+    x = f(x, rotated_as<8>(x));
+    x = f(x, rotated_as<4>(x));
+    x = f(x, rotated_as<2>(x));
+    x = f(x, rotated_as<1>(x));
+    if constexpr (G == 64) {
+        x = across<16>(x, f);
+        x = across<32>(x, f);
+    }
+    return x;
+}
+
+// A row's sum of squares (of a norm) and largest magnitude, over G threads; every thread gets both.  One barrier where several
+// waves share a row: the LDS is used in turn (`turn`), so that a wave that is a row ahead does not write what others still read.
+template <bool NORM, int G>
 __device__ __forceinline__ void reduce_row(double& sum, uint32_t& top, double (*lds_sum)[16], uint32_t (*lds_top)[16], int turn)
 {
-#pragma unroll
-    for (int d = 1; d < (G < 64 ? G : 64); d *= 2) {
-        sum += __shfl_xor(sum, d);
-        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    }
+    constexpr int LANES = G < 64 ? G : 64;
+    if constexpr (NORM) sum = combine<LANES>(sum, [](double x, double y) { return x + y; });
+    top = combine<LANES>(top, [](uint32_t x, uint32_t y) { return max(x, y); });
     if constexpr (G > 64) {
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
-            lds_sum[turn][wave] = sum;
+            if constexpr (NORM) lds_sum[turn][wave] = sum;
             lds_top[turn][wave] = top;
         }
         __syncthreads();
@@ -89,7 +209,7 @@ __device__ __forceinline__ void reduce_row(double& sum, uint32_t& top, double (*
         top = 0;
 #pragma unroll
         for (int w = 0; w < G / 64; ++w) {
-            sum += lds_sum[turn][w];
+            if constexpr (NORM) sum += lds_sum[turn][w];
             top = max(top, lds_top[turn][w]);
         }
     }
@@ -109,18 +229,16 @@ __device__ __forceinline__ float scale_of(uint32_t top_bits, float rstd)
     return static_cast<float>(static_cast<double>(__uint_as_float(top_bits)) * rstd * (1.0 / 127.0));
 }
 
-// h: the sum rounded to its type, in fp32; what the norm is of.
+// x becomes h: the sum rounded to its type; what the norm is of.
 template <int DTYPE>
-__device__ __forceinline__ void add_residual(float (&v)[8], const RowsArgs& a, int64_t row, int col, int n)
+__device__ __forceinline__ void add_residual(Raw<DTYPE>& x, const Raw<DTYPE>& residual)
 {
-    if constexpr (DTYPE != AG_F32) {
-        if (a.residual) {
-            float r[8];
-            load_row<DTYPE>(r, a.residual, row * a.ldr + col, n);
+    float f[8], r[8];
+    x.get(f);
+    residual.get(r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = to_f32<DTYPE == AG_BF16>(from_f32<DTYPE == AG_BF16>(v[e] + r[e]));
-        }
-    }
+    for (int e = 0; e < 8; ++e) f[e] += r[e];
+    x.set(f);
 }
 
 template <int DTYPE>
@@ -129,68 +247,77 @@ __device__ __forceinline__ void store_row(void* p, int64_t at, const float (&v)[
     if constexpr (DTYPE != AG_F32) store_16<DTYPE == AG_BF16>(static_cast<uint16_t*>(p) + at, v, n);
 }
 
+constexpr int group_threads(int G) { return G < 256 ? 256 : G; }
+
 // Rows of up to 8 G V elements, G threads to a row, the row in registers between its two uses.
-template <int DTYPE, bool NORM, int G, int V>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void ag_rows_kernel(RowsArgs a)
+template <int DTYPE, bool NORM, int G, int V, bool TAIL>
+__global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
 {
-    constexpr int ROWS = G < 256 ? 256 / G : 1;
+    constexpr int ROWS = group_threads(G) / G;
     __shared__ double lds_sum[2][16];
     __shared__ uint32_t lds_top[2][16];
     const int lane = threadIdx.x % G;
-    float weight[V][8];
-    if constexpr (NORM) {
+    const bool weighted = NORM && a.weight != nullptr, add = NORM && a.residual != nullptr;
+    int turn = 0;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.M; first += static_cast<int64_t>(gridDim.x) * ROWS) {
+        const int64_t mine = first + (ROWS > 1 ? threadIdx.x / G : 0), row = min(mine, a.M - 1);
+        const bool live = mine < a.M;
+        const void *xs = row_of<DTYPE>(a.x, row, a.ldx), *rs = row_of<DTYPE>(a.residual, row, a.ldr);
+        Raw<DTYPE> x[V], r[V], weight[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) weight[j][e] = 1.f;
-            if (a.weight) load_row<DTYPE>(weight[j], a.weight, col, a.K - col);
+            x[j].template load<TAIL>(xs, col, a.K);
+            if (add) r[j].template load<TAIL>(rs, col, a.K);
         }
-    }
-    int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.M; first += static_cast<int64_t>(gridDim.x) * ROWS) {
-        const int64_t mine = first + threadIdx.x / G, row = min(mine, a.M - 1);
-        const bool live = mine < a.M;
-        float v[V][8];
+        if (weighted) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) weight[j].template load<TAIL>(a.weight, (lane + j * G) * 8, a.K);
+        }
         double sum = 0;
         uint32_t top = 0;
+        float kept[NORM ? V : 1][8];        // h times the weight; codes of plain rows are taken from x again
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int col = (lane + j * G) * 8, n = a.K - col;
-            load_row<DTYPE>(v[j], a.x, row * a.ldx + col, n);
-            add_residual<DTYPE>(v[j], a, row, col, n);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int col = (lane + j * G) * 8, n = a.K - col;
+            const int col = (lane + j * G) * 8;
+            float (&v)[8] = kept[NORM ? j : 0];
             if constexpr (NORM) {
-                if (a.h && live) store_row<DTYPE>(a.h, row * a.ldh + col, v[j], n);
+                if (add) add_residual<DTYPE>(x[j], r[j]);
+                if (a.h && live) x[j].store(a.h, row * a.ldh + col, a.K - col);
+            }
+            x[j].get(v);
+            if constexpr (NORM) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sum = fma(static_cast<double>(v[j][e]), static_cast<double>(v[j][e]), sum);
-                    v[j][e] *= weight[j][e];
+                for (int e = 0; e < 8; ++e) sum = fma(static_cast<double>(v[e]), static_cast<double>(v[e]), sum);
+                if (weighted) {
+                    float w[8];
+                    weight[j].get(w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= w[e];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[j][e]));
+            for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
         }
-        reduce_row<G>(sum, top, lds_sum, lds_top, turn);
+        reduce_row<NORM, G>(sum, top, lds_sum, lds_top, turn);
         turn ^= 1;
         float rstd = 1.f;
         if constexpr (NORM) rstd = root(sum, a.K, a.eps);
-        if (live && lane == 0) {
+        if (!live) continue;
+        if (lane == 0) {
             if (a.scale) a.scale[row] = scale_of(top, rstd);
             if (a.rstd) a.rstd[row] = rstd;
         }
-        if (!live) continue;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8, n = a.K - col;
-            if (a.q) store_codes(a.q + row * a.ldq + col, v[j], top, n);
-            if (a.y) {
+            float (&v)[8] = kept[NORM ? j : 0];
+            if constexpr (!NORM) x[j].get(v);
+            if (a.q) store_codes(a.q + row * a.ldq + col, v, top, n);
+            if (NORM && a.y) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] *= rstd;
-                store_row<DTYPE>(a.y, row * a.ldy + col, v[j], n);
+                for (int e = 0; e < 8; ++e) v[e] *= rstd;
+                store_row<DTYPE>(a.y, row * a.ldy + col, v, n);
             }
         }
     }
@@ -203,32 +330,57 @@ __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
 {
     __shared__ double lds_sum[2][16];
     __shared__ uint32_t lds_top[2][16];
+    const bool weighted = NORM && a.weight != nullptr, add = NORM && a.residual != nullptr;
+    constexpr bool TAIL = true;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-        auto weighted = [&](float (&v)[8], int col, int n) {
-            if (!NORM || !a.weight) return;
-            float w[8];
-            load_row<DTYPE>(w, a.weight, col, n);
+        // Two vectors of h times the weight, or of the row itself; `stored`: h from where it was stored (x or the residual may
+        // be overwritten by then: a thread reads what it wrote itself).  Past the row's end they are 0.
+        auto load = [&](Raw<DTYPE> (&x)[2], Raw<DTYPE> (&w)[2], int col, bool stored) {
+            const bool from_h = NORM && stored && a.h;
+            Raw<DTYPE> r[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= w[e];
+            for (int j = 0; j < 2; ++j) {
+                const int at = col + j * kLongThreads * 8;
+                x[j].template load<TAIL>(from_h ? row_of<DTYPE>(a.h, row, a.ldh) : row_of<DTYPE>(a.x, row, a.ldx), at, a.K);
+                if (add && !from_h) r[j].template load<TAIL>(row_of<DTYPE>(a.residual, row, a.ldr), at, a.K);
+                if (weighted) w[j].template load<TAIL>(a.weight, at, a.K);
+            }
+            if constexpr (NORM) {
+                if (add && !from_h) {
+                    add_residual<DTYPE>(x[0], r[0]);
+                    add_residual<DTYPE>(x[1], r[1]);
+                }
+            }
+        };
+        auto weigh = [&](float (&v)[8], const Raw<DTYPE>& w) {
+            if (!weighted) return;
+            float f[8];
+            w.get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= f[e];
         };
         double sum = 0;
         uint32_t top = 0;
-        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 8) {
-            float v[8];
-            const int n = a.K - col;
-            load_row<DTYPE>(v, a.x, row * a.ldx + col, n);
-            add_residual<DTYPE>(v, a, row, col, n);
-            if constexpr (NORM) {
-                if (a.h) store_row<DTYPE>(a.h, row * a.ldh + col, v, n);
+        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 16) {
+            Raw<DTYPE> x[2], w[2];
+            load(x, w, col, false);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fma(static_cast<double>(v[e]), static_cast<double>(v[e]), sum);
+            for (int j = 0; j < 2; ++j) {
+                const int at = col + j * kLongThreads * 8;
+                float v[8];
+                x[j].get(v);
+                if constexpr (NORM) {
+                    if (a.h) x[j].store(a.h, row * a.ldh + at, a.K - at);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum = fma(static_cast<double>(v[e]), static_cast<double>(v[e]), sum);
+                }
+                weigh(v, w[j]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
             }
-            weighted(v, col, n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
         }
-        reduce_row<kLongThreads>(sum, top, lds_sum, lds_top, turn);
+        reduce_row<NORM, kLongThreads>(sum, top, lds_sum, lds_top, turn);
         turn ^= 1;
         float rstd = 1.f;
         if constexpr (NORM) rstd = root(sum, a.K, a.eps);
@@ -237,61 +389,87 @@ __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
             if (a.rstd) a.rstd[row] = rstd;
         }
         if (!a.q && !a.y) continue;
-        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 8) {
-            float v[8];
-            const int n = a.K - col;
-            if (NORM && a.h) {      // x or the residual may be overwritten by now; a thread reads what it wrote itself
-                load_row<DTYPE>(v, a.h, row * a.ldh + col, n);
-            } else {
-                load_row<DTYPE>(v, a.x, row * a.ldx + col, n);
-                add_residual<DTYPE>(v, a, row, col, n);
-            }
-            weighted(v, col, n);
-            if (a.q) store_codes(a.q + row * a.ldq + col, v, top, n);
-            if (a.y) {
+        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 16) {
+            Raw<DTYPE> x[2], w[2];
+            load(x, w, col, true);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= rstd;
-                store_row<DTYPE>(a.y, row * a.ldy + col, v, n);
+            for (int j = 0; j < 2; ++j) {
+                const int at = col + j * kLongThreads * 8, n = a.K - at;
+                float v[8];
+                x[j].get(v);
+                weigh(v, w[j]);
+                if (a.q) store_codes(a.q + row * a.ldq + at, v, top, n);
+                if (NORM && a.y) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= rstd;
+                    store_row<DTYPE>(a.y, row * a.ldy + at, v, n);
+                }
             }
         }
     }
 }
 
-// The values of codes, 16 to a thread.
+// The values of codes: 8 to a lane, so that a wave's stores are whole lines; a thread takes kDequantizeVectors of them.
+constexpr int kDequantizeVectors = 4;
 template <int DTYPE>
 __global__ __launch_bounds__(256) void ag_dequantize_kernel(DequantizeArgs a)
 {
-    const int64_t per_row = (a.K + 15) / 16, id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t row = id / per_row;
-    const int col = static_cast<int>(id - row * per_row) * 16;
-    if (row >= a.M) return;
-    float s = a.scale[row];
-    if (a.by_power) {
-        float rest;
-        split_scale<DTYPE == AG_BF16>(s, &s, &rest);
-    }
-    const int8_t* q = a.q + row * a.ldq + col;
+    const uint32_t per_row = (static_cast<uint32_t>(a.K) + 7u) / 8u;
+    const uint64_t vectors = static_cast<uint64_t>(a.M) * per_row;
+    constexpr uint64_t PER = 256 * kDequantizeVectors;
+    for (uint64_t from = blockIdx.x * PER; from < vectors; from += gridDim.x * PER) {
+        u32x2 q[kDequantizeVectors];
+        float s[kDequantizeVectors];
+        int64_t row[kDequantizeVectors];
+        int col[kDequantizeVectors];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int n = a.K - col - 8 * half;
-        if (n <= 0) break;
-        float v[8];
-        load_codes(v, q + 8 * half, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= s;
-        const int64_t at = row * a.ldy + col + 8 * half;
-        if constexpr (DTYPE == AG_F32) {
-            float* p = static_cast<float*>(a.y) + at;
-            if (n >= 8) {
-                *reinterpret_cast<f32x4u*>(p) = f32x4u{v[0], v[1], v[2], v[3]};
-                *reinterpret_cast<f32x4u*>(p + 4) = f32x4u{v[4], v[5], v[6], v[7]};
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < n) p[e] = v[e];
+        for (int j = 0; j < kDequantizeVectors; ++j) {
+            const uint64_t id = min(from + j * 256 + threadIdx.x, vectors - 1);     // past the end: the last one again
+            if (vectors >> 32) {
+                row[j] = static_cast<int64_t>(id / per_row);
+                col[j] = static_cast<int>(id - row[j] * per_row) * 8;
+            } else {        // a division of 64 bits takes as long as the rest
+                const uint32_t r = static_cast<uint32_t>(id) / per_row;
+                row[j] = r;
+                col[j] = static_cast<int>(static_cast<uint32_t>(id) - r * per_row) * 8;
             }
-        } else {
-            store_row<DTYPE>(a.y, at, v, n);
+            const int8_t* at = a.q + row[j] * a.ldq + col[j];
+            const int n = a.K - col[j];
+            s[j] = a.scale[row[j]];
+            if (n >= 8) {
+                q[j] = reinterpret_cast<const Any8*>(at)->v;
+            } else {
+                uint64_t w = 0;
+                for (int e = n - 1; e >= 0; --e) w = w << 8 | static_cast<uint8_t>(at[e]);
+                q[j] = u32x2{static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32)};
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kDequantizeVectors; ++j) {
+            if (from + j * 256 + threadIdx.x >= vectors) break;
+            const int n = a.K - col[j];
+            float scale = s[j], v[8];
+            if (a.by_power) {
+                float rest;
+                split_scale<DTYPE == AG_BF16>(s[j], &scale, &rest);
+            }
+            code_values(v, q[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= scale;
+            const int64_t at = row[j] * a.ldy + col[j];
+            if constexpr (DTYPE == AG_F32) {
+                float* p = static_cast<float*>(a.y) + at;
+                if (n >= 8) {
+                    *reinterpret_cast<f32x4u*>(p) = f32x4u{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4u*>(p + 4) = f32x4u{v[4], v[5], v[6], v[7]};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < n) p[e] = v[e];
+                }
+            } else {
+                store_row<DTYPE>(a.y, at, v, n);
+            }
         }
     }
 }
@@ -302,8 +480,7 @@ __global__ __launch_bounds__(256) void ag_dequantize_kernel(DequantizeArgs a)
 template <int G>
 __device__ __forceinline__ float sum_row(float s, float (*lds)[16], int turn)
 {
-#pragma unroll
-    for (int d = 1; d < (G < 64 ? G : 64); d *= 2) s += __shfl_xor(s, d);
+    s = combine<(G < 64 ? G : 64)>(s, [](float x, float y) { return x + y; });
     if constexpr (G > 64) {
         if ((threadIdx.x & 63) == 0) lds[turn][threadIdx.x >> 6] = s;
         __syncthreads();
@@ -315,49 +492,58 @@ __device__ __forceinline__ float sum_row(float s, float (*lds)[16], int turn)
 }
 
 // With n = h rstd and c = mean(g n): dx = rstd (g - n c) + dh, and dy n for dw, which a workgroup sums over its rows in
-// registers (its waves' sums joined through LDS where they take rows of their own).
-template <bool BF16, int G, int V>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void ag_norm_backward_kernel(NormBackwardArgs a)
+// registers (its waves' sums joined through LDS where they take rows of their own).  The row stays as it was loaded and is
+// taken apart twice, so that few registers leave many rows on their way.
+template <bool BF16, int G, int V, bool TAIL>
+__global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(NormBackwardArgs a)
 {
-    constexpr int ROWS = G < 256 ? 256 / G : 1;
+    constexpr int ROWS = group_threads(G) / G;
+    constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16;
     __shared__ float lds[2][16];
     __shared__ float join[ROWS > 1 ? ROWS * G * 8 : 1];
     const int lane = threadIdx.x % G;
-    float weight[V][8], dw[V][8];
+    Raw<DTYPE> weight[V], dy[V], h[V], dh[V];
+    float dw[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int col = (lane + j * G) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            weight[j][e] = 1.f;
-            dw[j][e] = 0.f;
-        }
-        if (a.weight) load_f32<BF16>(weight[j], a.weight + col, a.K - col);
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
+        if (a.weight) weight[j].template load<TAIL>(a.weight, col, a.K);
+        else weight[j].ones();
     }
+    const bool add = a.dh != nullptr && a.dx != nullptr;
     const float per_k = 1.f / max(a.K, 1);
     int turn = 0;
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.M; first += static_cast<int64_t>(gridDim.x) * ROWS) {
-        const int64_t mine = first + threadIdx.x / G, row = min(mine, a.M - 1);
+        const int64_t mine = first + (ROWS > 1 ? threadIdx.x / G : 0), row = min(mine, a.M - 1);
         const bool live = mine < a.M;
+        const void *ds = row_of<DTYPE>(a.dy, row, a.lddy), *hs = row_of<DTYPE>(a.h, row, a.ldh), *es = row_of<DTYPE>(a.dh, row, a.lddh);
         const float rstd = a.rstd[row];
-        float dy[V][8], n[V][8], dh[V][8];
-        float s = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
-            load_f32<BF16>(dy[j], a.dy + row * a.lddy + col, a.K - col);
-            load_f32<BF16>(n[j], a.h + row * a.ldh + col, a.K - col);
-            if (a.dh && a.dx) load_f32<BF16>(dh[j], a.dh + row * a.lddh + col, a.K - col);
+            dy[j].template load<TAIL>(ds, col, a.K);
+            h[j].template load<TAIL>(hs, col, a.K);
         }
+        if (add) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+            for (int j = 0; j < V; ++j) dh[j].template load<TAIL>(es, (lane + j * G) * 8, a.K);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float g[8], n[8], w[8];
+            dy[j].get(g);
+            h[j].get(n);
+            weight[j].get(w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                n[j][e] *= rstd;
-                if (live) dw[j][e] += dy[j][e] * n[j][e];
-                dy[j][e] *= weight[j][e];
-                s += dy[j][e] * n[j][e];
+                const float t = g[e] * (n[e] * rstd);
+                dw[j][e] += live ? t : 0.f;
+                s += t * w[e];
             }
+        }
         if (!a.dx) continue;
         const float c = sum_row<G>(s, lds, turn) * per_k;
         turn ^= 1;
@@ -365,14 +551,18 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void ag_norm_backward_kernel(Nor
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
-            float v[8];
+            float g[8], n[8], w[8], d[8] = {};
+            dy[j].get(g);
+            h[j].get(n);
+            weight[j].get(w);
+            if (add) dh[j].get(d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = rstd * (dy[j][e] - n[j][e] * c) + (a.dh ? dh[j][e] : 0.f);
-            store_16<BF16>(a.dx + row * a.lddx + col, v, a.K - col);
+            for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] * w[e] - n[e] * rstd * c) + d[e];
+            store_16<BF16>(a.dx + row * a.lddx + col, g, a.K - col);
         }
     }
     if (!a.sums) return;
-    float* out = a.sums + static_cast<int64_t>(blockIdx.x) * a.K;
+    float* out = a.sums + static_cast<int64_t>(blockIdx.x) * a.ldsums;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if constexpr (ROWS > 1) {
@@ -388,114 +578,207 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void ag_norm_backward_kernel(Nor
                 if (col < a.K) out[col] = t;
             }
         } else {
-            const int col = (lane + j * G) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < a.K) out[col + e] = dw[j][e];
+            const int col = (lane + j * G) * 8;     // the rows of sums are whole vectors
+            if (col < a.K) {
+                *reinterpret_cast<f32x4*>(out + col) = f32x4{dw[j][0], dw[j][1], dw[j][2], dw[j][3]};
+                *reinterpret_cast<f32x4*>(out + col + 4) = f32x4{dw[j][4], dw[j][5], dw[j][6], dw[j][7]};
+            }
         }
     }
 }
 
-// Longer rows: read twice, and the sums of dw kept in the workgroup's row of `sums`.
+// Longer rows in two passes: mean(g n) of each row, and then columns, 8 to a thread, over `rows` rows each.
 template <bool BF16>
-__global__ __launch_bounds__(kLongThreads) void ag_norm_backward_long_kernel(NormBackwardArgs a)
+__global__ __launch_bounds__(kLongThreads) void ag_norm_backward_mean_kernel(NormBackwardArgs a)
 {
+    constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16;
     __shared__ float lds[2][16];
-    const float per_k = 1.f / a.K;
-    float* out = a.sums ? a.sums + static_cast<int64_t>(blockIdx.x) * a.K : nullptr;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
         const float rstd = a.rstd[row];
+        const void *ds = row_of<DTYPE>(a.dy, row, a.lddy), *hs = row_of<DTYPE>(a.h, row, a.ldh);
         float s = 0.f;
-        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 8) {
-            const int left = a.K - col;
-            float dy[8], n[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-            load_f32<BF16>(dy, a.dy + row * a.lddy + col, left);
-            load_f32<BF16>(n, a.h + row * a.ldh + col, left);
-            if (a.weight) load_f32<BF16>(w, a.weight + col, left);
+        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 16) {
+            Raw<DTYPE> dy[2], h[2], weight[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {       // past the row's end: zeros
+                const int at = col + j * kLongThreads * 8;
+                dy[j].template load<true>(ds, at, a.K);
+                h[j].template load<true>(hs, at, a.K);
+                if (a.weight) weight[j].template load<true>(a.weight, at, a.K);
+                else weight[j].ones();
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float g[8], n[8], w[8];
+                dy[j].get(g);
+                h[j].get(n);
+                weight[j].get(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += g[e] * (n[e] * rstd) * w[e];
+            }
+        }
+        s = sum_row<kLongThreads>(s, lds, turn);
+        turn ^= 1;
+        if (threadIdx.x == 0) a.means[row] = s / a.K;
+    }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void ag_norm_backward_columns_kernel(NormBackwardArgs a, int column_groups, int rows)
+{
+    constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16, AHEAD = 4;       // rows on their way
+    const int group = static_cast<int>(blockIdx.x) % column_groups, batch = static_cast<int>(blockIdx.x) / column_groups;
+    const int col = (group * 256 + static_cast<int>(threadIdx.x)) * 8;
+    if (col >= a.K) return;
+    Raw<DTYPE> weight;
+    if (a.weight) weight.template load<true>(a.weight, col, a.K);
+    else weight.ones();
+    const bool add = a.dh != nullptr && a.dx != nullptr;
+    float w[8], dw[8] = {};
+    weight.get(w);
+    const int64_t from = static_cast<int64_t>(batch) * rows, end = min(from + rows, a.M);
+    for (int64_t first = from; first < end; first += AHEAD) {
+        Raw<DTYPE> dy[AHEAD], h[AHEAD], dh[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t row = min(first + j, end - 1);
+            dy[j].template load<true>(row_of<DTYPE>(a.dy, row, a.lddy), col, a.K);
+            h[j].template load<true>(row_of<DTYPE>(a.h, row, a.ldh), col, a.K);
+            if (add) dh[j].template load<true>(row_of<DTYPE>(a.dh, row, a.lddh), col, a.K);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t row = first + j;
+            if (row >= end) break;
+            const float rstd = a.rstd[row];
+            float g[8], n[8], d[8] = {};
+            dy[j].get(g);
+            h[j].get(n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 n[e] *= rstd;
-                s += dy[e] * w[e] * n[e];
-                if (out && e < left) out[col + e] = (row == blockIdx.x ? 0.f : out[col + e]) + dy[e] * n[e];
+                dw[e] += g[e] * n[e];
             }
-        }
-        if (!a.dx) continue;
-        const float c = sum_row<kLongThreads>(s, lds, turn) * per_k;
-        turn ^= 1;
-        for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 8) {
-            const int left = a.K - col;
-            float dy[8], n[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, dh[8] = {};
-            load_f32<BF16>(dy, a.dy + row * a.lddy + col, left);
-            load_f32<BF16>(n, a.h + row * a.ldh + col, left);
-            if (a.weight) load_f32<BF16>(w, a.weight + col, left);
-            if (a.dh) load_f32<BF16>(dh, a.dh + row * a.lddh + col, left);
+            if (!a.dx) continue;
+            const float c = a.means[row];
+            if (add) dh[j].get(d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dy[e] = rstd * (dy[e] * w[e] - n[e] * rstd * c) + dh[e];
-            store_16<BF16>(a.dx + row * a.lddx + col, dy, left);
+            for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] * w[e] - n[e] * c) + d[e];
+            store_16<BF16>(a.dx + row * a.lddx + col, g, a.K - col);
         }
+    }
+    if (!a.sums) return;
+    float* out = a.sums + batch * a.ldsums + col;
+    *reinterpret_cast<f32x4*>(out) = f32x4{dw[0], dw[1], dw[2], dw[3]};
+    *reinterpret_cast<f32x4*>(out + 4) = f32x4{dw[4], dw[5], dw[6], dw[7]};
+}
+
+// dw(k) (+)= the workgroups' sums, in order within 32 lanes and then over them.  32 columns to a workgroup, 4 to a thread.
+__global__ __launch_bounds__(256) void ag_norm_dw_kernel(NormDwArgs a)
+{
+    __shared__ float part[32][33];
+    const int c = (threadIdx.x & 7) * 4, lane = threadIdx.x >> 3;
+    const float* from = a.sums + static_cast<int64_t>(blockIdx.x) * 32 + c;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int q = lane; q < a.parts; q += 32) s += *reinterpret_cast<const f32x4*>(from + q * a.ldsums);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[lane][c + e] = s[e];
+    __syncthreads();
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x >= 32 || col >= a.K) return;
+    float t = 0.f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) t += part[r][threadIdx.x];
+    if (a.dtype == AG_F32) {
+        float* p = static_cast<float*>(a.dw) + col;
+        *p = a.accumulate ? *p + t : t;
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.dw) + col;
+        if (a.accumulate) t += a.dtype == AG_BF16 ? to_f32<true>(*p) : to_f32<false>(*p);
+        *p = a.dtype == AG_BF16 ? from_f32<true>(t) : from_f32<false>(t);
     }
 }
 
 // ---------------------------------------------------------------- choice of a kernel
 
 using RowsFn = void (*)(RowsArgs);
-template <int DTYPE, bool NORM> RowsFn pick_rows(const RowsShape& s)
+template <int DTYPE, bool NORM, bool TAIL> RowsFn pick_rows(const RowsShape& s)
 {
     switch (s.threads * 8 + s.vectors) {
-    case 16 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 16, 1>;
-    case 64 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 64, 1>;
-    case 64 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 64, 2>;
-    case 256 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 256, 1>;
-    case 256 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 256, 2>;
-    case 256 * 8 + 4: return ag_rows_kernel<DTYPE, NORM, 256, 4>;
-    case 1024 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 1024, 2>;
-    case 1024 * 8 + 4: return ag_rows_kernel<DTYPE, NORM, 1024, 4>;
+    case 16 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 16, 1, TAIL>;
+    case 64 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 64, 1, TAIL>;
+    case 64 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 64, 2, TAIL>;
+    case 256 * 8 + 1: return ag_rows_kernel<DTYPE, NORM, 256, 1, TAIL>;
+    case 256 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 256, 2, TAIL>;
+    case 512 * 8 + 2: return ag_rows_kernel<DTYPE, NORM, 512, 2, TAIL>;
+    case 1024 * 8 + 2:
+        if constexpr (NORM) return ag_rows_kernel<DTYPE, NORM, 1024, 2, TAIL>;
+        else return nullptr;
+    case 512 * 8 + 4:
+        if constexpr (NORM) return nullptr;
+        else return ag_rows_kernel<DTYPE, NORM, 512, 4, TAIL>;
+    case 1024 * 8 + 4:
+        if constexpr (NORM) return nullptr;
+        else return ag_rows_kernel<DTYPE, NORM, 1024, 4, TAIL>;
     case kLongThreads * 8: return ag_rows_long_kernel<DTYPE, NORM>;
     default: return nullptr;
     }
 }
+template <int DTYPE, bool NORM> RowsFn pick_rows(const RowsShape& s, int K)
+{
+    return K % 8 ? pick_rows<DTYPE, NORM, true>(s) : pick_rows<DTYPE, NORM, false>(s);
+}
 
 using NormBackwardFn = void (*)(NormBackwardArgs);
-template <bool BF16> NormBackwardFn pick_backward(const RowsShape& s)
+template <bool BF16, bool TAIL> NormBackwardFn pick_backward(const RowsShape& s)
 {
     switch (s.threads * 8 + s.vectors) {
-    case 16 * 8 + 1: return ag_norm_backward_kernel<BF16, 16, 1>;
-    case 64 * 8 + 1: return ag_norm_backward_kernel<BF16, 64, 1>;
-    case 64 * 8 + 2: return ag_norm_backward_kernel<BF16, 64, 2>;
-    case 256 * 8 + 1: return ag_norm_backward_kernel<BF16, 256, 1>;
-    case 256 * 8 + 2: return ag_norm_backward_kernel<BF16, 256, 2>;
-    case 256 * 8 + 4: return ag_norm_backward_kernel<BF16, 256, 4>;
-    case 1024 * 8 + 2: return ag_norm_backward_kernel<BF16, 1024, 2>;
-    case 1024 * 8 + 4: return ag_norm_backward_kernel<BF16, 1024, 4>;
-    case kLongThreads * 8: return ag_norm_backward_long_kernel<BF16>;
+    case 16 * 8 + 1: return ag_norm_backward_kernel<BF16, 16, 1, TAIL>;
+    case 64 * 8 + 1: return ag_norm_backward_kernel<BF16, 64, 1, TAIL>;
+    case 64 * 8 + 2: return ag_norm_backward_kernel<BF16, 64, 2, TAIL>;
+    case 256 * 8 + 1: return ag_norm_backward_kernel<BF16, 256, 1, TAIL>;
+    case 256 * 8 + 2: return ag_norm_backward_kernel<BF16, 256, 2, TAIL>;
+    case 512 * 8 + 2: return ag_norm_backward_kernel<BF16, 512, 2, TAIL>;
+    case 1024 * 8 + 2: return ag_norm_backward_kernel<BF16, 1024, 2, TAIL>;
     default: return nullptr;
     }
+}
+template <bool BF16> NormBackwardFn pick_backward(const RowsShape& s, int K)
+{
+    return K % 8 ? pick_backward<BF16, true>(s) : pick_backward<BF16, false>(s);
 }
 
 }  // namespace
 
 // ---------------------------------------------------------------- launchers
 
-RowsShape rows_shape(int64_t K)
+// Four vectors a thread where the row itself is all that is kept (codes of 4096 x 16384 bf16: 512 threads with four 39.6 us,
+// 1024 with two 47 to 52).  A norm keeps the residual, the weight and products in fp32 too and has no registers for them (with
+// 512 threads and four 104 us, 1024 and two 94 to 99; 4000 x 20000: 1024 and four 185, read twice 164).
+RowsShape rows_shape(int64_t K, bool norm)
 {
     if (K <= 128) return {16, 1, 16};
     if (K <= 512) return {64, 1, 4};
     if (K <= 1024) return {64, 2, 4};
     if (K <= 2048) return {256, 1, 1};
     if (K <= 4096) return {256, 2, 1};
-    if (K <= 8192) return {256, 4, 1};
-    if (K <= 16384) return {1024, 2, 1};
-    if (K <= 32768) return {1024, 4, 1};
+    if (K <= 8192) return {512, 2, 1};
+    if (norm && K <= 16384) return {1024, 2, 1};
+    if (!norm && K <= 16384) return {512, 4, 1};
+    if (!norm && K <= 32768) return {1024, 4, 1};
     return {kLongThreads, 0, 1};
 }
 
+RowsShape norm_backward_shape(int64_t K) { return K <= 16384 ? rows_shape(K, true) : RowsShape{256, 0, 1}; }
+
 hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hipStream_t stream)
 {
-    const RowsShape s = rows_shape(a.K);
-    const RowsFn fn = norm ? (dtype == AG_BF16 ? pick_rows<AG_BF16, true>(s) : dtype == AG_F16 ? pick_rows<AG_F16, true>(s) : nullptr)
-                           : (dtype == AG_BF16 ? pick_rows<AG_BF16, false>(s) : dtype == AG_F16 ? pick_rows<AG_F16, false>(s)
-                                                                                                : pick_rows<AG_F32, false>(s));
+    const RowsShape s = rows_shape(a.K, norm);
+    const RowsFn fn = norm ? (dtype == AG_BF16 ? pick_rows<AG_BF16, true>(s, a.K) : dtype == AG_F16 ? pick_rows<AG_F16, true>(s, a.K) : nullptr)
+                           : (dtype == AG_BF16 ? pick_rows<AG_BF16, false>(s, a.K) : dtype == AG_F16 ? pick_rows<AG_F16, false>(s, a.K)
+                                                                                                : pick_rows<AG_F32, false>(s, a.K));
     if (fn == nullptr || programs < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(static_cast<uint32_t>(s.threads * s.per_group)), 0, stream, a);
     return hipGetLastError();
@@ -503,8 +786,9 @@ hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hi
 
 hipError_t launch_dequantize(const DequantizeArgs& a, int dtype, hipStream_t stream)
 {
-    const int64_t groups = (a.M * ((a.K + 15) / 16) + 255) / 256;
-    if (groups < 1 || groups > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t vectors = a.M * ((a.K + 7) / 8), per = 256 * kDequantizeVectors;
+    if (vectors < 1) return hipErrorInvalidValue;
+    const int64_t groups = std::min<int64_t>((vectors + per - 1) / per, kMaxRowsPrograms);
     auto fn = dtype == AG_BF16 ? ag_dequantize_kernel<AG_BF16> : dtype == AG_F16 ? ag_dequantize_kernel<AG_F16> : ag_dequantize_kernel<AG_F32>;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, stream, a);
     return hipGetLastError();
@@ -512,10 +796,32 @@ hipError_t launch_dequantize(const DequantizeArgs& a, int dtype, hipStream_t str
 
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int bf16, int programs, hipStream_t stream)
 {
-    const RowsShape s = rows_shape(a.K);
-    const NormBackwardFn fn = bf16 ? pick_backward<true>(s) : pick_backward<false>(s);
+    const RowsShape s = norm_backward_shape(a.K);
+    const NormBackwardFn fn = bf16 ? pick_backward<true>(s, a.K) : pick_backward<false>(s, a.K);
     if (fn == nullptr || programs < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(static_cast<uint32_t>(s.threads * s.per_group)), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_backward_long(const NormBackwardArgs& a, int bf16, int batches, int rows, hipStream_t stream)
+{
+    const int64_t column_groups = (a.K + 2047) / 2048, grid = column_groups * batches;
+    if (batches < 1 || rows < 1 || grid > kMaxRowsPrograms || (a.dx && !a.means)) return hipErrorInvalidValue;
+    if (a.dx) {
+        hipLaunchKernelGGL((bf16 ? ag_norm_backward_mean_kernel<true> : ag_norm_backward_mean_kernel<false>),
+                           dim3(static_cast<uint32_t>(std::min<int64_t>(a.M, kMaxRowsPrograms))), dim3(kLongThreads), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((bf16 ? ag_norm_backward_columns_kernel<true> : ag_norm_backward_columns_kernel<false>),
+                       dim3(static_cast<uint32_t>(grid)), dim3(256), 0, stream, a, static_cast<int>(column_groups), rows);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_dw(const NormDwArgs& a, hipStream_t stream)
+{
+    if (a.K < 1 || (a.parts > 0 && (a.ldsums % 32 != 0 || a.ldsums < a.K))) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ag_norm_dw_kernel, dim3(static_cast<uint32_t>((a.K + 31) / 32)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

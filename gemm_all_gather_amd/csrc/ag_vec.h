@@ -64,16 +64,20 @@ __device__ __forceinline__ void store_16(uint16_t* p, const float (&v)[8], int n
 // Eight 8-bit codes at any address.
 struct __attribute__((packed, aligned(1))) Any8 { u32x2 v; };
 
+__device__ __forceinline__ void code_values(float (&v)[8], u32x2 codes)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = static_cast<float>(static_cast<int8_t>(codes.x >> (8 * e)));
+        v[4 + e] = static_cast<float>(static_cast<int8_t>(codes.y >> (8 * e)));
+    }
+}
+
 // n <= 8 codes as numbers, the others 0.
 __device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, int n)
 {
     if (n >= 8) {
-        const u32x2 t = reinterpret_cast<const Any8*>(p)->v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = static_cast<float>(static_cast<int8_t>(t.x >> (8 * e)));
-            v[4 + e] = static_cast<float>(static_cast<int8_t>(t.y >> (8 * e)));
-        }
+        code_values(v, reinterpret_cast<const Any8*>(p)->v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = e < n ? static_cast<float>(p[e]) : 0.f;
