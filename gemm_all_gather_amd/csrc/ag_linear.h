@@ -86,6 +86,7 @@ struct LinearStreamArgs {
 hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, int cus, hipStream_t stream);
 
 // The same of 8-bit integers.
+constexpr int kLinearI8StreamRows = 64;
 struct LinearI8StreamArgs {
     const int8_t* x;
     const int8_t* w;
@@ -96,9 +97,13 @@ struct LinearI8StreamArgs {
     LinearEpilogue epi;
 };
 hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cus, hipStream_t stream);
-// Copies rows of bytes to aligned rows (ld_dst a multiple of 16).
-hipError_t launch_linear_i8_pack(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst, int64_t rows, int64_t cols,
-                                 hipStream_t stream);
+// Copies rows of bytes to aligned rows (ld_dst a multiple of 16); rows 0: nothing.
+struct LinearI8Pack {
+    const int8_t* src;
+    int8_t* dst;
+    int64_t ld_src, ld_dst, rows, cols;
+};
+hipError_t launch_linear_i8_pack(const LinearI8Pack& first, const LinearI8Pack& second, hipStream_t stream);
 
 // Copies rows to aligned rows (ld_dst a multiple of 8).
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,

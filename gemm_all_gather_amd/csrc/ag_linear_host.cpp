@@ -36,7 +36,8 @@ struct Operand {
     int esize = 2;
     bool pack = false;
     uint64_t copy_offset = 0;
-    int64_t copy_ld() const { return (cols * esize + 15) / 16 * 16 / esize; }
+    // whole vectors; of 8-bit integers whole 128-byte lines, a stage's part of a row
+    int64_t copy_ld() const { return esize == 1 ? (cols + 127) / 128 * 128 : (cols + 7) / 8 * 8; }
     uint64_t copy_bytes() const { return up256(static_cast<uint64_t>(rows) * copy_ld() * esize); }
 };
 
@@ -64,7 +65,7 @@ struct Kind {
 constexpr Kind kKinds[ag::kLinearTiles] = {{{1.42, 1.46, 1.48}, 6.0},     // 256 x 256
                                            {{0.53, 0.60, 0.75}, 4.0},     // 128 x 128
                                            {{1.02, 0.98, 1.00}, 5.0}};    // 256 x 128
-constexpr Kind kKindsI8[ag::kLinearTiles] = {{{1.42, 0, 0}, 6.0}, {{0.53, 0, 0}, 4.0}, {{1.02, 0, 0}, 5.0}};   // 128-wide steps
+constexpr Kind kKindsI8[ag::kLinearTiles] = {{{1.45, 0, 0}, 6.0}, {{0.58, 0, 0}, 4.0}, {{0.93, 0, 0}, 5.0}};   // 128-wide steps
 const Kind& kind_of(const Product& p, int tile) { return p.i8 ? kKindsI8[tile] : kKinds[tile]; }
 
 // Whole tiles of one kind; us is a tile's time.
@@ -228,16 +229,23 @@ ag::LinearGemmArgs gemm_args(const Product& p, const uint16_t* A, int64_t lda, c
     return a;
 }
 
-ag_status_t pack(const Operand& o, void* workspace, hipStream_t stream, const int8_t** at, int64_t* ld)
+// Both operands of 8-bit integers; the copies that are needed in one launch.
+ag_status_t pack(const Operand& x, const Operand& w, void* workspace, hipStream_t stream, const int8_t* (*at)[2], int64_t (*ld)[2])
 {
-    *at = reinterpret_cast<const int8_t*>(o.at);
-    *ld = o.rows > 1 && !o.pack ? o.ld : o.copy_ld();
-    if (!o.pack) return AG_OK;
-    int8_t* dst = static_cast<int8_t*>(workspace) + o.copy_offset;
-    const hipError_t e = ag::launch_linear_i8_pack(*at, o.ld, dst, *ld, o.rows, o.cols, stream);
-    if (e != hipSuccess) return fail_hip(e, "linear operand copy");
-    *at = dst;
-    return AG_OK;
+    ag::LinearI8Pack copy[2]{};
+    const Operand* o[2] = {&x, &w};
+    for (int i = 0; i < 2; ++i) {
+        const int8_t* src = reinterpret_cast<const int8_t*>(o[i]->at);
+        (*at)[i] = src;
+        (*ld)[i] = o[i]->rows > 1 && !o[i]->pack ? o[i]->ld : o[i]->copy_ld();
+        if (!o[i]->pack) continue;
+        int8_t* dst = static_cast<int8_t*>(workspace) + o[i]->copy_offset;
+        copy[i] = ag::LinearI8Pack{src, dst, o[i]->ld, (*ld)[i], o[i]->rows, o[i]->cols};
+        (*at)[i] = dst;
+    }
+    if (!x.pack && !w.pack) return AG_OK;
+    const hipError_t e = ag::launch_linear_i8_pack(copy[0], copy[1], stream);
+    return e == hipSuccess ? AG_OK : fail_hip(e, "linear operand copy");
 }
 
 ag_status_t run_product(const Product& p, const ag::LinearGemmArgs& a, int bf16, hipStream_t stream)
@@ -357,7 +365,12 @@ ag_status_t plan_forward_i8(const ag_linear_i8_args_t* a, int cus, ForwardI8* f)
     p.I = M;
     p.J = N;
     p.R = K;
-    p.stream = M <= 16 || (M <= ag::kLinearStreamRows && N * K < (int64_t{1} << 23));
+    // Few rows of x: w is what there is to move, and is streamed.  Every workgroup reads all of x beside its 16 rows of w, so tiles
+    // with cut reductions take over the sooner, the larger w and the longer a row (bf16, us streamed and in tiles): 32 rows, N x
+    // K 8192 x 3584 12.4 and 18.6, 3584 x 8192 14.0 and 18.9, 8192 x 8192 26.0 and 27.0, 28672 x 4096 44.6 and 33.0; 64 rows, 2048
+    // x 2048 8.2 and 15.5, 4096 x 4096 12.3 and 15.9, 512 x 4096 12.1 and 13.9, 1024 x 8192 20.9 and 15.3, 3584 x 8192 21.5 and 20.1.
+    p.stream = M <= 16 || (M <= 32 && N * K <= (int64_t{1} << 26)) ||
+               (M <= ag::kLinearI8StreamRows && K <= 4096 && N * K <= (int64_t{1} << 24));
     if (!p.stream) {
         if ((s = choose(&p, cus)) != AG_OK) return s;
         f->ox = Operand{f->x.at, f->x.ld, M, K, 1};
@@ -367,7 +380,7 @@ ag_status_t plan_forward_i8(const ag_linear_i8_args_t* a, int cus, ForwardI8* f)
         f->partial_offset = f->workspace;
         f->workspace += p.partial_bytes;
     }
-    f->launches = p.launches() + (f->ox.pack ? 1 : 0) + (f->ow.pack ? 1 : 0);
+    f->launches = p.launches() + (f->ox.pack || f->ow.pack ? 1 : 0);
     return AG_OK;
 }
 
@@ -645,12 +658,11 @@ ag_status_t ag_linear_i8(const ag_linear_i8_args_t* args, void* workspace, size_
         const hipError_t err = ag::launch_linear_i8_stream(a, bf16, cus, stream);
         return err == hipSuccess ? ok() : fail_hip(err, "linear stream");
     }
-    const int8_t *A, *B;
-    int64_t lda, ldb;
-    if ((s = pack(f.ox, workspace, stream, &A, &lda)) != AG_OK) return s;
-    if ((s = pack(f.ow, workspace, stream, &B, &ldb)) != AG_OK) return s;
+    const int8_t* at[2];
+    int64_t ld[2];
+    if ((s = pack(f.ox, f.ow, workspace, stream, &at, &ld)) != AG_OK) return s;
     float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.partial_offset);
-    ag::LinearI8GemmArgs a{gemm_args(f.product, reinterpret_cast<const uint16_t*>(A), lda, reinterpret_cast<const uint16_t*>(B), ldb, e,
+    ag::LinearI8GemmArgs a{gemm_args(f.product, reinterpret_cast<const uint16_t*>(at[0]), ld[0], reinterpret_cast<const uint16_t*>(at[1]), ld[1], e,
                                      partial),
                            args->x_scale, args->w_scale};
     hipError_t err = ag::launch_linear_i8_gemm(a, bf16, f.product.tile, static_cast<int>(f.product.programs), stream);

@@ -81,35 +81,47 @@ __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI
         live[b] = m < a.M;
         x[b] = a.x + (live[b] ? m : 0) * a.ldx + k_lane;
     }
+    // What the epilogue's threads read, one per row of x and 4 rows of w, is on its way before the weights.
+    const int tid = threadIdx.x;
+    const int64_t my_row = (tid >> 6) * 16 + (tid & 15), my_col = n0 + ((tid & 63) >> 4) * 4;
+    const int my_n = tid < MB * 64 && my_row < a.M ? static_cast<int>(max(int64_t{0}, min(int64_t{4}, a.N - my_col))) : 0;
+    float scale[8] = {}, bias[8] = {}, residual[8] = {}, x_scale = 0.f;
+    if (my_n > 0) {
+        x_scale = a.x_scale[my_row];
+        load_scales(scale, a.w_scale + my_col, my_n);
+        if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + my_col, my_n);
+        if (a.epi.residual) load_f32<BF16>(residual, a.epi.residual + my_row * a.epi.ldr + my_col, my_n);
+    }
     i32x4 acc[MB];
     const i32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[b] = zero;
 
+    constexpr int U = 4 / MB;           // 64-wide steps of a block: more rows of x leave registers for fewer
     struct Block {
-        i32x4 w[4], x[MB][4];
+        i32x4 w[U], x[MB][U];
     };
     auto load = [&](Block& t, int64_t k) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t.w[u] = load16(w + k + u * 64);
+        for (int u = 0; u < U; ++u) t.w[u] = load16(w + k + u * 64);
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 t.x[b][u] = zero;
                 if (live[b]) t.x[b][u] = load16(x[b] + k + u * 64);
             }
     };
     auto multiply = [&](const Block& t) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int b = 0; b < MB; ++b) acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.w[u], t.x[b][u], acc[b], 0, 0, 0);
     };
-    // two 256-wide blocks on their way per wave while a third is multiplied
-    constexpr int64_t NEXT = WAVES * 256;
-    const int64_t whole = a.K / 256 * 256;
-    int64_t k = wave * 256;
+    // two blocks on their way per wave while a third is multiplied
+    constexpr int64_t WIDE = 64 * U, NEXT = WAVES * WIDE;
+    const int64_t whole = a.K / WIDE * WIDE;
+    int64_t k = wave * WIDE;
     Block even, odd;
     if (k < whole) load(even, k);
     for (; k < whole; k += 2 * NEXT) {
@@ -119,10 +131,10 @@ __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI
         if (k + 2 * NEXT < whole) load(even, k + 2 * NEXT);
         if (more) multiply(odd);
     }
-    if (whole < a.K && wave == (whole / 256) % WAVES) {   // the last, shorter block
+    if (whole < a.K && wave == (whole / WIDE) % WAVES) {   // the last, shorter block
         k = whole;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t left = a.K - k - u * 64 - k_lane;
             const i32x4 fw = load16(w + k + u * 64, left);
 #pragma unroll
@@ -135,38 +147,38 @@ __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI
 #pragma unroll
     for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[b];
     __syncthreads();
-    // one thread per row of x and 4 rows of w
-    const int tid = threadIdx.x;
-    if (tid < MB * 64) {
+    if (my_n > 0) {
         const int b = tid >> 6, l = tid & 63;
         i32x4 s = part[0][b][l];
 #pragma unroll
         for (int wv = 1; wv < WAVES; ++wv) s += part[wv][b][l];
-        const int64_t m = b * 16 + (l & 15), col = n0 + (l >> 4) * 4;
-        const int n = static_cast<int>(max(int64_t{0}, min(int64_t{4}, a.N - col)));
-        if (m < a.M && n > 0) {
-            float v[8] = {}, scale[8], bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float v[8] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __int_as_float(s[e]);
-            load_scales(scale, a.w_scale + col, n);
-            apply_scales(v, a.x_scale[m], scale);
-            if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
-            finish_layer<BF16>(v, bias, a.epi, a.epi.act, m, col, n);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = __int_as_float(s[e]);
+        apply_scales(v, x_scale, scale);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += bias[e];
+        if (a.epi.z) store_16<BF16>(a.epi.z + my_row * a.epi.ldz + my_col, v, my_n);
+        activate(v, a.epi.act);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += residual[e];
+        store_16<BF16>(static_cast<uint16_t*>(a.epi.out) + my_row * a.epi.ldo + my_col, v, my_n);
     }
 }
 
 // ---------------------------------------------------------------- rows to aligned rows
 
-// A matrix's rows to rows of 16-byte multiples, for operands that do not start on 4 bytes or have other strides.
-__global__ __launch_bounds__(256) void ag_linear_i8_pack_kernel(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst,
-                                                                int64_t rows, int64_t cols)
+// Rows to rows of 16-byte multiples, for operands that do not start on 4 bytes or have other strides: one matrix, or both
+// operands one after the other in one launch.
+__global__ __launch_bounds__(256) void ag_linear_i8_pack_kernel(LinearI8Pack first, LinearI8Pack second, uint32_t first_groups)
 {
-    const int64_t per_row = (cols + 15) / 16;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t row = id / per_row, col = (id - row * per_row) * 16;
-    if (row >= rows) return;
-    *reinterpret_cast<i32x4*>(dst + row * ld_dst + col) = load16(src + row * ld_src + col, cols - col);
+    const bool one = blockIdx.x < first_groups;
+    const LinearI8Pack& p = one ? first : second;
+    const int64_t per_row = (p.cols + 15) / 16;
+    const int64_t id = static_cast<int64_t>(one ? blockIdx.x : blockIdx.x - first_groups) * 256 + threadIdx.x;
+    const int64_t row = id >> 32 ? id / per_row : static_cast<uint32_t>(id) / static_cast<uint32_t>(per_row), col = (id - row * per_row) * 16;
+    if (row >= p.rows) return;
+    *reinterpret_cast<i32x4*>(p.dst + row * p.ld_dst + col) = load16(p.src + row * p.ld_src + col, p.cols - col);
 }
 
 using StreamFn = void (*)(LinearI8StreamArgs);
@@ -209,20 +221,21 @@ hipError_t launch_linear_i8_join(const LinearI8GemmArgs& a, int bf16, int tile, 
 hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cus, hipStream_t stream)
 {
     dim3 grid;
-    if (a.M < 1 || a.M > kLinearStreamRows || !grid_of(a.N, 16, &grid)) return hipErrorInvalidValue;
+    if (a.M < 1 || a.M > kLinearI8StreamRows || !grid_of(a.N, 16, &grid)) return hipErrorInvalidValue;
     const bool wide = static_cast<int64_t>(grid.x) <= cus;
     const StreamFn fn = a.M <= 16 ? (bf16 ? pick_stream<true, 1>(wide) : pick_stream<false, 1>(wide))
-                                  : (bf16 ? pick_stream<true, 2>(wide) : pick_stream<false, 2>(wide));
+                        : a.M <= 32 ? (bf16 ? pick_stream<true, 2>(wide) : pick_stream<false, 2>(wide))
+                                    : (bf16 ? pick_stream<true, 4>(wide) : pick_stream<false, 4>(wide));
     hipLaunchKernelGGL(fn, grid, dim3(wide ? 1024 : 512), 0, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_linear_i8_pack(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst, int64_t rows, int64_t cols,
-                                 hipStream_t stream)
+hipError_t launch_linear_i8_pack(const LinearI8Pack& first, const LinearI8Pack& second, hipStream_t stream)
 {
-    dim3 grid;
-    if (!grid_of(rows * ((cols + 15) / 16), 256, &grid)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(ag_linear_i8_pack_kernel, grid, dim3(256), 0, stream, src, ld_src, dst, ld_dst, rows, cols);
+    auto groups = [](const LinearI8Pack& p) { return (p.rows * ((p.cols + 15) / 16) + 255) / 256; };
+    const int64_t one = groups(first), all = one + groups(second);
+    if (all < 1 || all >= (int64_t{1} << 24)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ag_linear_i8_pack_kernel, dim3(static_cast<uint32_t>(all)), dim3(256), 0, stream, first, second, static_cast<uint32_t>(one));
     return hipGetLastError();
 }
 

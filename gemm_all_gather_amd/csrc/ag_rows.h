@@ -77,6 +77,8 @@ struct NormDwArgs {
     int32_t accumulate;
 };
 hipError_t launch_norm_dw(const NormDwArgs& a, hipStream_t stream);
+// Both gradients of little work in one launch (rows of up to 4096; no sums).
+hipError_t launch_norm_backward_small(const NormBackwardArgs& a, const NormDwArgs& d, int bf16, int dx_programs, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int bf16, int programs, hipStream_t stream);
 // Longer rows: `batches` of `rows` rows each, and as many rows of sums.
 hipError_t launch_norm_backward_long(const NormBackwardArgs& a, int bf16, int batches, int rows, hipStream_t stream);

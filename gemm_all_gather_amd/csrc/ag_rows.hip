@@ -491,11 +491,24 @@ __device__ __forceinline__ float sum_row(float s, float (*lds)[16], int turn)
     return s;
 }
 
+// One element of dw: an earlier gradient, rounding, store.
+__device__ __forceinline__ void put_dw(const NormDwArgs& a, int col, float t)
+{
+    if (a.dtype == AG_F32) {
+        float* p = static_cast<float*>(a.dw) + col;
+        *p = a.accumulate ? *p + t : t;
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.dw) + col;
+        if (a.accumulate) t += a.dtype == AG_BF16 ? to_f32<true>(*p) : to_f32<false>(*p);
+        *p = a.dtype == AG_BF16 ? from_f32<true>(t) : from_f32<false>(t);
+    }
+}
+
 // With n = h rstd and c = mean(g n): dx = rstd (g - n c) + dh, and dy n for dw, which a workgroup sums over its rows in
 // registers (its waves' sums joined through LDS where they take rows of their own).  The row stays as it was loaded and is
 // taken apart twice, so that few registers leave many rows on their way.
 template <bool BF16, int G, int V, bool TAIL>
-__global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(NormBackwardArgs a)
+__device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int program, int programs)
 {
     constexpr int ROWS = group_threads(G) / G;
     constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16;
@@ -515,7 +528,7 @@ __global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(Norm
     const bool add = a.dh != nullptr && a.dx != nullptr;
     const float per_k = 1.f / max(a.K, 1);
     int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.M; first += static_cast<int64_t>(gridDim.x) * ROWS) {
+    for (int64_t first = static_cast<int64_t>(program) * ROWS; first < a.M; first += static_cast<int64_t>(programs) * ROWS) {
         const int64_t mine = first + (ROWS > 1 ? threadIdx.x / G : 0), row = min(mine, a.M - 1);
         const bool live = mine < a.M;
         const void *ds = row_of<DTYPE>(a.dy, row, a.lddy), *hs = row_of<DTYPE>(a.h, row, a.ldh), *es = row_of<DTYPE>(a.dh, row, a.lddh);
@@ -562,7 +575,7 @@ __global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(Norm
         }
     }
     if (!a.sums) return;
-    float* out = a.sums + static_cast<int64_t>(blockIdx.x) * a.ldsums;
+    float* out = a.sums + static_cast<int64_t>(program) * a.ldsums;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if constexpr (ROWS > 1) {
@@ -585,6 +598,64 @@ __global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(Norm
             }
         }
     }
+}
+
+template <bool BF16, int G, int V, bool TAIL>
+__global__ __launch_bounds__(group_threads(G)) void ag_norm_backward_kernel(NormBackwardArgs a)
+{
+    backward_rows<BF16, G, V, TAIL>(a, blockIdx.x, gridDim.x);
+}
+
+// dw of 64 columns straight from dy and h, 8 columns to a thread and every 32nd row: for little work, where a second pass over
+// the rows beside the first costs less than a second launch after it.
+template <bool BF16>
+__device__ __forceinline__ void backward_weight(const NormBackwardArgs& a, const NormDwArgs& d, int block, float (*part)[65])
+{
+    constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16;
+    const int c = (threadIdx.x & 7) * 8, lane = threadIdx.x >> 3, col = block * 64 + c;
+    float dw[8] = {};
+    if (col < a.K) {
+#pragma unroll 1
+        for (int64_t first = lane; first < a.M; first += 128) {
+            Raw<DTYPE> dy[4], h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {       // past the last row nothing is loaded
+                const int64_t row = min(first + 32 * j, a.M - 1);
+                const int K = first + 32 * j < a.M ? a.K : 0;
+                dy[j].template load<true>(row_of<DTYPE>(a.dy, row, a.lddy), col, K);
+                h[j].template load<true>(row_of<DTYPE>(a.h, row, a.ldh), col, K);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (first + 32 * j >= a.M) break;
+                const float rstd = a.rstd[first + 32 * j];
+                float g[8], n[8];
+                dy[j].get(g);
+                h[j].get(n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dw[e] += g[e] * (n[e] * rstd);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[lane][c + e] = dw[e];
+    __syncthreads();
+    const int out = block * 64 + threadIdx.x;
+    if (threadIdx.x >= 64 || out >= a.K) return;
+    float t = 0.f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) t += part[r][threadIdx.x];
+    put_dw(d, out, t);
+}
+
+template <bool BF16, int G, int V, bool TAIL>
+__global__ __launch_bounds__(256) void ag_norm_backward_small_kernel(NormBackwardArgs a, NormDwArgs d, int dx_programs)
+{
+    static_assert(group_threads(G) == 256, "both parts take 256 threads");
+    __shared__ float part[32][65];
+    const int p = blockIdx.x;
+    if (p < dx_programs) backward_rows<BF16, G, V, TAIL>(a, p, dx_programs);
+    else backward_weight<BF16>(a, d, p - dx_programs, part);
 }
 
 // Longer rows in two passes: mean(g n) of each row, and then columns, 8 to a thread, over `rows` rows each.
@@ -691,14 +762,7 @@ __global__ __launch_bounds__(256) void ag_norm_dw_kernel(NormDwArgs a)
     float t = 0.f;
 #pragma unroll
     for (int r = 0; r < 32; ++r) t += part[r][threadIdx.x];
-    if (a.dtype == AG_F32) {
-        float* p = static_cast<float*>(a.dw) + col;
-        *p = a.accumulate ? *p + t : t;
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(a.dw) + col;
-        if (a.accumulate) t += a.dtype == AG_BF16 ? to_f32<true>(*p) : to_f32<false>(*p);
-        *p = a.dtype == AG_BF16 ? from_f32<true>(t) : from_f32<false>(t);
-    }
+    put_dw(a, col, t);
 }
 
 // ---------------------------------------------------------------- choice of a kernel
@@ -745,6 +809,23 @@ template <bool BF16, bool TAIL> NormBackwardFn pick_backward(const RowsShape& s)
     default: return nullptr;
     }
 }
+using NormBackwardSmallFn = void (*)(NormBackwardArgs, NormDwArgs, int);
+template <bool BF16, bool TAIL> NormBackwardSmallFn pick_backward_small(const RowsShape& s)
+{
+    switch (s.threads * 8 + s.vectors) {
+    case 16 * 8 + 1: return ag_norm_backward_small_kernel<BF16, 16, 1, TAIL>;
+    case 64 * 8 + 1: return ag_norm_backward_small_kernel<BF16, 64, 1, TAIL>;
+    case 64 * 8 + 2: return ag_norm_backward_small_kernel<BF16, 64, 2, TAIL>;
+    case 256 * 8 + 1: return ag_norm_backward_small_kernel<BF16, 256, 1, TAIL>;
+    case 256 * 8 + 2: return ag_norm_backward_small_kernel<BF16, 256, 2, TAIL>;
+    default: return nullptr;
+    }
+}
+template <bool BF16> NormBackwardSmallFn pick_backward_small(const RowsShape& s, int K)
+{
+    return K % 8 ? pick_backward_small<BF16, true>(s) : pick_backward_small<BF16, false>(s);
+}
+
 template <bool BF16> NormBackwardFn pick_backward(const RowsShape& s, int K)
 {
     return K % 8 ? pick_backward<BF16, true>(s) : pick_backward<BF16, false>(s);
@@ -800,6 +881,15 @@ hipError_t launch_norm_backward(const NormBackwardArgs& a, int bf16, int program
     const NormBackwardFn fn = bf16 ? pick_backward<true>(s, a.K) : pick_backward<false>(s, a.K);
     if (fn == nullptr || programs < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(programs)), dim3(static_cast<uint32_t>(s.threads * s.per_group)), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_backward_small(const NormBackwardArgs& a, const NormDwArgs& d, int bf16, int dx_programs, hipStream_t stream)
+{
+    const RowsShape s = norm_backward_shape(a.K);
+    const NormBackwardSmallFn fn = bf16 ? pick_backward_small<true>(s, a.K) : pick_backward_small<false>(s, a.K);
+    if (fn == nullptr || dx_programs < 1 || a.sums != nullptr) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(dx_programs + (a.K + 63) / 64)), dim3(256), 0, stream, a, d, dx_programs);
     return hipGetLastError();
 }
 

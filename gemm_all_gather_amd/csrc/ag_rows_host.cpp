@@ -34,6 +34,10 @@ int64_t row_groups(int64_t M, const RowsShape& s) { return (M + s.per_group - 1)
 // TB/s where these reach 5.7 (the norm of 16384 x 8192 bf16 with residual and codes, 182 and 165 us).
 int rows_programs(int64_t M, const RowsShape& s) { return static_cast<int>(std::min(row_groups(M, s), kMaxRowsPrograms)); }
 
+// A norm's 1024 threads have a CU to themselves, and nothing runs beside the end of one workgroup and the start of the next: they
+// take rows in turn (4096 x 16384 bf16 104 us, a row each 113).
+int norm_programs(int64_t M, const RowsShape& s, int cus) { return s.threads == 1024 ? static_cast<int>(std::min<int64_t>(M, cus)) : rows_programs(M, s); }
+
 // ------------------------------------------------------------------ codes
 
 struct Codes {
@@ -61,7 +65,7 @@ struct Norm {
     int programs = 0;
 };
 
-ag_status_t plan_norm(const ag_rms_norm_args_t* a, Norm* n)
+ag_status_t plan_norm(const ag_rms_norm_args_t* a, int cus, Norm* n)
 {
     if (!a) return fail(AG_ERR_INVALID_ARG, "args is NULL");
     for (int32_t r : a->reserved)
@@ -91,7 +95,7 @@ ag_status_t plan_norm(const ag_rms_norm_args_t* a, Norm* n)
     }
     if (M == 0) return AG_OK;
     n->shape = rows_shape(K, true);
-    n->programs = rows_programs(M, n->shape);
+    n->programs = norm_programs(M, n->shape, cus);
     return AG_OK;
 }
 
@@ -103,6 +107,7 @@ struct NormBackward {
     int64_t ldsums = 0;             // floats from one row of sums to the next
     int64_t means = 0;              // of rows, between the two passes
     bool sum = false;               // dw's sums are joined
+    bool small = false;             // both gradients in one launch, without sums
     uint64_t sums_offset = 0, workspace = 0;
     int launches = 0;
 };
@@ -140,6 +145,14 @@ ag_status_t plan_norm_backward(const ag_rms_norm_backward_args_t* a, int cus, No
     if (M == 0) return AG_OK;
     n->shape = norm_backward_shape(K);
     n->ldsums = (K + 31) / 32 * 32;
+    // Few rows: dw from dy and h again, beside dx, in one launch (80 x 520 fp16 8.6 us for 11.3, 512 x 4096 bf16 10.1 for 11.5; 1024
+    // x 4096 19.4 for 16.0, as every column's sum goes down all rows in 32 lanes).
+    if (n->sum && !n->dx.empty() && K <= 4096 && M <= 512) {
+        n->small = true;
+        n->parts = static_cast<int>(row_groups(M, n->shape));
+        n->launches = 1;
+        return AG_OK;
+    }
     if (n->shape.vectors > 0) {
         // Rows in turn, 1024 threads of a CU: each workgroup leaves a row of sums.  Twice as many measured 211 us for 207
         // (16384 x 8192 bf16), at 1000 x 4100 19.7 for 15.0.
@@ -201,8 +214,9 @@ ag_status_t ag_plan_rms_norm(const ag_rms_norm_args_t* args, int num_cus, ag_row
     if (!plan) return fail(AG_ERR_INVALID_ARG, "plan is NULL");
     if (num_cus < 0) return fail(AG_ERR_INVALID_ARG, "num_cus %d < 0", num_cus);
     ag_status_t s;
+    if (num_cus == 0 && (s = current_cus(&num_cus)) != AG_OK) return s;
     Norm n;
-    if ((s = plan_norm(args, &n)) != AG_OK) return s;
+    if ((s = plan_norm(args, num_cus, &n)) != AG_OK) return s;
     ag_rows_plan_t p{};
     if (n.programs > 0) {
         p.threads_per_row = n.shape.threads;
@@ -221,9 +235,12 @@ ag_status_t ag_plan_rms_norm(const ag_rms_norm_args_t* args, int num_cus, ag_row
 ag_status_t ag_rms_norm(const ag_rms_norm_args_t* args, void* stream)
 {
     Norm n;
-    ag_status_t s = plan_norm(args, &n);
+    // validation first (on any CU count), so that a bad argument is named even without a device
+    ag_status_t s = plan_norm(args, 256, &n);
     if (s != AG_OK) return s;
     if (n.programs == 0) return ok();
+    int cus = 0;
+    if ((s = current_cus(&cus)) != AG_OK) return s;
     RowsArgs a{};
     a.x = args->x;
     a.residual = n.residual.empty() ? nullptr : args->residual;
@@ -241,7 +258,7 @@ ag_status_t ag_rms_norm(const ag_rms_norm_args_t* args, void* stream)
     a.M = args->M;
     a.K = static_cast<int32_t>(args->K);
     a.eps = args->eps;
-    const hipError_t e = launch_rows(a, args->dtype, true, n.programs, static_cast<hipStream_t>(stream));
+    const hipError_t e = launch_rows(a, args->dtype, true, norm_programs(args->M, n.shape, cus), static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : fail_hip(e, "rms norm");
 }
 
@@ -285,6 +302,7 @@ ag_status_t ag_rms_norm_backward(const ag_rms_norm_backward_args_t* args, void* 
     if (s != AG_OK) return s;
     const hipStream_t stream = static_cast<hipStream_t>(stream_);
     float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + n.sums_offset);
+    const NormDwArgs d{sums, args->dw, n.ldsums, n.parts, static_cast<int32_t>(args->K), args->dw_dtype, args->accumulate};
     if (n.parts > 0) {
         NormBackwardArgs a{};
         a.dy = static_cast<const uint16_t*>(args->dy);
@@ -293,7 +311,7 @@ ag_status_t ag_rms_norm_backward(const ag_rms_norm_backward_args_t* args, void* 
         a.weight = static_cast<const uint16_t*>(args->weight);
         a.rstd = args->rstd;
         a.dx = static_cast<uint16_t*>(args->dx);
-        a.sums = n.sum ? sums : nullptr;
+        a.sums = n.sum && !n.small ? sums : nullptr;
         a.ldsums = n.ldsums;
         a.lddy = n.dy.ld;
         a.ldh = n.h.ld;
@@ -303,13 +321,13 @@ ag_status_t ag_rms_norm_backward(const ag_rms_norm_backward_args_t* args, void* 
         a.K = static_cast<int32_t>(args->K);
         a.means = n.means > 0 ? static_cast<float*>(workspace) : nullptr;
         const int bf16 = args->dtype == AG_BF16;
-        const hipError_t e = n.shape.vectors > 0 ? launch_norm_backward(a, bf16, n.parts, stream)
+        const hipError_t e = n.small ? launch_norm_backward_small(a, d, bf16, n.parts, stream)
+                             : n.shape.vectors > 0 ? launch_norm_backward(a, bf16, n.parts, stream)
                                                  : launch_norm_backward_long(a, bf16, n.parts, static_cast<int>(n.rows), stream);
         if (e != hipSuccess) return fail_hip(e, "rms norm gradients");
     }
-    if (n.sum) {
-        const NormDwArgs a{sums, args->dw, n.ldsums, n.parts, static_cast<int32_t>(args->K), args->dw_dtype, args->accumulate};
-        const hipError_t e = launch_norm_dw(a, stream);
+    if (n.sum && !n.small) {
+        const hipError_t e = launch_norm_dw(d, stream);
         if (e != hipSuccess) return fail_hip(e, "rms norm weight gradient");
     }
     return ok();

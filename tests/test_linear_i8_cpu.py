@@ -70,7 +70,7 @@ def test_plans():
     assert one.product.variant == 1 and one.workspace_bytes == 0 and one.launches == 1
     # copies of rows that do not start on 4 bytes
     odd = ag.plan_linear_i8(**dict(FORWARD, K=8191))
-    assert odd.product.packed == 3 and odd.launches >= 3 and odd.workspace_bytes >= (1000 + 3584) * 8192
+    assert odd.product.packed == 3 and odd.launches >= 2 and odd.workspace_bytes >= (1000 + 3584) * 8192
     assert ag.plan_linear_i8(**dict(FORWARD, x=A + 2)).product.packed == 1
     assert ag.plan_linear_i8(**dict(FORWARD, ldw=8194)).product.packed == 2
     assert ag.plan_linear_i8(**dict(FORWARD, x=A + 4, ldw=8196)).product.packed == 0

@@ -310,8 +310,11 @@ class Backward:
             assert_close(self.dx.f64(), dx, rounded_bound(dx, off, self.dtype), f"{what} dx")
             self.dx.check_surroundings(f"{what} dx")
         if self.dw is not None:
-            rows = max(1, 256 // plan.threads_per_row) if plan.threads_per_row else 1
-            adds = -(-M // max(1, plan.n_programs * rows)) + rows + -(-plan.n_programs // 8) + 8
+            if plan.launches == 1:      # little work: 32 lanes down the rows, then over the lanes
+                adds = -(-M // 32) + 32
+            else:                       # a thread's rows, a workgroup's threads, the workgroups in 32 lanes, the lanes
+                rows = max(1, 256 // plan.threads_per_row) if plan.threads_per_row else 1
+                adds = -(-M // max(1, plan.n_programs * rows)) + rows + -(-plan.n_programs // 32) + 32
             off = (adds + 3) * U32 * np.abs(dy * n).sum(0)
             if self.accumulate:
                 dw = dw + self.before
@@ -332,7 +335,7 @@ def test_norm_backward_sizes(M, K, dtype):
         b.check(what, b.run())
 
 
-@pytest.mark.parametrize("M,K,dtype", [(70001, 64, "bf16"), (9001, 300, "f16"), (9001, 1000, "bf16"), (5000, 2050, "f16"),
+@pytest.mark.parametrize("M,K,dtype", [(511, 1000, "bf16"), (512, 4096, "f16"), (513, 4096, "bf16"), (70001, 64, "bf16"), (9001, 300, "f16"), (9001, 1000, "bf16"), (5000, 2050, "f16"),
                                        (1200, 16384, "bf16"), (520, 40000, "f16")])
 def test_norm_backward_many_rows(M, K, dtype):
     require_gpu()
