@@ -546,19 +546,31 @@ __device__ __forceinline__ void gemm_body(const typename E::Args& a, int program
     auto next_slot = [](int slot, int slots) { return slot + 1 == slots ? 0 : slot + 1; };
     // Where the reduction is no multiple of 64, the last stage of an r-contiguous operand goes on into the next
     // rows: that is set to zero in LDS, once, when a tile's last stage has landed.
-    constexpr uint32_t IN_STAGE = E::I8 ? 128 : 64, IN_CHUNK = IN_STAGE / 8;       // elements
+    // Of 8-bit integers B's part alone is: a product with 0 is 0 whatever the other factor, which floats' infinities are not.
+    constexpr uint32_t IN_STAGE = E::I8 ? 128 : 64;     // elements
     const bool ragged = !(TA && TB) && (a.R & (IN_STAGE - 1)) != 0;
     auto clear_tail = [&](int slot_a, int slot_b) {
         const uint32_t from = static_cast<uint32_t>(a.R & (IN_STAGE - 1));
+        if constexpr (E::I8) {
+            for (int id = tid; id < C::TN * 8; id += C::NT) {
+                const uint32_t row = static_cast<uint32_t>(id) >> 3, c = static_cast<uint32_t>(id) & 7u;
+                if (c * 16 + 16 <= from) continue;
+                uint32_t* words = reinterpret_cast<uint32_t*>(ring_b + slot_b * C::B_BYTES + row * 128 + ((c ^ (row & 7u)) << 4));
+#pragma unroll
+                for (uint32_t w = 0; w < 4; ++w) {
+                    const uint32_t at = c * 16 + 4 * w;      // of the word's first byte
+                    const uint32_t kept = from <= at ? 0u : from >= at + 4 ? 4u : from - at;
+                    words[w] = kept == 0 ? 0u : kept == 4 ? words[w] : words[w] & ((1u << (8 * kept)) - 1u);
+                }
+            }
+        } else
         for (int row = tid; row < C::TM + C::TN; row += C::NT) {
             if ((TA && row < C::TM) || (TB && row >= C::TM)) continue;
             uint8_t* line = row < C::TM ? ring + slot_a * C::A_BYTES + row * 128 : ring_b + slot_b * C::B_BYTES + (row - C::TM) * 128;
-            for (uint32_t c = from / IN_CHUNK; c < 8; ++c) {
+            for (uint32_t c = from >> 3; c < 8; ++c) {
                 uint8_t* chunk = line + ((c ^ (static_cast<uint32_t>(row) & 7u)) << 4);   // TM is a multiple of 8
-                if (c * IN_CHUNK >= from) {
+                if (c * 8 >= from) {
                     *reinterpret_cast<u32x4*>(chunk) = u32x4{0u, 0u, 0u, 0u};
-                } else if constexpr (E::I8) {
-                    for (uint32_t e = from & 15u; e < 16; ++e) chunk[e] = 0;
                 } else {
                     for (uint32_t e = from & 7u; e < 8; ++e) reinterpret_cast<uint16_t*>(chunk)[e] = 0;
                 }
@@ -694,6 +706,7 @@ __device__ __forceinline__ void gemm_body(const typename E::Args& a, int program
                 for (int b = 0; b < BN / 2; ++b) {
                     float x[8];
                     widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
+                    if (E::I8 && col0 + 32 * b >= a.J) continue;        // an edge tile's other columns are not joined
                     *reinterpret_cast<f32x4*>(d + 32 * b) = f32x4{x[0], x[1], x[2], x[3]};
                     *reinterpret_cast<f32x4*>(d + 32 * b + 4) = f32x4{x[4], x[5], x[6], x[7]};
                     __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time

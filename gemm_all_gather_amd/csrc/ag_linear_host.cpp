@@ -35,9 +35,13 @@ struct Operand {
     int64_t ld, rows, cols;      // as stored
     int esize = 2;
     bool pack = false;
+    bool lines = false;          // the copy's rows start on whole 128-byte lines, else on 16 bytes
     uint64_t copy_offset = 0;
-    // whole vectors; of 8-bit integers whole 128-byte lines, a stage's part of a row
-    int64_t copy_ld() const { return esize == 1 ? (cols + 127) / 128 * 128 : (cols + 7) / 8 * 8; }
+    int64_t copy_ld() const
+    {
+        const int64_t unit = (lines ? 128 : 16) / esize;
+        return (cols + unit - 1) / unit * unit;
+    }
     uint64_t copy_bytes() const { return up256(static_cast<uint64_t>(rows) * copy_ld() * esize); }
 };
 
@@ -65,7 +69,7 @@ struct Kind {
 constexpr Kind kKinds[ag::kLinearTiles] = {{{1.42, 1.46, 1.48}, 6.0},     // 256 x 256
                                            {{0.53, 0.60, 0.75}, 4.0},     // 128 x 128
                                            {{1.02, 0.98, 1.00}, 5.0}};    // 256 x 128
-constexpr Kind kKindsI8[ag::kLinearTiles] = {{{1.45, 0, 0}, 6.0}, {{0.58, 0, 0}, 4.0}, {{0.93, 0, 0}, 5.0}};   // 128-wide steps
+constexpr Kind kKindsI8[ag::kLinearTiles] = {{{1.45, 0, 0}, 6.0}, {{0.57, 0, 0}, 4.0}, {{0.93, 0, 0}, 5.0}};   // 128-wide steps
 const Kind& kind_of(const Product& p, int tile) { return p.i8 ? kKindsI8[tile] : kKinds[tile]; }
 
 // Whole tiles of one kind; us is a tile's time.
@@ -121,6 +125,9 @@ ag_status_t choose(Product* p, int cus)
         for (int64_t keep = rounds; keep >= std::max<int64_t>(0, rounds - 1); --keep) {
             const int64_t tail = tiles - keep * cus;
             if (tail == 0) continue;
+            // a part after whole tiles has its loads on their way before it starts (1000 x 4100 x 4100 in 256 whole tiles of 128 x 128
+            // and 8 in seven parts 38.2 us, in 132 of 256 x 128 42.3; the 16-bit products' choice is as it was measured)
+            const double part_us = p->i8 && keep > 0 ? 2.0 : kind_of(*p, tile).fixed_us;
             for (int64_t s = 2; s <= std::min<int64_t>(32, p->stages / 2); ++s) {
                 const int64_t run = (p->stages + s - 1) / s, splits = (p->stages + run - 1) / run;
                 if (splits != s) continue;
@@ -128,7 +135,7 @@ ag_status_t choose(Product* p, int cus)
                 if (bytes > 512e6) break;
                 const double parts = static_cast<double>((tail * splits + cus - 1) / cus);
                 consider(keep * cus, splits, run,
-                         keep * tile_us + parts * (run * step_us + kind_of(*p, tile).fixed_us) + kJoinUs + 2 * bytes / kBytesPerUs);
+                         keep * tile_us + parts * (run * step_us + part_us) + kJoinUs + 2 * bytes / kBytesPerUs);
             }
         }
     }
@@ -373,8 +380,8 @@ ag_status_t plan_forward_i8(const ag_linear_i8_args_t* a, int cus, ForwardI8* f)
                (M <= ag::kLinearI8StreamRows && K <= 4096 && N * K <= (int64_t{1} << 24));
     if (!p.stream) {
         if ((s = choose(&p, cus)) != AG_OK) return s;
-        f->ox = Operand{f->x.at, f->x.ld, M, K, 1};
-        f->ow = Operand{f->w.at, f->w.ld, N, K, 1};
+        f->ox = Operand{f->x.at, f->x.ld, M, K, 1, false, true};
+        f->ow = Operand{f->w.at, f->w.ld, N, K, 1, false, true};
         place(&f->ox, &f->workspace);
         place(&f->ow, &f->workspace);
         f->partial_offset = f->workspace;
@@ -442,7 +449,8 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
         b->store_dz = (want_dx || (want_dw && !b->fold)) && (act || !aligned);
         b->slope = b->store_dz || b->fold || want_db;
     }
-    b->lddz = (N + 7) / 8 * 8;
+    // dz beside kept activations, and their copies, start their rows on whole 128-byte lines
+    b->lddz = b->fold ? (N + 63) / 64 * 64 : (N + 7) / 8 * 8;
     // about 1024 workgroups of 256 columns: enough for every CU, and few partial sums of a long column
     b->rows = std::max<int64_t>(8, std::min<int64_t>(256, (M * ((N + 255) / 256) / 1024 + 7) / 8 * 8));
     if (b->store_dz) {
@@ -490,7 +498,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
         if ((s = choose(&b->pw, cus)) != AG_OK) return s;
         b->ox = Operand{b->x.at, b->x.ld, M, K};
         if (b->fold) {      // the codes times the scales' powers of two, in 16 bits
-            b->ox.pack = true;
+            b->ox.pack = b->ox.lines = true;
             b->ox.copy_offset = used;
             used += b->ox.copy_bytes();
         } else {

@@ -1,6 +1,7 @@
 // The activation's gradient from activations that were kept in 8 bits.
 
 #include "ag_linear_device.h"
+#include "ag_raw.h"
 #include "ag_scale.h"
 
 namespace ag {
@@ -21,42 +22,64 @@ __global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Ar
     const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.N - col)));
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
-#pragma unroll 4
-        for (int i = rl; i < a.rows; i += 8) {
-            const int64_t row = row0 + i;
-            if (row >= a.M) break;
-            float v[8];
-            load_f32<BF16>(v, a.dy + row * a.lddy + col, n);
-            if (a.z) {
-                float z[8];
+        constexpr int DTYPE = BF16 ? AG_BF16 : AG_F16, AHEAD = 4;       // rows on their way
+        const int64_t end = min(row0 + a.rows, a.M);
+        const int at = static_cast<int>(col), N = static_cast<int>(a.N);
+        for (int64_t first = row0 + rl; first < end; first += 8 * AHEAD) {
+            Raw<DTYPE> dy[AHEAD], z16[AHEAD];
+            u32x2 z8[AHEAD];
+            float x_scale[AHEAD], z_scale[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {       // past the end: the last row again
+                const int64_t row = min(first + 8 * j, end - 1);
+                dy[j].template load<true>(a.dy + row * a.lddy, at, N);
                 if constexpr (Z8) {
-                    const float s = a.z_scale[row];
-                    load_codes(z, reinterpret_cast<const int8_t*>(a.z) + row * a.ldz + col, n);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] *= s;
-                } else {
-                    load_f32<BF16>(z, a.z + row * a.ldz + col, n);
+                    z_scale[j] = 0.f;
+                    z8[j] = u32x2{0u, 0u};
+                    if (a.z) {
+                        z_scale[j] = a.z_scale[row];
+                        z8[j] = load_codes(reinterpret_cast<const int8_t*>(a.z) + row * a.ldz + col, n);
+                    }
+                } else if (a.z) {
+                    z16[j].template load<true>(a.z + row * a.ldz, at, N);
                 }
-                apply_slope(v, z, a.act);
+                if constexpr (X8) x_scale[j] = a.x_scale[row];
             }
-            if (a.dz) store_16<BF16>(a.dz + row * a.lddz + col, v, n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += v[e];
-            if constexpr (X8) {
-                float power, rest;
-                split_scale<BF16>(a.x_scale[row], &power, &rest);
+            for (int j = 0; j < AHEAD; ++j) {
+                const int64_t row = first + 8 * j;
+                if (row >= end) break;
+                float v[8], z[8];
+                dy[j].get(v);
+                if (a.z) {
+                    if constexpr (Z8) {
+                        code_values(z, z8[j]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= rest;
-                store_16<BF16>(a.dz_fold + row * a.lddz + col, v, n);
-            }
-            if constexpr (REST) {
-                float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float kept = to_f32<BF16>(from_f32<BF16>(v[e]));
-                    rest[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
+                        for (int e = 0; e < 8; ++e) z[e] *= z_scale[j];
+                    } else {
+                        z16[j].get(z);
+                    }
+                    apply_slope(v, z, a.act);
                 }
-                store_16<BF16>(a.dz_rest + row * a.lddz + col, rest, n);
+                if (a.dz) store_16<BF16>(a.dz + row * a.lddz + col, v, n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += v[e];
+                if constexpr (X8) {
+                    float power, rest;
+                    split_scale<BF16>(x_scale[j], &power, &rest);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= rest;
+                    store_16<BF16>(a.dz_fold + row * a.lddz + col, v, n);
+                }
+                if constexpr (REST) {
+                    float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float kept = to_f32<BF16>(from_f32<BF16>(v[e]));
+                        rest[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
+                    }
+                    store_16<BF16>(a.dz_rest + row * a.lddz + col, rest, n);
+                }
             }
         }
     }

@@ -73,15 +73,13 @@ __device__ __forceinline__ void code_values(float (&v)[8], u32x2 codes)
     }
 }
 
-// n <= 8 codes as numbers, the others 0.
-__device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, int n)
+// n <= 8 codes, the others 0.
+__device__ __forceinline__ u32x2 load_codes(const int8_t* p, int n)
 {
-    if (n >= 8) {
-        code_values(v, reinterpret_cast<const Any8*>(p)->v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < n ? static_cast<float>(p[e]) : 0.f;
-    }
+    if (n >= 8) return reinterpret_cast<const Any8*>(p)->v;
+    uint64_t w = 0;
+    for (int e = n - 1; e >= 0; --e) w = w << 8 | static_cast<uint8_t>(p[e]);
+    return u32x2{static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32)};
 }
 
 }  // namespace
