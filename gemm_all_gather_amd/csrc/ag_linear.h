@@ -129,7 +129,9 @@ struct LinearSlopeQ8Args : LinearSlopeArgs {
     const float* z_scale;
     uint16_t* dz_fold;
 };
-hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, int bf16, hipStream_t stream);
+// x: the codes to 16-bit numbers in the same launch (M 0: none).
+struct DequantizeArgs;
+hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, const DequantizeArgs& x, int bf16, hipStream_t stream);
 hipError_t launch_linear_bias_grad(const LinearBiasGradArgs& a, hipStream_t stream);
 
 using LinearInTurnFn = void (*)(LinearGemmArgs, LinearGemmArgs, LinearBiasGradArgs);

@@ -543,7 +543,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
     b->workspace = used + std::max({b->px.partial_bytes, b->pw.partial_bytes, b->rest.partial_bytes});
     b->db_alone = want_db && !b->px.on && !b->pw.on;
     b->launches = (b->slope ? 1 : 0) + (b->together || b->in_turn ? 1 : (b->db_alone ? 1 : 0) + b->px.launches() + b->pw.launches()) +
-                  b->rest.launches() + (b->ow.pack ? 1 : 0) + (b->ox.pack ? 1 : 0);
+                  b->rest.launches() + (b->ow.pack ? 1 : 0) + (b->ox.pack && !b->fold ? 1 : 0);
     return AG_OK;
 }
 
@@ -762,7 +762,13 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         a.dz_fold = b.fold ? dz_fold : nullptr;
         a.x_scale = b.fold ? x_scale : nullptr;
         a.z_scale = a.z ? z_scale : nullptr;
-        const hipError_t e = a.x_scale || a.z_scale ? ag::launch_linear_slope_q8(a, bf16, stream) : ag::launch_linear_slope(a, bf16, stream);
+        ag::DequantizeArgs codes{};
+        if (b.fold) {
+            codes = ag::DequantizeArgs{static_cast<const int8_t*>(args->x), x_scale, ws + b.ox.copy_offset, b.x.ld, b.ox.copy_ld(),
+                                       args->M, static_cast<int32_t>(args->K), 1};
+        }
+        const hipError_t e = a.x_scale || a.z_scale ? ag::launch_linear_slope_q8(a, codes, bf16, stream)
+                                                    : ag::launch_linear_slope(a, bf16, stream);
         if (e != hipSuccess) return fail_hip(e, "linear slope");
         if (b.store_dz) {
             dz = a.dz;
@@ -791,13 +797,9 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
     if (b.pw.on) {
         const uint16_t* X;
         int64_t ldx;
-        if (b.fold) {
+        if (b.fold) {       // made beside dz
             X = reinterpret_cast<const uint16_t*>(ws + b.ox.copy_offset);
             ldx = b.ox.copy_ld();
-            const ag::DequantizeArgs a{static_cast<const int8_t*>(args->x), x_scale, ws + b.ox.copy_offset, b.x.ld, ldx, args->M,
-                                       static_cast<int32_t>(args->K), 1};
-            const hipError_t e = ag::launch_dequantize(a, args->dtype, stream);
-            if (e != hipSuccess) return fail_hip(e, "linear operand of codes");
         } else if ((s = pack(b.ox, workspace, stream, &X, &ldx)) != AG_OK) {
             return s;
         }

@@ -1,5 +1,6 @@
 // The activation's gradient from activations that were kept in 8 bits.
 
+#include "ag_dequantize.h"
 #include "ag_linear_device.h"
 #include "ag_raw.h"
 #include "ag_scale.h"
@@ -11,12 +12,12 @@ namespace {
 // (x's codes times the scale's power of two are exact in 16 bits), with what that rounding leaves; and the column sums
 // of the unrounded dz over a.rows rows.  Threads and sums as in the kernel without codes.
 template <bool BF16, bool REST, bool X8, bool Z8>
-__global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a)
+__device__ __forceinline__ void slope_body(const LinearSlopeQ8Args& a, uint32_t program)
 {
     __shared__ float part[8][264];
     const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const uint32_t col_blocks = static_cast<uint32_t>((a.N + 255) / 256);
-    const int64_t bx = blockIdx.x % col_blocks, by = blockIdx.x / col_blocks;
+    const int64_t bx = program % col_blocks, by = program / col_blocks;
     const int64_t col = (bx * 32 + c) * 8;
     const int64_t row0 = by * a.rows;
     const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.N - col)));
@@ -97,7 +98,15 @@ __global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Ar
     }
 }
 
-using SlopeFn = void (*)(LinearSlopeQ8Args);
+// dz, and beside it x's codes as 16-bit numbers for the product that follows (x.M 0: none): two passes over memory in one launch.
+template <bool BF16, bool REST, bool X8, bool Z8>
+__global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a, DequantizeArgs x, uint32_t slope_programs)
+{
+    if (blockIdx.x < slope_programs) slope_body<BF16, REST, X8, Z8>(a, blockIdx.x);
+    else if constexpr (X8) dequantize_body<(BF16 ? AG_BF16 : AG_F16)>(x, blockIdx.x - slope_programs, gridDim.x - slope_programs);
+}
+
+using SlopeFn = void (*)(LinearSlopeQ8Args, DequantizeArgs, uint32_t);
 template <bool BF16, bool REST> SlopeFn pick(bool x8, bool z8)
 {
     return x8 ? (z8 ? ag_linear_slope_q8_kernel<BF16, REST, true, true> : ag_linear_slope_q8_kernel<BF16, REST, true, false>)
@@ -106,14 +115,15 @@ template <bool BF16, bool REST> SlopeFn pick(bool x8, bool z8)
 
 }  // namespace
 
-hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, int bf16, hipStream_t stream)
+hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, const DequantizeArgs& x, int bf16, hipStream_t stream)
 {
     const int64_t groups = a.rows < 1 ? 0 : (a.N + 255) / 256 * ((a.M + a.rows - 1) / a.rows);
-    if (groups < 1 || groups > 0x7fffffff || (!a.x_scale && !a.z_scale) || (a.x_scale && !a.dz_fold)) return hipErrorInvalidValue;
     const bool x8 = a.x_scale != nullptr, z8 = a.z_scale != nullptr;
+    const int64_t copies = x8 && x.M > 0 && x.K > 0 ? dequantize_programs(x) : 0;
+    if (groups < 1 || groups + copies >= (int64_t{1} << 24) || (!x8 && !z8) || (x8 && !a.dz_fold)) return hipErrorInvalidValue;
     const SlopeFn fn = a.dz_rest ? (bf16 ? pick<true, true>(x8, z8) : pick<false, true>(x8, z8))
-                        : (bf16 ? pick<true, false>(x8, z8) : pick<false, false>(x8, z8));
-    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, stream, a);
+                                 : (bf16 ? pick<true, false>(x8, z8) : pick<false, false>(x8, z8));
+    hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(groups + copies)), dim3(256), 0, stream, a, x, static_cast<uint32_t>(groups));
     return hipGetLastError();
 }
 

@@ -7,6 +7,9 @@
 
 namespace ag {
 
+// A grid's workgroups: with up to 1024 threads each, a launch's threads stay below 2^32.
+constexpr int64_t kMaxRowsPrograms = (int64_t{1} << 22) - 1;
+
 // One pass over rows: h = x + residual, its norm, and the row in 16 or 8 bits; without `norm` the row itself in 8 bits.
 struct RowsArgs {
     const void* x;
@@ -33,9 +36,6 @@ struct RowsShape {
 RowsShape rows_shape(int64_t K, bool norm);
 RowsShape norm_backward_shape(int64_t K);       // vectors 0: in two passes, launch_norm_backward_long
 
-// A grid's workgroups: with up to 1024 threads each, a launch's threads stay below 2^32.
-constexpr int64_t kMaxRowsPrograms = (int64_t{1} << 22) - 1;
-
 // norm with dtype AG_F16 or AG_BF16; without it AG_F32 too.
 hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hipStream_t stream);
 
@@ -49,6 +49,12 @@ struct DequantizeArgs {
     int32_t K;
     int32_t by_power;
 };
+constexpr int kDequantizeVectors = 4;
+inline int64_t dequantize_programs(const DequantizeArgs& a)      // workgroups of 256 threads
+{
+    const int64_t vectors = a.M * ((a.K + 7) / 8), per = 256 * kDequantizeVectors, groups = (vectors + per - 1) / per;
+    return groups < kMaxRowsPrograms ? groups : kMaxRowsPrograms;
+}
 hipError_t launch_dequantize(const DequantizeArgs& a, int dtype, hipStream_t stream);
 
 struct NormBackwardArgs {

@@ -62,7 +62,7 @@ def test_plans():
     both = ag.plan_linear_backward_q8(**BACKWARD)
     M, N, K = 1000, 3584, 8192
     assert both.bytes_read == 2 * M * N + M * N + 4 * M + M * K + 4 * M + 2 * N * K and both.flops == 4.0 * M * N * K
-    assert both.bytes_written == plain.bytes_written and both.launches > plain.launches
+    assert both.bytes_written == plain.bytes_written and both.launches == plain.launches
     # dz for dx, dz with the scale's factor for dw, x's codes in 16 bits
     assert both.workspace_bytes >= 2 * (2 * M * N + M * K)
     z_only = ag.plan_linear_backward_q8(**dict(BACKWARD, x_scale=None))
