@@ -25,26 +25,47 @@ __device__ __forceinline__ float nearest_code(float v, float per, float top, boo
     return q;
 }
 
-__device__ __forceinline__ void store_codes(int8_t* p, const float (&v)[8], uint32_t top_bits, int n)
-{
-    const float top = __uint_as_float(top_bits);
-    uint32_t lo = 0, hi = 0;
-    if (top_bits != 0 && top_bits < 0x7f800000u) {      // a row of zeros, or one that is not finite, has codes of zero
-        const float per = 127.f / top;
-        const bool wide = top < 1e-30f;                 // 127 / top may not be finite
-        uint32_t c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = static_cast<uint32_t>(static_cast<int>(nearest_code(v[e], per, top, wide))) & 255u;
-        lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-        hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+// What a row's codes are made with: 127 over its largest magnitude.
+struct Unit {
+    float top, per;
+    bool none, wide;        // no codes but 0; 127 / top may not be finite
+    __device__ __forceinline__ explicit Unit(uint32_t top_bits)
+    {
+        top = __uint_as_float(top_bits);
+        none = top_bits == 0 || top_bits >= 0x7f800000u;        // a row of zeros, or one that is not finite
+        per = none ? 0.f : 127.f / top;
+        wide = top < 1e-30f;
     }
+    __device__ __forceinline__ uint32_t code(float v) const      // in 8 bits
+    {
+        return none ? 0u : static_cast<uint32_t>(static_cast<int>(nearest_code(v, per, top, wide))) & 255u;
+    }
+};
+
+__device__ __forceinline__ void store_codes(int8_t* p, const float (&v)[8], const Unit& unit, int n)
+{
+    uint32_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = unit.code(v[e]);
     if (n >= 8) {
-        reinterpret_cast<Any8*>(p)->v = u32x2{lo, hi};
+        reinterpret_cast<Any8*>(p)->v = u32x2{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < n) p[e] = static_cast<int8_t>((e < 4 ? lo >> (8 * e) : hi >> (8 * (e - 4))) & 255u);
+            if (e < n) p[e] = static_cast<int8_t>(c[e]);
     }
+}
+
+// One element, for the up to seven behind a row's last whole vector.
+template <int DTYPE> __device__ __forceinline__ float element(const void* row, int col)
+{
+    if constexpr (DTYPE == AG_F32) return static_cast<const float*>(row)[col];
+    else return to_f32<DTYPE == AG_BF16>(static_cast<const uint16_t*>(row)[col]);
+}
+template <int DTYPE> __device__ __forceinline__ void put_element(void* p, int64_t at, float v)
+{
+    if constexpr (DTYPE == AG_F32) static_cast<float*>(p)[at] = v;
+    else static_cast<uint16_t*>(p)[at] = from_f32<DTYPE == AG_BF16>(v);
 }
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }   // NaN above infinity
@@ -165,21 +186,30 @@ __global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
     __shared__ uint32_t lds_top[2][16];
     const int lane = threadIdx.x % G;
     const bool weighted = NORM && a.weight != nullptr, add = NORM && a.residual != nullptr;
+    // TAIL: the K % 8 elements behind the last whole vector go to as many lanes, one each
+    const int whole = TAIL ? a.K & ~7 : a.K, tail = whole + lane;
+    const bool extra = TAIL && tail < a.K;
     int turn = 0;
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.M; first += static_cast<int64_t>(gridDim.x) * ROWS) {
         const int64_t mine = first + (ROWS > 1 ? threadIdx.x / G : 0), row = min(mine, a.M - 1);
         const bool live = mine < a.M;
         const void *xs = row_of<DTYPE>(a.x, row, a.ldx), *rs = row_of<DTYPE>(a.residual, row, a.ldr);
         Raw<DTYPE> x[V], r[V], weight[V];
+        float one = 0.f, one_r = 0.f, one_w = 1.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
-            x[j].template load<TAIL>(xs, col, a.K);
-            if (add) r[j].template load<TAIL>(rs, col, a.K);
+            x[j].template load<false>(xs, col, whole);
+            if (add) r[j].template load<false>(rs, col, whole);
+        }
+        if (extra) {
+            one = element<DTYPE>(xs, tail);
+            if (add) one_r = element<DTYPE>(rs, tail);
+            if (weighted) one_w = element<DTYPE>(a.weight, tail);
         }
         if (weighted) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) weight[j].template load<TAIL>(a.weight, (lane + j * G) * 8, a.K);
+            for (int j = 0; j < V; ++j) weight[j].template load<false>(a.weight, (lane + j * G) * 8, whole);
         }
         double sum = 0;
         uint32_t top = 0;
@@ -190,7 +220,7 @@ __global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
             float (&v)[8] = kept[NORM ? j : 0];
             if constexpr (NORM) {
                 if (add) add_residual<DTYPE>(x[j], r[j]);
-                if (a.h && live) x[j].store(a.h, row * a.ldh + col, a.K - col);
+                if (a.h && live && col < whole) x[j].store(a.h, row * a.ldh + col, 8);
             }
             x[j].get(v);
             if constexpr (NORM) {
@@ -206,6 +236,15 @@ __global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
         }
+        if constexpr (TAIL) {
+            if constexpr (NORM) {
+                if (add) one = to_f32<DTYPE == AG_BF16>(from_f32<DTYPE == AG_BF16>(one + one_r));
+                if (a.h && live && extra) put_element<DTYPE>(a.h, row * a.ldh + tail, one);
+                sum = fma(static_cast<double>(one), static_cast<double>(one), sum);
+                one *= one_w;
+            }
+            top = max(top, magnitude(one));
+        }
         reduce_row<NORM, G>(sum, top, lds_sum, lds_top, turn);
         turn ^= 1;
         float rstd = 1.f;
@@ -215,17 +254,23 @@ __global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
             if (a.scale) a.scale[row] = scale_of(top, rstd);
             if (a.rstd) a.rstd[row] = rstd;
         }
+        const Unit unit(top);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int col = (lane + j * G) * 8, n = a.K - col;
+            const int col = (lane + j * G) * 8;
+            if (col >= whole) continue;
             float (&v)[8] = kept[NORM ? j : 0];
             if constexpr (!NORM) x[j].get(v);
-            if (a.q) store_codes(a.q + row * a.ldq + col, v, top, n);
+            if (a.q) store_codes(a.q + row * a.ldq + col, v, unit, 8);
             if (NORM && a.y) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= rstd;
-                store_row<DTYPE>(a.y, row * a.ldy + col, v, n);
+                store_row<DTYPE>(a.y, row * a.ldy + col, v, 8);
             }
+        }
+        if (extra) {
+            if (a.q) a.q[row * a.ldq + tail] = static_cast<int8_t>(unit.code(one));
+            if (NORM && a.y) put_element<DTYPE>(a.y, row * a.ldy + tail, one * rstd);
         }
     }
 }
@@ -296,6 +341,7 @@ __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
             if (a.rstd) a.rstd[row] = rstd;
         }
         if (!a.q && !a.y) continue;
+        const Unit unit(top);
         for (int col = threadIdx.x * 8; col < a.K; col += kLongThreads * 16) {
             Raw<DTYPE> x[2], w[2];
             load(x, w, col, true);
@@ -305,7 +351,7 @@ __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
                 float v[8];
                 x[j].get(v);
                 weigh(v, w[j]);
-                if (a.q) store_codes(a.q + row * a.ldq + at, v, top, n);
+                if (a.q) store_codes(a.q + row * a.ldq + at, v, unit, n);
                 if (NORM && a.y) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= rstd;
@@ -363,14 +409,18 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
     __shared__ float lds[2][16];
     __shared__ float join[ROWS > 1 ? ROWS * G * 8 : 1];
     const int lane = threadIdx.x % G;
+    // TAIL: the K % 8 elements behind the last whole vector go to as many lanes, one each
+    const int whole = TAIL ? a.K & ~7 : a.K, tail = whole + lane;
+    const bool extra = TAIL && tail < a.K;
     Raw<DTYPE> weight[V], dy[V], h[V], dh[V];
-    float dw[V][8];
+    float dw[V][8], one_w = 1.f, one_dw = 0.f;
+    if (extra && a.weight) one_w = element<DTYPE>(a.weight, tail);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int col = (lane + j * G) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
-        if (a.weight) weight[j].template load<TAIL>(a.weight, col, a.K);
+        if (a.weight) weight[j].template load<false>(a.weight, col, whole);
         else weight[j].ones();
     }
     const bool add = a.dh != nullptr && a.dx != nullptr;
@@ -384,12 +434,18 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
-            dy[j].template load<TAIL>(ds, col, a.K);
-            h[j].template load<TAIL>(hs, col, a.K);
+            dy[j].template load<false>(ds, col, whole);
+            h[j].template load<false>(hs, col, whole);
         }
         if (add) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) dh[j].template load<TAIL>(es, (lane + j * G) * 8, a.K);
+            for (int j = 0; j < V; ++j) dh[j].template load<false>(es, (lane + j * G) * 8, whole);
+        }
+        float one_g = 0.f, one_n = 0.f, one_dh = 0.f;
+        if (extra) {
+            one_g = element<DTYPE>(ds, tail);
+            one_n = element<DTYPE>(hs, tail);
+            if (add) one_dh = element<DTYPE>(es, tail);
         }
         float s = 0.f;
 #pragma unroll
@@ -405,6 +461,12 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
                 s += t * w[e];
             }
         }
+        if constexpr (TAIL) {
+            one_n *= rstd;
+            const float t = one_g * one_n;
+            one_dw += live ? t : 0.f;
+            s += t * one_w;
+        }
         if (!a.dx) continue;
         const float c = sum_row<G>(s, lds, turn) * per_k;
         turn ^= 1;
@@ -412,6 +474,7 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int col = (lane + j * G) * 8;
+            if (col >= whole) continue;
             float g[8], n[8], w[8], d[8] = {};
             dy[j].get(g);
             h[j].get(n);
@@ -419,8 +482,9 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
             if (add) dh[j].get(d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] * w[e] - n[e] * rstd * c) + d[e];
-            store_16<BF16>(a.dx + row * a.lddx + col, g, a.K - col);
+            store_16<BF16>(a.dx + row * a.lddx + col, g, 8);
         }
+        if (extra) put_element<DTYPE>(a.dx, row * a.lddx + tail, rstd * (one_g * one_w - one_n * c) + one_dh);
     }
     if (!a.sums) return;
     float* out = a.sums + static_cast<int64_t>(program) * a.ldsums;
@@ -436,14 +500,29 @@ __device__ __forceinline__ void backward_rows(const NormBackwardArgs& a, int pro
                 float t = 0.f;
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) t += join[r * (G * 8) + c];
-                if (col < a.K) out[col] = t;
+                if (col < whole) out[col] = t;
             }
         } else {
             const int col = (lane + j * G) * 8;     // the rows of sums are whole vectors
-            if (col < a.K) {
+            if (col < whole) {
                 *reinterpret_cast<f32x4*>(out + col) = f32x4{dw[j][0], dw[j][1], dw[j][2], dw[j][3]};
                 *reinterpret_cast<f32x4*>(out + col + 4) = f32x4{dw[j][4], dw[j][5], dw[j][6], dw[j][7]};
             }
+        }
+    }
+    if constexpr (TAIL) {
+        if constexpr (ROWS > 1) {
+            __syncthreads();
+            join[threadIdx.x] = one_dw;
+            __syncthreads();
+            if (threadIdx.x < static_cast<unsigned>(a.K - whole)) {
+                float t = 0.f;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) t += join[r * G + threadIdx.x];
+                out[whole + threadIdx.x] = t;
+            }
+        } else if (extra) {
+            out[tail] = one_dw;
         }
     }
 }
