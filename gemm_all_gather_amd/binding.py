@@ -578,6 +578,13 @@ _I8 = Struct("<8Q8q8i")
 _BACKWARD = Struct("<7Q9q8i")
 
 
+def _checked_workspace(workspace):
+    """Address and bytes of a workspace on the current device, or of none."""
+    if workspace is None:
+        return 0, 0
+    return _addresses((workspace, None, "workspace"))[0], workspace.numel() * workspace.element_size()
+
+
 def quantize_rows(x, q, scale, M, K, dtype, ldx=0, ldq=0, stream=None) -> None:
     """Each row of x as int8 codes and one fp32 scale (ag_quantize_rows)."""
     d = _dtype(dtype)
@@ -636,7 +643,7 @@ def rms_norm_backward(dy, h, rstd, M, K, dtype, weight=None, dh=None, dx=None, d
                       dw_dtype=None, accumulate=False, workspace=None, stream=None) -> None:
     """The norm's gradients dx (with dh, what reaches h otherwise) and dw, those that are given (ag_rms_norm_backward)."""
     a = _norm_backward_args(dy, h, rstd, M, K, dtype, weight, dh, dx, dw, lddy, ldh, lddh, lddx, dw_dtype, accumulate)
-    ws, nbytes = _workspace(workspace)
+    ws, nbytes = _checked_workspace(workspace)
     _check(lib().ag_rms_norm_backward(a, ws, nbytes, _stream(stream)), "ag_rms_norm_backward")
 
 
@@ -660,7 +667,7 @@ def linear_i8(x, w, x_scale, w_scale, y, M, N, K, dtype, act="none", bias=None, 
               ldz=0, workspace=None, stream=None) -> None:
     """y = act(x_scale w_scale (x w^T) + bias) + residual of int8 codes x and w (ag_linear_i8)."""
     a = _i8_args(M, N, K, dtype, act, x, w, x_scale, w_scale, y, bias, residual, z, ldx, ldw, ldr, ldy, ldz)
-    ws, nbytes = _workspace(workspace)
+    ws, nbytes = _checked_workspace(workspace)
     _check(lib().ag_linear_i8(a, ws, nbytes, _stream(stream)), "ag_linear_i8")
 
 
@@ -690,7 +697,7 @@ def linear_backward_q8(dy, x, w, M, N, K, dtype, x_scale=None, act="none", z=Non
     (ag_linear_backward_q8)."""
     a, xs, zs = _backward_q8_args(M, N, K, dtype, act, dy, x, w, x_scale, z, z_scale, dx, dw, db, lddy, ldx, ldw, ldz, lddx, lddw,
                                   dw_dtype, accumulate)
-    ws, nbytes = _workspace(workspace)
+    ws, nbytes = _checked_workspace(workspace)
     _check(lib().ag_linear_backward_q8(a, xs, zs, ws, nbytes, _stream(stream)), "ag_linear_backward_q8")
 
 

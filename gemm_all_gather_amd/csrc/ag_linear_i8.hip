@@ -174,11 +174,12 @@ __global__ __launch_bounds__(256) void ag_linear_i8_pack_kernel(LinearI8Pack fir
 {
     const bool one = blockIdx.x < first_groups;
     const LinearI8Pack& p = one ? first : second;
-    const int64_t per_row = (p.cols + 15) / 16;
-    const int64_t id = static_cast<int64_t>(one ? blockIdx.x : blockIdx.x - first_groups) * 256 + threadIdx.x;
-    const int64_t row = id >> 32 ? id / per_row : static_cast<uint32_t>(id) / static_cast<uint32_t>(per_row), col = (id - row * per_row) * 16;
-    if (row >= p.rows) return;
-    *reinterpret_cast<i32x4*>(p.dst + row * p.ld_dst + col) = load16(p.src + row * p.ld_src + col, p.cols - col);
+    const uint32_t program = one ? blockIdx.x : blockIdx.x - first_groups, programs = one ? first_groups : gridDim.x - first_groups;
+    const int64_t per_row = (p.cols + 15) / 16, all = p.rows * per_row;
+    for (int64_t id = static_cast<int64_t>(program) * 256 + threadIdx.x; id < all; id += static_cast<int64_t>(programs) * 256) {
+        const int64_t row = id >> 32 ? id / per_row : static_cast<uint32_t>(id) / static_cast<uint32_t>(per_row), col = (id - row * per_row) * 16;
+        *reinterpret_cast<i32x4*>(p.dst + row * p.ld_dst + col) = load16(p.src + row * p.ld_src + col, p.cols - col);
+    }
 }
 
 using StreamFn = void (*)(LinearI8StreamArgs);
@@ -232,9 +233,9 @@ hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cu
 
 hipError_t launch_linear_i8_pack(const LinearI8Pack& first, const LinearI8Pack& second, hipStream_t stream)
 {
-    auto groups = [](const LinearI8Pack& p) { return (p.rows * ((p.cols + 15) / 16) + 255) / 256; };
+    auto groups = [](const LinearI8Pack& p) { return min((p.rows * ((p.cols + 15) / 16) + 255) / 256, int64_t{1} << 22); };
     const int64_t one = groups(first), all = one + groups(second);
-    if (all < 1 || all >= (int64_t{1} << 24)) return hipErrorInvalidValue;
+    if (all < 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL(ag_linear_i8_pack_kernel, dim3(static_cast<uint32_t>(all)), dim3(256), 0, stream, first, second, static_cast<uint32_t>(one));
     return hipGetLastError();
 }

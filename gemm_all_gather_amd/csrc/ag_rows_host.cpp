@@ -59,6 +59,8 @@ ag_status_t plan_codes(const void* x, int64_t ldx, const int8_t* q, int64_t ldq,
 
 // ------------------------------------------------------------------ the norm
 
+constexpr double kLeastEps = 1e-60;      // a row of zeros has the finite rstd 1e30 then
+
 struct Norm {
     Mat x, residual, weight, h, y, q, scale, rstd;
     RowsShape shape{};
@@ -72,7 +74,8 @@ ag_status_t plan_norm(const ag_rms_norm_args_t* a, int cus, Norm* n)
         if (r != 0) return fail(AG_ERR_INVALID_ARG, "a reserved field is not 0");
     ag_status_t s = check_rows(a->M, a->K, a->dtype, false);
     if (s != AG_OK) return s;
-    if (!(a->eps > 0) || !std::isfinite(a->eps)) return fail(AG_ERR_INVALID_ARG, "eps %g is not positive and finite", a->eps);
+    if (!(a->eps >= kLeastEps) || !std::isfinite(a->eps))
+        return fail(AG_ERR_INVALID_ARG, "eps %g is not finite and %g or more", a->eps, kLeastEps);
     const int64_t M = a->M, K = a->K;
     n->x = Mat{"x", addr(a->x), M, K, a->ldx ? a->ldx : K, 2};
     n->residual = Mat{"residual", addr(a->residual), M, K, a->ldr ? a->ldr : K, 2};

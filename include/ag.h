@@ -2,8 +2,9 @@
  * ag.h -- C ABI of libag: a symmetric heap of logical ranks on one MI355X
  * (gfx950), a persistent tiled multi-destination all-gather, a tiled GEMM
  * whose epilogue performs the same multi-destination store, and what a rank
- * trains with between collectives: a linear layer with its epilogue, its
- * gradients, and an AdamW step over many tensors.
+ * works with between collectives: a linear layer with its epilogue, its
+ * gradients, the root-mean-square norm, rows in 8 bits with the products and
+ * gradients that read them, and an AdamW step over many tensors.
  *
  * Sources (the three pages on the iris all-gather):
  *  - ROCm/iris #626, "Summary": the device-side all-gather loads the local
@@ -629,11 +630,12 @@ ag_status_t ag_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale,
  * weight     device, K of dtype, or NULL (ones)
  * q, scale   device, M x K int8 and M floats, or both NULL
  * rstd       device, M floats, or NULL (ag_rms_norm_backward reads it)
- * eps        > 0, finite
- * Squares are summed in fp64 and products h weight kept exact (fp32), so that
- * no size of h overflows; the codes are those of exact arithmetic, wherever
- * the products lie within fp32's normal numbers.  A row with a product past
- * fp32's largest has the scale NaN, as one with a NaN or an infinity.
+ * eps        finite, 1e-60 or more
+ * Squares are summed in fp64: no size of h leaves their range.  Products h
+ * weight are exact in fp32 wherever they lie within its normal numbers, and
+ * the codes are those of exact arithmetic there.  A product past fp32's
+ * largest is an infinity: in y, and its row's scale is NaN with codes 0, as
+ * one with a NaN or an infinity.
  * Sizes, strides and overlaps as above.  One launch.
  * ------------------------------------------------------------------------ */
 typedef struct ag_rms_norm_args {
@@ -738,7 +740,9 @@ ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_l
  * that the codes stand for.  A row's x_scale goes into its dz before dz's
  * rounding to dtype, but for its power of two, which goes to the codes and
  * leaves them exact: dw carries one rounding of dz, as without codes, and
- * needs no rounded copy of x.  A dw in AG_F32 takes dz in two terms of dtype.
+ * needs no rounded copy of x.  The other factor lies in [1/2, 1) (1 and more
+ * in AG_F16 for rows that hold 32512 or more), so that a dz that has a place
+ * in dtype keeps one.  A dw in AG_F32 takes dz in two terms of dtype.
  * Either scale may be NULL. */
 ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);

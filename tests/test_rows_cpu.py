@@ -2,6 +2,11 @@
 the pins of their oracle."""
 
 import ctypes
+import os
+import re
+import shutil
+import subprocess
+from concurrent.futures import ThreadPoolExecutor
 from fractions import Fraction
 
 import numpy as np
@@ -25,7 +30,7 @@ VALUES = dict(q=A, scale=A + GIB, y=A + 2 * GIB, M=100, K=4096, dtype="f32")
     (dict(rstd=A + 7 * GIB + 1), INVALID), (dict(q=None), INVALID), (dict(scale=None), INVALID),
     (dict(M=-1), INVALID), (dict(K=-1), INVALID), (dict(M=1 << 31), UNSUPPORTED), (dict(K=(1 << 20) + 1), UNSUPPORTED),
     (dict(dtype="f32"), UNSUPPORTED), (dict(dtype=9), INVALID),
-    (dict(eps=0.0), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(eps=0.0), INVALID), (dict(eps=9e-61), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(ldx=8191), INVALID), (dict(ldr=1), INVALID), (dict(ldh=-1), INVALID), (dict(ldy=8000), INVALID), (dict(ldq=8191), INVALID),
     (dict(ldq=(1 << 20) + 1), UNSUPPORTED),
     (dict(y=A), INVALID), (dict(y=A + 2 * GIB), INVALID), (dict(q=A + 64), INVALID), (dict(scale=A + GIB), INVALID),
@@ -37,7 +42,7 @@ def test_plan_norm_rejects(over, status):
 
 
 @pytest.mark.parametrize("over", [
-    dict(), dict(h=A), dict(h=A + 2 * GIB), dict(h=A + 2 * GIB, ldh=9000, ldr=9000), dict(q=None, scale=None), dict(y=None),
+    dict(), dict(eps=1e-60), dict(h=A), dict(h=A + 2 * GIB), dict(h=A + 2 * GIB, ldh=9000, ldr=9000), dict(q=None, scale=None), dict(y=None),
     dict(weight=None, residual=None, h=None), dict(y=None, q=None, scale=None, h=None), dict(M=0, x=None, y=None),
     dict(K=0, x=None, q=None), dict(M=1, ldx=1 << 40), dict(x=A + 2, ldx=8193, q=A + 5 * GIB + 1, ldq=8193),
 ])
@@ -126,6 +131,11 @@ def test_tensors_are_checked(name, fn, args):
         fn(**dict(args, **{name: torch.zeros(4, dtype=right)}))
 
 
+def test_workspaces_are_checked():
+    with pytest.raises(ValueError, match="workspace"):
+        ag.rms_norm_backward(**{k: v for k, v in BACKWARD.items() if k != "num_cus"}, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
 def test_plans():
     p = ag.plan_rms_norm(**NORM)
     assert (p.threads_per_row * p.vectors_per_thread * 8 >= 8192 and p.launches == 1 and p.workspace_bytes == 0 and
@@ -184,3 +194,24 @@ def test_codes_product_oracle():
     x, w = np.array([[1, -2], [127, 127]], dtype=np.int8), np.array([[3, 4], [-128, 127]], dtype=np.int8)
     got = codes_product_oracle(x, w, np.array([1.0, 0.5], np.float32), np.array([2.0, 1.0], np.float32))
     assert got.tolist() == [[-10.0, -382.0], [889.0, -63.5]]
+
+
+# ------------------------------------------------------------------ generated code
+
+def test_row_kernels_never_spill(tmp_path):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "gemm_all_gather_amd", "csrc")
+
+    def kernels(name):
+        out = str(tmp_path / (name + ".s"))
+        subprocess.run([hipcc, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
+                        "-packed-fp32-ops", f"-I{csrc}", f"-I{os.path.join(root, 'include')}", "--cuda-device-only",
+                        "-S", "-o", out, os.path.join(csrc, name + ".hip")], check=True, capture_output=True)
+        return re.findall(r"\.amdhsa_kernel (\S+)\n.*?private_segment_fixed_size (\d+)", open(out).read(), re.S)
+
+    with ThreadPoolExecutor(3) as pool:
+        found = sum(pool.map(kernels, ("ag_rows", "ag_linear_i8", "ag_linear_q8")), [])
+    assert len(found) > 100 and all(int(scratch) == 0 for _, scratch in found), [f for f in found if int(f[1])]

@@ -171,6 +171,25 @@ def test_norm_special_rows(K, dtype):
     assert np.isnan(got_scale[[1, 2, 3]]).all() and np.isnan(got_y[1]).all() and np.isnan(got_y[2, K - 1]) and np.isnan(got_y[3, 0])
 
 
+@pytest.mark.parametrize("K", [40, 1000, 5000, 40000])
+def test_norm_products_past_fp32(K):
+    """h weight past fp32's largest: an infinity in y, the row's scale NaN and its codes 0; the sums keep their range."""
+    require_gpu()
+    log(f"norm of products past fp32, K {K}")
+    x = torch.ones(3, K, dtype=torch.bfloat16)
+    x[1] = 2.0 ** 120
+    n = Norm(3, K, "bf16", x=x, residual=False)
+    n.w.view.fill_(1.0)
+    n.w.view[0, K - 1] = 2.0 ** 20
+    n.w.snapshot()
+    ag.rms_norm(**n.args())
+    torch.cuda.synchronize()
+    y, q, s, r = n.y.f64(), n.q.numpy(), n.scale.f64()[0], n.rstd.f64()[0]
+    assert np.isposinf(y[1, K - 1]) and np.isfinite(y[1, :-1]).all() and np.isnan(s[1]) and not q[1].any()
+    assert np.isfinite(y[[0, 2]]).all() and np.isfinite(s[[0, 2]]).all() and (q[[0, 2], K - 1] == 127).all()
+    assert abs(r[1] * 2.0 ** 120 - 1) <= 2.5 * U32
+
+
 # ------------------------------------------------------------------ codes
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
@@ -450,3 +469,22 @@ def test_rows_in_a_graph():
         step(torch.cuda.current_stream())
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(got, outputs)), f"replay {i}"
+
+
+def test_two_streams_at_once():
+    """Calls that may run side by side, each with a workspace of its own."""
+    require_gpu()
+    log("norm gradients on two streams")
+    work = []
+    for i, (M, K) in enumerate(((3000, 4100), (4000, 1000), (300, 600), (900, 20000))):
+        b = Backward(M, K, "bf16", "f32", seed=20 + i)
+        p = ag.plan_rms_norm_backward(**b.args())
+        work.append((b, p, torch.full((max(1, p.workspace_bytes),), 0xA5, dtype=torch.uint8, device="cuda")))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, (b, p, ws) in enumerate(work):
+            ag.rms_norm_backward(**b.args(), workspace=ws, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for b, p, _ in work:
+        b.check(f"norm backward {b.shape} beside others", p)
