@@ -128,6 +128,7 @@ struct LinearSlopeQ8Args : LinearSlopeArgs {
     const float* x_scale;
     const float* z_scale;
     uint16_t* dz_fold;
+    uint16_t* dz_last;          // what dz_rest's rounding leaves, rounded: a third term; or null
 };
 // x: the codes to 16-bit numbers in the same launch (M 0: none).
 struct DequantizeArgs;

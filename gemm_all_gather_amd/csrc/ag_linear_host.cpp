@@ -397,13 +397,14 @@ struct Backward {
     Mat dy, z, x, w, dx, dw, db, x_scale, z_scale;
     Product px, pw;
     Product rest;               // dw of dz's second term, before pw
+    bool last = false;          // and of its third, before that
     Operand ox, ow;
     bool slope = false, store_dz = false;
     bool fold = false;          // dw takes dz times its row's x_scale (but for a power of two), dx takes dz
     bool together = false;      // dx, dw and db in one launch, side by side
     bool in_turn = false, dx_first = false;   // or one after the other
     bool db_alone = false;      // db in a launch of its own; else beside a product
-    uint64_t dz_offset = 0, dz_fold_offset = 0, dz_rest_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
+    uint64_t dz_offset = 0, dz_fold_offset = 0, dz_rest_offset = 0, dz_last_offset = 0, sums_offset = 0, partial_offset = 0, workspace = 0;
     int64_t parts = 0, lddz = 0, rows = 8;
     int launches = 0;
 };
@@ -466,10 +467,16 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
     // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 to 2290 us against 1468
     // to 1490 of a bf16 dw, of 1024 rows 231 against 122.  dx and a 16-bit dw take one term: their own rounding is as
     // large (2.3e-3 in all against 1.7e-3), and two would double the time of both products.  relu's dz needs no rounding.
-    // With a row's scale in it, every dz does.
+    // With a row's scale in it, every dz does, and in bf16 three of them: two would leave 2.5e-6 where x itself has no error (and
+    // where, without codes, none's and relu's dw is one product of exact operands).
     const bool two_terms = want_dw && a->dw_dtype == AG_F32 && (b->fold || (b->store_dz && act && a->act != AG_ACT_RELU));
     if (two_terms) {
         b->dz_rest_offset = used;
+        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
+        b->last = b->fold && a->dtype == AG_BF16;
+    }
+    if (b->last) {
+        b->dz_last_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
     }
     if (want_db) {
@@ -543,7 +550,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
     b->workspace = used + std::max({b->px.partial_bytes, b->pw.partial_bytes, b->rest.partial_bytes});
     b->db_alone = want_db && !b->px.on && !b->pw.on;
     b->launches = (b->slope ? 1 : 0) + (b->together || b->in_turn ? 1 : (b->db_alone ? 1 : 0) + b->px.launches() + b->pw.launches()) +
-                  b->rest.launches() + (b->ow.pack ? 1 : 0) + (b->ox.pack && !b->fold ? 1 : 0);
+                  b->rest.launches() * (b->last ? 2 : 1) + (b->ow.pack ? 1 : 0) + (b->ox.pack && !b->fold ? 1 : 0);
     return AG_OK;
 }
 
@@ -760,6 +767,7 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         a.act = args->act;
         a.rows = static_cast<int32_t>(b.rows);
         a.dz_fold = b.fold ? dz_fold : nullptr;
+        a.dz_last = b.last ? reinterpret_cast<uint16_t*>(ws + b.dz_last_offset) : nullptr;
         a.x_scale = b.fold ? x_scale : nullptr;
         a.z_scale = a.z ? z_scale : nullptr;
         ag::DequantizeArgs codes{};
@@ -810,10 +818,12 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         e.ldo = b.dw.ld;
         e.out_f32 = args->dw_dtype == AG_F32;
         e.accumulate = args->accumulate;
-        if (b.rest.on) {    // the small term first, on the earlier gradient if there is one; the other adds to it
-            const uint16_t* dz_rest = reinterpret_cast<const uint16_t*>(ws + b.dz_rest_offset);
-            if ((s = run_product(b.rest, gemm_args(b.rest, dz_rest, b.lddz, X, ldx, e, partial), bf16, stream)) != AG_OK) return s;
-            e.accumulate = 1;
+        if (b.rest.on) {    // the smallest term first, on the earlier gradient if there is one; the others add to it
+            for (int term = b.last ? 2 : 1; term > 0; --term) {
+                const uint16_t* dz_term = reinterpret_cast<const uint16_t*>(ws + (term == 2 ? b.dz_last_offset : b.dz_rest_offset));
+                if ((s = run_product(b.rest, gemm_args(b.rest, dz_term, b.lddz, X, ldx, e, partial), bf16, stream)) != AG_OK) return s;
+                e.accumulate = 1;
+            }
         }
         dw = gemm_args(b.pw, dzw, lddzw, X, ldx, e, partial);
     }

@@ -9,9 +9,9 @@ namespace ag {
 namespace {
 
 // dz = dy act'(z), where z may be codes, rounded for dx; dz times the factor in [1/2, 1) of its row's x_scale, rounded for dw
-// (x's codes times the scale's power of two are exact in 16 bits), with what that rounding leaves; and the column sums
-// of the unrounded dz over a.rows rows.  Threads and sums as in the kernel without codes.
-template <bool BF16, bool REST, bool X8, bool Z8>
+// (x's codes times the scale's power of two are exact in 16 bits), with up to two more terms of what that rounding leaves;
+// and the column sums of the unrounded dz over a.rows rows.  Threads and sums as in the kernel without codes.
+template <bool BF16, int TERMS, bool X8, bool Z8>
 __device__ __forceinline__ void slope_body(const LinearSlopeQ8Args& a, uint32_t program)
 {
     __shared__ float part[8][264];
@@ -72,14 +72,14 @@ __device__ __forceinline__ void slope_body(const LinearSlopeQ8Args& a, uint32_t 
                     for (int e = 0; e < 8; ++e) v[e] *= rest;
                     store_16<BF16>(a.dz_fold + row * a.lddz + col, v, n);
                 }
-                if constexpr (REST) {
-                    float rest[8];      // exact in fp32; nothing of what is not finite in 16 bits
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                for (int term = 1; term < TERMS; ++term) {      // what the term before leaves
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {       // exact in fp32; nothing of what is not finite in 16 bits
                         const float kept = to_f32<BF16>(from_f32<BF16>(v[e]));
-                        rest[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
+                        v[e] = __builtin_isfinite(kept) ? v[e] - kept : 0.f;
                     }
-                    store_16<BF16>(a.dz_rest + row * a.lddz + col, rest, n);
+                    store_16<BF16>((term == 1 ? a.dz_rest : a.dz_last) + row * a.lddz + col, v, n);
                 }
             }
         }
@@ -99,18 +99,18 @@ __device__ __forceinline__ void slope_body(const LinearSlopeQ8Args& a, uint32_t 
 }
 
 // dz, and beside it x's codes as 16-bit numbers for the product that follows (x.M 0: none): two passes over memory in one launch.
-template <bool BF16, bool REST, bool X8, bool Z8>
+template <bool BF16, int TERMS, bool X8, bool Z8>
 __global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a, DequantizeArgs x, uint32_t slope_programs)
 {
-    if (blockIdx.x < slope_programs) slope_body<BF16, REST, X8, Z8>(a, blockIdx.x);
+    if (blockIdx.x < slope_programs) slope_body<BF16, TERMS, X8, Z8>(a, blockIdx.x);
     else if constexpr (X8) dequantize_body<(BF16 ? AG_BF16 : AG_F16)>(x, blockIdx.x - slope_programs, gridDim.x - slope_programs);
 }
 
 using SlopeFn = void (*)(LinearSlopeQ8Args, DequantizeArgs, uint32_t);
-template <bool BF16, bool REST> SlopeFn pick(bool x8, bool z8)
+template <bool BF16, int TERMS> SlopeFn pick(bool x8, bool z8)
 {
-    return x8 ? (z8 ? ag_linear_slope_q8_kernel<BF16, REST, true, true> : ag_linear_slope_q8_kernel<BF16, REST, true, false>)
-              : ag_linear_slope_q8_kernel<BF16, REST, false, true>;
+    return x8 ? (z8 ? ag_linear_slope_q8_kernel<BF16, TERMS, true, true> : ag_linear_slope_q8_kernel<BF16, TERMS, true, false>)
+              : ag_linear_slope_q8_kernel<BF16, TERMS, false, true>;
 }
 
 }  // namespace
@@ -121,8 +121,9 @@ hipError_t launch_linear_slope_q8(const LinearSlopeQ8Args& a, const DequantizeAr
     const bool x8 = a.x_scale != nullptr, z8 = a.z_scale != nullptr;
     const int64_t copies = x8 && x.M > 0 && x.K > 0 ? dequantize_programs(x) : 0;
     if (groups < 1 || groups + copies >= (int64_t{1} << 24) || (!x8 && !z8) || (x8 && !a.dz_fold)) return hipErrorInvalidValue;
-    const SlopeFn fn = a.dz_rest ? (bf16 ? pick<true, true>(x8, z8) : pick<false, true>(x8, z8))
-                                 : (bf16 ? pick<true, false>(x8, z8) : pick<false, false>(x8, z8));
+    if (a.dz_last && (!a.dz_rest || !bf16)) return hipErrorInvalidValue;
+    const SlopeFn fn = a.dz_last ? pick<true, 3>(x8, z8) : a.dz_rest ? (bf16 ? pick<true, 2>(x8, z8) : pick<false, 2>(x8, z8))
+                                                                  : (bf16 ? pick<true, 1>(x8, z8) : pick<false, 1>(x8, z8));
     hipLaunchKernelGGL(fn, dim3(static_cast<uint32_t>(groups + copies)), dim3(256), 0, stream, a, x, static_cast<uint32_t>(groups));
     return hipGetLastError();
 }

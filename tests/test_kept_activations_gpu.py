@@ -97,15 +97,18 @@ def test_training(dtype):
     assert_codes(n8.cpu().numpy(), codes, "kept norm")
     nk, zk = codes * f64(ns)[:, None], z8.cpu().numpy() * f64(zs)[:, None]
     want_dn, want_dw, want_db, dz = linear_backward_oracle(f64(dy), zk, nk, f64(w), "gelu")
-    # dz's evaluation and, for dn, its rounding; for dw two terms of dz times a factor of at least 1/2
+    # dz's evaluation and, for dn, its rounding; for dw two terms (bf16: three) of dz times a factor of at least 1/2
     half, tiny = HALF_STEP[dtype], TINY[dtype]
     dz_off = (ACT_ERROR * (1 + np.abs(zk)) + U32 + 1.2 * U32 * np.abs(zk)) * np.abs(f64(dy))
     dz_x = rounded_bound(dz, dz_off, dtype)
     off = dz_x @ np.abs(f64(w)) + product_bound(np.abs(dz) + dz_x, f64(w).T, N)
     assert_close(f64(dn), want_dn, rounded_bound(want_dn, off, dtype), "gradient of the layer's input")
     folded = dz_off + U32 * np.abs(dz)
-    dz_w = folded + half * (half * (np.abs(dz) + folded) + 2 * tiny) + 2 * tiny
-    off = dz_w.T @ np.abs(nk) + 3 * product_bound((np.abs(dz) + dz_w).T, nk.T, M)
+    dz_w = half * (np.abs(dz) + folded) + 2 * tiny
+    for _ in range(2 if dtype == "bf16" else 1):
+        dz_w = half * dz_w + 2 * tiny
+    dz_w = folded + dz_w
+    off = dz_w.T @ np.abs(nk) + 3 * product_bound((np.abs(dz) + dz_w).T, nk.T, M + 2)
     assert_close(f64(dw), want_dw, rounded_bound(want_dw, off, "f32"), "gradient of the weight")
     assert_close(f64(db), want_db, rounded_bound(want_db, dz_off.sum(0) + (M + 8) * U32 * (np.abs(dz) + dz_off).sum(0), "f32"), "gradient of the bias")
     # the norm's, from the gradient that was stored

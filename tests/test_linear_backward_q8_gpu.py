@@ -37,6 +37,7 @@ class BackwardQ8(Backward):
     def __init__(self, M, N, K, dtype, act="none", dw_dtype=None, accumulate=False, db=True, pad=0, offset=0, seed=1, x8=True, z8=True):
         super().__init__(M, N, K, dtype, act, dw_dtype, accumulate, db, pad, offset, seed)
         self.x8, self.z8 = x8, z8 and act != "none"
+        self.terms = 3 if x8 and dtype == "bf16" else 2         # of dz for a dw in fp32
         if x8:
             self.x = Kept(self.x, pad, offset)
         if self.z8:
@@ -61,18 +62,21 @@ class BackwardQ8(Backward):
         folded = dz_off + U32 * np.abs(dz)
         if not self.x8:
             dz_w = dz_x if self.dw_dtype != "f32" or self.act == "none" else dz_off + h * (h * (np.abs(dz) + dz_off) + tiny) + tiny
-        elif self.dw_dtype == "f32":        # two terms: the second is off by half a step of half a step
-            dz_w = folded + h * (h * (np.abs(dz) + folded) + 2 * tiny) + 2 * tiny
+        elif self.dw_dtype == "f32":        # each term is what the one before leaves, half a step of it
+            dz_w = h * (np.abs(dz) + folded) + 2 * tiny
+            for _ in range(self.terms - 1):
+                dz_w = h * dz_w + 2 * tiny
+            dz_w = folded + dz_w
         else:                               # the factor is at least 1/2
             dz_w = folded + h * (np.abs(dz) + folded) + 2 * tiny
         size, size_w = np.abs(dz) + dz_x, np.abs(dz) + dz_w
         off_x = dz_x @ np.abs(w) + (N + 8) * U32 * (size @ np.abs(w))
-        sums = 2 * (M + 8) + 2 if self.dw_dtype == "f32" else M + 8
+        sums = self.terms * (M + 10) if self.dw_dtype == "f32" else M + 8
         off_w = dz_w.T @ np.abs(x) + sums * U32 * (size_w.T @ np.abs(x))
         off_b = dz_off.sum(0) + (M + 8) * U32 * size.sum(0)
         if self.accumulate:
             dw = dw + self.dw0
-            off_w = off_w + 2 * U32 * (np.abs(dw) + np.abs(self.dw0))
+            off_w = off_w + self.terms * U32 * (np.abs(dw) + np.abs(self.dw0))
             if self.db is not None:
                 db = db + self.db0[0]
                 off_b = off_b + U32 * (np.abs(db) + np.abs(self.db0[0]))
