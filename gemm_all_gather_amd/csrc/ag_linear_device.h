@@ -778,22 +778,71 @@ __device__ __forceinline__ void gemm_body(const typename E::Args& a, int program
                 }
             });
         } else {
+            // As above (1000 x 4096 x 4096: 29.5 -> 27.0 us).  What a lane may not use is awaited all the same, by the empty asm: a load
+            // left pending would be awaited in the next tile's products, with all of its own (16384 x 3584 x 8192: 390 -> 412 us).
+            [[maybe_unused]] float col_scale[E::I8 ? BN / 2 : 1][8], col_bias[E::I8 ? BN / 2 : 1][8], row_ahead = 1.f;
+            [[maybe_unused]] u32x4 ahead[E::I8 ? BN / 2 : 1];
+            [[maybe_unused]] auto residual_of = [&](int64_t row, int b) __attribute__((always_inline)) {
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (a.epi.residual && row < a.I && col0 + 32 * b + 8 <= a.J)
+                    v = reinterpret_cast<const Any16*>(a.epi.residual + row * a.epi.ldr + col0 + 32 * b)->v;
+                return v;
+            };
+            if constexpr (E::I8) {
+#pragma unroll
+                for (int b = 0; b < BN / 2; ++b) {
+                    const int64_t col = col0 + 32 * b;
+                    const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
+                    load_scales(col_scale[b], a.col_scale + col, n);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) col_bias[b][e] = 0.f;
+                    if (a.epi.bias) load_f32<BF16>(col_bias[b], a.epi.bias + col, n);
+                }
+                row_ahead = a.row_scale[min(row0, a.I - 1)];
+#pragma unroll
+                for (int b = 0; b < BN / 2; ++b) ahead[b] = residual_of(row0, b);
+#pragma unroll
+                for (int b = 0; b < BN / 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(col_scale[b][e]), "+v"(col_bias[b][e]));
+            }
             each<BM>([&](auto row_block) __attribute__((always_inline)) {
                 constexpr int bm = decltype(row_block)::value;
                 const int64_t row = row0 + 16 * bm;
+                [[maybe_unused]] float row_scale = row_ahead;
+                if constexpr (E::I8) {
+                    asm volatile("" : "+v"(row_scale));
+                    if constexpr (bm + 1 < BM) row_ahead = a.row_scale[min(row + 16, a.I - 1)];
+                }
 #pragma unroll
                 for (int b = 0; b < BN / 2; ++b) {
                     float x[8];
                     widen(x, acc[bm][2 * b], acc[bm][2 * b + 1]);
                     const int64_t col = col0 + 32 * b;
                     const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.J - col)));
+                    [[maybe_unused]] u32x4 residual = {};
+                    if constexpr (E::I8) {
+                        residual = ahead[b];
+                        asm volatile("" : "+v"(residual));
+                        if constexpr (bm + 1 < BM) ahead[b] = residual_of(row + 16, b);
+                    }
                     if (row < a.I && n > 0) {
                         if constexpr (E::I8) {
-                            float col_scale[8];
-                            load_scales(col_scale, a.col_scale + col, n);
-                            apply_scales(x, a.row_scale[row], col_scale);
-                        }
-                        if constexpr (FORM == kFormNT) {
+                            apply_scales(x, row_scale, col_scale[b]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] += col_bias[b][e];
+                            if (a.epi.z) store_16<BF16>(a.epi.z + row * a.epi.ldz + col, x, n);
+                            activate(x, ACT);
+                            if (a.epi.residual) {
+                                float r[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) r[e] = to_f32<BF16>(static_cast<uint16_t>(residual[e >> 1] >> (16 * (e & 1))));
+                                if (n < 8) load_f32<BF16>(r, a.epi.residual + row * a.epi.ldr + col, n);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[e] += r[e];
+                            }
+                            store_16<BF16>(static_cast<uint16_t*>(a.epi.out) + row * a.epi.ldo + col, x, n);
+                        } else if constexpr (FORM == kFormNT) {
                             float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                             if (a.epi.bias) load_f32<BF16>(bias, a.epi.bias + col, n);
                             finish_layer<BF16>(x, bias, a.epi, ACT, row, col, n);
