@@ -528,8 +528,20 @@ __device__ __forceinline__ void gemm_body(const typename E::Args& a, int program
         return PartB::start(a.B, j0, a.J, E::units(a.R), ldb2, w.first, w.count);
     };
     int qa = 0, qb = 0;
-    typename PartA::Next na = start_a(0);
-    typename PartB::Next nb = start_b(0);
+    typename PartA::Next na;
+    typename PartB::Next nb;
+    [[maybe_unused]] Piece first;
+    if constexpr (E::I8) {      // the first piece's divisions once, with what the loads need on its way: nothing hides them here
+        asm volatile("" ::"s"(a.A), "s"(a.B), "s"(a.I), "s"(a.J), "s"(a.R), "s"(a.stages), "s"(a.tiles_i));
+        first = piece_of(a, program, programs, 0);
+        int64_t i0, j0;
+        place_tile(a, first.tile, C::TM, C::TN, &i0, &j0);
+        na = PartA::start(a.A, i0, a.I, E::units(a.R), lda2, first.first, first.count);
+        nb = PartB::start(a.B, j0, a.J, E::units(a.R), ldb2, first.first, first.count);
+    } else {
+        na = start_a(0);
+        nb = start_b(0);
+    }
     auto take_a = [&] {
         const typename PartA::At t = PartA::take(na, lda2);
         if (na.stages == 0) na = start_a(++qa);     // past the last piece: no stages, nothing more is fetched
@@ -616,7 +628,7 @@ __device__ __forceinline__ void gemm_body(const typename E::Args& a, int program
     wait_vmcnt<C::SA * C::LA + C::SB * C::LB - C::LA - C::LB - (C::LATE_A ? C::LA : C::LB)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    Piece w = piece_of(a, program, programs, 0);
+    Piece w = E::I8 ? first : piece_of(a, program, programs, 0);
     if (ragged && w.count == 1 && w.first + 1 == a.stages) clear_tail(0, 0);
 #pragma unroll
     for (int i = 0; i < BM + BN; ++i) read(0, lds_a, lds_b, 0, i);
