@@ -12,7 +12,7 @@ namespace ag {
 namespace {
 
 // The values of codes: 8 to a lane, so that a wave's stores are whole lines; a thread takes kDequantizeVectors of them.
-template <int DTYPE>
+template <int DTYPE, bool MORE = false>
 __device__ __forceinline__ void dequantize_body(const DequantizeArgs& a, uint32_t program, uint32_t programs)
 {
     const uint32_t per_row = (static_cast<uint32_t>(a.K) + 7u) / 8u;
@@ -64,6 +64,9 @@ __device__ __forceinline__ void dequantize_body(const DequantizeArgs& a, uint32_
                 }
             } else {
                 store_16<DTYPE == AG_BF16>(static_cast<uint16_t*>(a.y) + at, v, n);
+                if constexpr (MORE) {
+                    for (int c = 1; c <= a.more; ++c) store_16<DTYPE == AG_BF16>(static_cast<uint16_t*>(a.y) + at + c * a.M * a.ldy, v, n);
+                }
             }
         }
     }

@@ -398,6 +398,7 @@ struct Backward {
     Product px, pw;
     Product rest;               // dw of dz's second term, before pw
     bool last = false;          // and of its third, before that
+    int stacked = 0;            // or dw in one product of so many terms, one below the other, the smallest first, and as many copies of x
     Operand ox, ow;
     bool slope = false, store_dz = false;
     bool fold = false;          // dw takes dz times its row's x_scale (but for a power of two), dx takes dz
@@ -458,10 +459,6 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
         b->dz_offset = used;
         used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
     }
-    if (b->fold) {
-        b->dz_fold_offset = used;
-        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
-    }
     // A weight gradient in fp32 takes dz in two 16-bit terms and so two products: with one it would carry the error
     // of a 16-bit gradient (2-norm relative to dw's 1.7e-3 in bf16, 2.1e-4 in fp16; with two 2.5e-6 and 3.5e-7, as
     // far as fp32 sums go).  It costs a product: all gradients of 16384 x 3584 x 8192, bf16, 2245 to 2290 us against 1468
@@ -470,14 +467,22 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
     // With a row's scale in it, every dz does, and in bf16 three of them: two would leave 2.5e-6 where x itself has no error (and
     // where, without codes, none's and relu's dw is one product of exact operands).
     const bool two_terms = want_dw && a->dw_dtype == AG_F32 && (b->fold || (b->store_dz && act && a->act != AG_ACT_RELU));
-    if (two_terms) {
-        b->dz_rest_offset = used;
-        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
-        b->last = b->fold && a->dtype == AG_BF16;
-    }
-    if (b->last) {
+    b->last = two_terms && b->fold && a->dtype == AG_BF16;
+    const int terms = !b->fold ? 0 : b->last ? 3 : two_terms ? 2 : 1;
+    // In one product rather than each in its own, adding to dw in memory: fewer launches, dw written once and its tiles' fixed costs paid
+    // once, for copies of x's values, one per term, to be written and read (bf16, all gradients with dw in fp32, us apart and as one: 1 x
+    // 4783 x 3520 154 and 59, 1024 x 3584 x 8192 326 and 238, 16384 x 3584 x 8192 3010 and 2935, 16384 x 512 x 1024 177 and 139).  The
+    // copies weigh more, the narrower dw: 8192 x 128 x 8192 226 and 253.
+    b->stacked = terms > 1 && M / 32 <= N ? terms : 0;
+    const uint64_t term_bytes = static_cast<uint64_t>(M) * b->lddz * 2;
+    if (b->fold) {          // the smallest term first, each right below the one before
         b->dz_last_offset = used;
-        used += up256(static_cast<uint64_t>(M) * b->lddz * 2);
+        b->dz_rest_offset = used + (b->last ? term_bytes : 0);
+        b->dz_fold_offset = used + (terms - 1) * term_bytes;
+        used += up256(terms * term_bytes);
+    } else if (two_terms) {
+        b->dz_rest_offset = used;
+        used += up256(term_bytes);
     }
     if (want_db) {
         b->parts = (M + b->rows - 1) / b->rows;
@@ -501,9 +506,9 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
         b->pw.form = ag::kFormTN;
         b->pw.I = N;
         b->pw.J = K;
-        b->pw.R = M;
+        b->pw.R = b->stacked ? b->stacked * M : M;
         if ((s = choose(&b->pw, cus)) != AG_OK) return s;
-        b->ox = Operand{b->x.at, b->x.ld, M, K};
+        b->ox = Operand{b->x.at, b->x.ld, b->pw.R, K};
         if (b->fold) {      // the codes times the scales' powers of two, in 16 bits
             b->ox.pack = b->ox.lines = true;
             b->ox.copy_offset = used;
@@ -511,7 +516,7 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
         } else {
             place(&b->ox, &used);
         }
-        if (two_terms) b->rest = b->pw;
+        if (two_terms && !b->stacked) b->rest = b->pw;
     }
     // Both products' 128 x 128 tiles on CUs of their own: one launch for what follows dz.
     if (b->px.on && b->pw.on) {
@@ -757,7 +762,7 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         a.dy = static_cast<const uint16_t*>(args->dy);
         a.z = args->act != AG_ACT_NONE ? static_cast<const uint16_t*>(args->z) : nullptr;
         a.dz = b.store_dz ? reinterpret_cast<uint16_t*>(ws + b.dz_offset) : nullptr;
-        a.dz_rest = b.rest.on ? reinterpret_cast<uint16_t*>(ws + b.dz_rest_offset) : nullptr;
+        a.dz_rest = b.rest.on || b.stacked ? reinterpret_cast<uint16_t*>(ws + b.dz_rest_offset) : nullptr;
         a.sums = want_db ? sums : nullptr;
         a.lddy = b.dy.ld;
         a.ldz = b.z.ld;
@@ -773,7 +778,7 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         ag::DequantizeArgs codes{};
         if (b.fold) {
             codes = ag::DequantizeArgs{static_cast<const int8_t*>(args->x), x_scale, ws + b.ox.copy_offset, b.x.ld, b.ox.copy_ld(),
-                                       args->M, static_cast<int32_t>(args->K), 1};
+                                       args->M, static_cast<int32_t>(args->K), 1, b.stacked ? b.stacked - 1 : 0};
         }
         const hipError_t e = a.x_scale || a.z_scale ? ag::launch_linear_slope_q8(a, codes, bf16, stream)
                                                     : ag::launch_linear_slope(a, bf16, stream);
@@ -811,7 +816,7 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         } else if ((s = pack(b.ox, workspace, stream, &X, &ldx)) != AG_OK) {
             return s;
         }
-        const uint16_t* dzw = b.fold ? dz_fold : dz;
+        const uint16_t* dzw = b.stacked ? reinterpret_cast<const uint16_t*>(ws + b.dz_last_offset) : b.fold ? dz_fold : dz;
         const int64_t lddzw = b.fold ? b.lddz : lddz;
         ag::LinearEpilogue e{};
         e.out = args->dw;

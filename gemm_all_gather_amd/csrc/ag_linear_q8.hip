@@ -103,7 +103,7 @@ template <bool BF16, int TERMS, bool X8, bool Z8>
 __global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a, DequantizeArgs x, uint32_t slope_programs)
 {
     if (blockIdx.x < slope_programs) slope_body<BF16, TERMS, X8, Z8>(a, blockIdx.x);
-    else if constexpr (X8) dequantize_body<(BF16 ? AG_BF16 : AG_F16)>(x, blockIdx.x - slope_programs, gridDim.x - slope_programs);
+    else if constexpr (X8) dequantize_body<(BF16 ? AG_BF16 : AG_F16), true>(x, blockIdx.x - slope_programs, gridDim.x - slope_programs);
 }
 
 using SlopeFn = void (*)(LinearSlopeQ8Args, DequantizeArgs, uint32_t);

@@ -48,6 +48,7 @@ struct DequantizeArgs {
     int64_t M;
     int32_t K;
     int32_t by_power;
+    int32_t more = 0;       // further copies of all M rows, one below the other (beside other work only)
 };
 constexpr int kDequantizeVectors = 4;
 inline int64_t dequantize_programs(const DequantizeArgs& a)      // workgroups of 256 threads

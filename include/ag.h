@@ -743,7 +743,8 @@ ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_l
  * needs no rounded copy of x.  The other factor lies in [1/2, 1) (1 and more
  * in AG_F16 for rows that hold 32512 or more), so that a dz that has a place
  * in dtype keeps one.  A dw in AG_F32 takes dz in two terms of AG_F16 or
- * three of AG_BF16, and as many products.
+ * three of AG_BF16, and their products.  The workspace holds x's codes as
+ * values of dtype, for such a dw one copy per term unless M > 32 N.
  * Either scale may be NULL. */
 ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);

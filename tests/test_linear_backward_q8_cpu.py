@@ -67,3 +67,16 @@ def test_plans():
     assert both.workspace_bytes >= 2 * (2 * M * N + M * K)
     z_only = ag.plan_linear_backward_q8(**dict(BACKWARD, x_scale=None))
     assert z_only.workspace_bytes == plain.workspace_bytes and z_only.launches == plain.launches
+
+
+@pytest.mark.parametrize("dtype,terms", [("f16", 2), ("bf16", 3)])
+@pytest.mark.parametrize("M", [1, 200, 32 * 200 + 31, 32 * 200 + 32])
+def test_terms_of_a_wide_weight_gradient(M, dtype, terms):
+    """dw in fp32: dz's terms in one product with as many copies of x, or, of few columns, a product each."""
+    N, K = 200, 256         # rows of dz's terms take 256 elements, those of x's values 256
+    wide = ag.plan_linear_backward_q8(**dict(BACKWARD, M=M, N=N, K=K, dtype=dtype, dw_dtype="f32", dx=None, w=None, db=None))
+    dz, x = 2 * M * 256 * terms, 2 * M * K
+    if M // 32 <= N:
+        assert wide.workspace_bytes >= dz + terms * x and wide.launches <= 3        # codes and terms, the product, its join
+    else:
+        assert wide.launches >= 1 + terms       # (cut tiles' sums are in the workspace too, so its size says nothing here)

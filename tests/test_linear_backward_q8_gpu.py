@@ -237,3 +237,16 @@ def test_stays_inside_its_workspace(M, N, K, pad, dw):
         bits = [m.buffer.view(torch.int32 if m.dtype == "f32" else torch.int16).clone() for m in (b.dx, b.dw, b.db)]
         assert first is None or all(torch.equal(u, v) for u, v in zip(first, bits))
         first = bits
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 520), (3, 1030, 70), (127, 4, 264), (128, 4, 264), (700, 9, 33), (2100, 64, 600), (2111, 130, 1030)])
+def test_terms_of_a_wide_weight_gradient(M, N, K, dtype):
+    """dw in fp32: dz's terms below each other in one product, whose stages the rows of one term end inside, or a product each."""
+    require_gpu()
+    for acc, pad in ((False, 0), (True, 3)):
+        what = f"linear_backward_q8 {M}x{N}x{K} {dtype} dw f32 accumulate {acc} pad {pad}"
+        log(what)
+        b = BackwardQ8(M, N, K, dtype, "gelu_tanh", "f32", acc, pad=pad, seed=M)
+        b.run()
+        b.check(what)
