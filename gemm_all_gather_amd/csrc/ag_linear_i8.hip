@@ -9,7 +9,7 @@ namespace {
 // ---------------------------------------------------------------- join of cut tiles
 
 // Adds the parts of a tail tile, 8 consecutive columns per thread: sums of integers, exact in any order; then the epilogue.
-// Bound by memory as the join of 16-bit products.
+// Bound by memory as the join of 16-bit products: 256 tiles of 256 x 256 in two parts 17 to 18 us (8 of 128 x 128 in 11 parts, latency, 5.5).
 template <bool BF16>
 __global__ __launch_bounds__(256) void ag_linear_i8_join_kernel(LinearI8GemmArgs a, int tm, int tn)
 {
@@ -63,7 +63,8 @@ __device__ __forceinline__ i32x4 load16(const int8_t* p, int64_t left)
 
 // y for up to 16 MB rows of x: the weights are streamed once, straight into matrix-instruction fragments, 16 rows of w per
 // workgroup.  The workgroup's waves share the reduction, 256 wide at a time, and add up through LDS; D rows are rows of
-// w, D columns rows of x.  Bound by the stream of w and the start and end of a launch.
+// w, D columns rows of x.  Bound by the stream of w and the start and end of a launch: 3584 x 8192 8.2 us of one row (29 MB; 5.3 at a
+// large copy's rate), 11.5 of 17, where each workgroup's reads of x weigh as much as those of w.
 template <bool BF16, int MB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI8StreamArgs a)
 {
@@ -169,7 +170,7 @@ __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI
 // ---------------------------------------------------------------- rows to aligned rows
 
 // Rows to rows of 16-byte multiples, for operands that do not start on 4 bytes or have other strides: one matrix, or both
-// operands one after the other in one launch.
+// operands one after the other in one launch.  Bound by memory: 1000 x 4100 and 4100 x 4100 9.2 us (42 MB).
 __global__ __launch_bounds__(256) void ag_linear_i8_pack_kernel(LinearI8Pack first, LinearI8Pack second, uint32_t first_groups)
 {
     const bool one = blockIdx.x < first_groups;

@@ -98,7 +98,8 @@ __device__ __forceinline__ void slope_body(const LinearSlopeQ8Args& a, uint32_t 
     }
 }
 
-// dz, and beside it x's codes as 16-bit numbers for the product that follows (x.M 0: none): two passes over memory in one launch.
+// dz, and beside it x's codes as 16-bit numbers for the product that follows (x.M 0: none): two passes over memory in one launch,
+// bound by it: 16384 x 3584 (z in codes) beside 16384 x 8192 bf16 132 to 138 us (814 MB, 6 TB/s), dz alone 74.
 template <bool BF16, int TERMS, bool X8, bool Z8>
 __global__ __launch_bounds__(256) void ag_linear_slope_q8_kernel(LinearSlopeQ8Args a, DequantizeArgs x, uint32_t slope_programs)
 {
