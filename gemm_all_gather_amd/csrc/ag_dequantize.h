@@ -11,10 +11,12 @@
 namespace ag {
 namespace {
 
-// The values of codes: 8 to a lane, so that a wave's stores are whole lines; a thread takes kDequantizeVectors of them.
-template <int DTYPE, bool MORE = false>
+// The values of codes: 8 to a lane, so that a wave's stores are whole lines; a thread takes kDequantizeVectors of them.  POWERS (bf16):
+// the codes times the powers of two of their scales, and a.more copies of that.
+template <int DTYPE, bool POWERS = false>
 __device__ __forceinline__ void dequantize_body(const DequantizeArgs& a, uint32_t program, uint32_t programs)
 {
+    static_assert(!POWERS || DTYPE == AG_BF16, "fp16's powers depend on the gradients too");
     const uint32_t per_row = (static_cast<uint32_t>(a.K) + 7u) / 8u;
     const uint64_t vectors = static_cast<uint64_t>(a.M) * per_row;
     constexpr uint64_t PER = 256 * kDequantizeVectors;
@@ -44,9 +46,9 @@ __device__ __forceinline__ void dequantize_body(const DequantizeArgs& a, uint32_
             if (from + j * 256 + threadIdx.x >= vectors) break;
             const int n = a.K - col[j];
             float scale = s[j], v[8];
-            if (a.by_power) {
+            if constexpr (POWERS) {
                 float rest;
-                split_scale<DTYPE == AG_BF16>(s[j], &scale, &rest);
+                split_scale_bf16(s[j], &scale, &rest);
             }
             code_values(v, q[j]);
 #pragma unroll
@@ -64,7 +66,7 @@ __device__ __forceinline__ void dequantize_body(const DequantizeArgs& a, uint32_
                 }
             } else {
                 store_16<DTYPE == AG_BF16>(static_cast<uint16_t*>(a.y) + at, v, n);
-                if constexpr (MORE) {
+                if constexpr (POWERS) {
                     for (int c = 1; c <= a.more; ++c) store_16<DTYPE == AG_BF16>(static_cast<uint16_t*>(a.y) + at + c * a.M * a.ldy, v, n);
                 }
             }

@@ -123,7 +123,7 @@ struct LinearSlopeArgs {
 };
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, int bf16, hipStream_t stream);
 // The same from activations in 8 bits: z holds codes where z_scale is not null, and dz_fold, where x_scale is not null, receives
-// dz times the scale's factor in [1/2, 1) (split_scale), rounded; dz_rest is then what that rounding leaves.
+// dz times the rest of the scale (ag_scale.h), rounded; dz_rest is then what that rounding leaves.
 struct LinearSlopeQ8Args : LinearSlopeArgs {
     const float* x_scale;
     const float* z_scale;

@@ -778,7 +778,7 @@ ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const f
         ag::DequantizeArgs codes{};
         if (b.fold) {
             codes = ag::DequantizeArgs{static_cast<const int8_t*>(args->x), x_scale, ws + b.ox.copy_offset, b.x.ld, b.ox.copy_ld(),
-                                       args->M, static_cast<int32_t>(args->K), 1, b.stacked ? b.stacked - 1 : 0};
+                                       args->M, static_cast<int32_t>(args->K), b.stacked ? b.stacked - 1 : 0};
         }
         const hipError_t e = a.x_scale || a.z_scale ? ag::launch_linear_slope_q8(a, codes, bf16, stream)
                                                     : ag::launch_linear_slope(a, bf16, stream);

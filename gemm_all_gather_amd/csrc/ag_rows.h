@@ -39,7 +39,7 @@ RowsShape norm_backward_shape(int64_t K);       // vectors 0: in two passes, lau
 // norm with dtype AG_F16 or AG_BF16; without it AG_F32 too.
 hipError_t launch_rows(const RowsArgs& a, int dtype, bool norm, int programs, hipStream_t stream);
 
-// y = q * scale in dtype.  scales_by_two: y = q * (the scale's power of two, by split_scale) in a 16-bit type, exactly.
+// y = q * scale in dtype; beside the gradients that read it, q * (the scale's power of two) in their 16-bit type, exactly.
 struct DequantizeArgs {
     const int8_t* q;
     const float* scale;
@@ -47,8 +47,7 @@ struct DequantizeArgs {
     int64_t ldq, ldy;
     int64_t M;
     int32_t K;
-    int32_t by_power;
-    int32_t more = 0;       // further copies of all M rows, one below the other (beside other work only)
+    int32_t more = 0;       // further copies of all M rows, one below the other (beside the gradients only)
 };
 constexpr int kDequantizeVectors = 4;
 inline int64_t dequantize_programs(const DequantizeArgs& a)      // workgroups of 256 threads

@@ -207,7 +207,7 @@ ag_status_t ag_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale,
     if (s != AG_OK) return s;
     if ((s = check_overlaps({c.q, c.scale}, {c.rows})) != AG_OK) return s;
     if (M == 0 || K == 0) return ok();
-    const DequantizeArgs a{q, scale, y, c.q.ld, c.rows.ld, M, static_cast<int32_t>(K), 0};
+    const DequantizeArgs a{q, scale, y, c.q.ld, c.rows.ld, M, static_cast<int32_t>(K)};
     const hipError_t e = launch_dequantize(a, dtype, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : fail_hip(e, "dequantize rows");
 }

@@ -737,14 +737,18 @@ ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_l
 /* ag_linear_backward from activations that were kept in 8 bits: where x_scale
  * (M floats) is not NULL, args->x holds int8 codes (ldx in codes), and where
  * z_scale is not NULL, args->z does.  The gradients are those of the values
- * that the codes stand for.  A row's x_scale goes into its dz before dz's
- * rounding to dtype, but for its power of two, which goes to the codes and
- * leaves them exact: dw carries one rounding of dz, as without codes, and
- * needs no rounded copy of x.  The other factor lies in [1/2, 1) (1 and more
- * in AG_F16 for rows that hold 32512 or more), so that a dz that has a place
- * in dtype keeps one.  A dw in AG_F32 takes dz in two terms of AG_F16 or
- * three of AG_BF16, and their products.  The workspace holds x's codes as
- * values of dtype, for such a dw one copy per term unless M > 32 N.
+ * that the codes stand for.  For dw, x_scale times dz is rounded to dtype, but for
+ * a power of two, which goes to the codes and leaves them exact: one rounding,
+ * and no rounded copy of x.  (Without codes dz is rounded behind gelu,
+ * gelu_tanh and silu, and exact behind none and relu.)  A dw in AG_F32 takes
+ * dz in two terms of AG_F16 or three of AG_BF16, and their products.
+ * In AG_BF16 the other factor lies in [1/2, 1) for every normal scale.  In
+ * AG_F16 the power is taken from the scale and the row's largest finite |dy|,
+ * D: an element of dz is off by at most half a step of itself in one term and
+ * 2^-22 of itself in two, or by 2^-24 D where that is more (by 2^-49 / x_scale
+ * where x_scale D is below 2^-23); dz x_scale of 2^24 and more leaves AG_F16.
+ * The workspace holds x's codes as values of dtype, for such a dw one copy per
+ * term unless M > 32 N.
  * Either scale may be NULL. */
 ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);
