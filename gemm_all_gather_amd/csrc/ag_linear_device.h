@@ -467,11 +467,18 @@ struct Walk {
     __device__ __forceinline__ void down() { p += rows16; }
 };
 
-// Sums of 8-bit products (the bits of v), times the scales.
+// Sums of 8-bit products (the bits of v), times the scales.  A sum of up to 2^31 times a row's scale is within fp32's normal numbers
+// where the scale is within 2^-126 and 2^96, and then times the column's scale it is the result.  Other rows take 2^64 out of their
+// scale, or into it, and have it back last: what lies between is normal where the result is, and past fp32 only where that is.
 __device__ __forceinline__ void apply_scales(float (&v)[8], float row, const float (&col)[8])
 {
+    asm volatile("" : "+v"(row));       // both factors are worked out here: kept over a tile's columns they cost registers that it has not
+    const uint32_t exponent = (__float_as_uint(row) >> 23) & 255u;
+    const float up = 18446744073709551616.f, down = 1.f / up;       // 2^64
+    const float first = row * (exponent == 0 ? up : exponent >= 127 + 96 ? down : 1.f);
+    const float last = exponent == 0 ? down : exponent >= 127 + 96 ? up : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(__float_as_int(v[e])) * row * col[e];
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(__float_as_int(v[e])) * first * col[e] * last;
 }
 __device__ __forceinline__ void load_scales(float (&v)[8], const float* p, int n)
 {

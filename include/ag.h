@@ -710,9 +710,11 @@ ag_status_t ag_plan_rms_norm_backward(const ag_rms_norm_backward_args_t* args, i
  *   z = x_scale[m] w_scale[n] sum_k x(m,k) w(n,k) + bias
  *   y = act(z) + residual                    (fp32, rounded once to dtype)
  *
- * The sums are exact (int32).  x is M x K, w N x K, both int8; K up to 131071
- * (131072 products of -128 and -128 would leave int32).  bias, residual, y
- * and z have dtype (AG_F16 or AG_BF16).  Everything else is as for ag_linear;
+ * The sums are exact (int32), and with finite scales z leaves fp32's range only
+ * where x_scale w_scale times the sum does, whatever x_scale times the sum is.
+ * x is M x K, w N x K, both int8; K up to 131071 (131072 products of -128 and
+ * -128 would leave int32).  bias, residual, y and z have dtype (AG_F16 or
+ * AG_BF16).  Everything else is as for ag_linear;
  * operands of a tiled product whose rows do not start on 4 bytes are copied.
  * ------------------------------------------------------------------------ */
 typedef struct ag_linear_i8_args {
