@@ -87,6 +87,10 @@ hipError_t launch_linear_stream(const LinearStreamArgs& a, int bf16, int cus, hi
 
 // The same of 8-bit integers.
 constexpr int kLinearI8StreamRows = 64;
+// Blocks of 16 rows of x that a workgroup holds, 1, 2 or 4, and how much of the reduction a wave takes at a time: the more blocks, the
+// fewer registers are left for it.
+inline int linear_i8_stream_blocks(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+constexpr int linear_i8_stream_width(int blocks) { return 256 / blocks; }
 struct LinearI8StreamArgs {
     const int8_t* x;
     const int8_t* w;

@@ -169,9 +169,10 @@ void report(const Product& p, bool pack_a, bool pack_b, ag_product_plan_t* out)
     if (!p.on) return;
     if (p.stream) {
         out->variant = 1;
-        out->tile_m = static_cast<int32_t>((p.I + 15) / 16 * 16);
+        const int blocks = p.i8 ? ag::linear_i8_stream_blocks(p.I) : static_cast<int>((p.I + 15) / 16);
+        out->tile_m = 16 * blocks;
         out->tile_n = 16;
-        out->tile_k = static_cast<int32_t>(2 * p.stage());
+        out->tile_k = p.i8 ? ag::linear_i8_stream_width(blocks) : static_cast<int32_t>(2 * p.stage());
         out->full_tiles = out->n_programs = static_cast<int32_t>((p.J + 15) / 16);
         out->splits = 1;
         return;

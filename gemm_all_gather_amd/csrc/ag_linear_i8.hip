@@ -62,7 +62,7 @@ __device__ __forceinline__ i32x4 load16(const int8_t* p, int64_t left)
 }
 
 // y for up to 16 MB rows of x: the weights are streamed once, straight into matrix-instruction fragments, 16 rows of w per
-// workgroup.  The workgroup's waves share the reduction, 256 wide at a time, and add up through LDS; D rows are rows of
+// workgroup.  The workgroup's waves share the reduction, 256 / MB wide at a time, and add up through LDS; D rows are rows of
 // w, D columns rows of x.  Bound by the stream of w and the start and end of a launch: 3584 x 8192 8.2 us of one row (29 MB; 5.3 at a
 // large copy's rate), 11.5 of 17, where each workgroup's reads of x weigh as much as those of w.
 template <bool BF16, int MB, int WAVES>
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * WAVES) void ag_linear_i8_stream_kernel(LinearI
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[b] = zero;
 
-    constexpr int U = 4 / MB;           // 64-wide steps of a block: more rows of x leave registers for fewer
+    constexpr int U = linear_i8_stream_width(MB) / 64;       // steps of a block
     struct Block {
         i32x4 w[U], x[MB][U];
     };
@@ -225,9 +225,10 @@ hipError_t launch_linear_i8_stream(const LinearI8StreamArgs& a, int bf16, int cu
     dim3 grid;
     if (a.M < 1 || a.M > kLinearI8StreamRows || !grid_of(a.N, 16, &grid)) return hipErrorInvalidValue;
     const bool wide = static_cast<int64_t>(grid.x) <= cus;
-    const StreamFn fn = a.M <= 16 ? (bf16 ? pick_stream<true, 1>(wide) : pick_stream<false, 1>(wide))
-                        : a.M <= 32 ? (bf16 ? pick_stream<true, 2>(wide) : pick_stream<false, 2>(wide))
-                                    : (bf16 ? pick_stream<true, 4>(wide) : pick_stream<false, 4>(wide));
+    const int blocks = linear_i8_stream_blocks(a.M);
+    const StreamFn fn = blocks == 1 ? (bf16 ? pick_stream<true, 1>(wide) : pick_stream<false, 1>(wide))
+                        : blocks == 2 ? (bf16 ? pick_stream<true, 2>(wide) : pick_stream<false, 2>(wide))
+                                      : (bf16 ? pick_stream<true, 4>(wide) : pick_stream<false, 4>(wide));
     hipLaunchKernelGGL(fn, grid, dim3(wide ? 1024 : 512), 0, stream, a);
     return hipGetLastError();
 }
