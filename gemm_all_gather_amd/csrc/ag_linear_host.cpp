@@ -411,6 +411,8 @@ struct Backward {
     int launches = 0;
 };
 
+constexpr uint64_t kMostCopies = uint64_t{128} << 20;     // bytes
+
 // x_scale, z_scale: x and z are 8-bit codes where they are not null.
 ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_scale, const float* z_scale, int cus, Backward* b)
 {
@@ -472,9 +474,12 @@ ag_status_t plan_backward(const ag_linear_backward_args_t* a, const float* x_sca
     const int terms = !b->fold ? 0 : b->last ? 3 : two_terms ? 2 : 1;
     // In one product rather than each in its own, adding to dw in memory: fewer launches, dw written once and its tiles' fixed costs paid
     // once, for copies of x's values, one per term, to be written and read (bf16, all gradients with dw in fp32, us apart and as one: 1 x
-    // 4783 x 3520 154 and 59, 1024 x 3584 x 8192 326 and 238, 16384 x 3584 x 8192 3010 and 2935, 16384 x 512 x 1024 177 and 139).  The
-    // copies weigh more, the narrower dw: 8192 x 128 x 8192 226 and 253.
-    b->stacked = terms > 1 && M / 32 <= N ? terms : 0;
+    // 4783 x 3520 154 and 59, 1024 x 3584 x 8192 326 and 238, 16384 x 512 x 1024 177 and 139).  The copies weigh more, the narrower dw:
+    // 8192 x 128 x 8192 226 and 253.  And they take room, which x was kept in 8 bits to save, for less and less of the time: no more than
+    // kMostCopies beside the first (2048 x 3584 x 8192 490 and 415 us in 93 and 160 MB, 8192 rows 1595 and 1540 in 370 and 840, 16384
+    // rows 3100 and 3000 in 739 and 1478; 16384 x 1024 x 4096 560 and 545 in 337 and 605).
+    const uint64_t more_copies = static_cast<uint64_t>(std::max(0, terms - 1)) * M * ((K + 63) / 64 * 64) * 2;
+    b->stacked = terms > 1 && M / 32 <= N && more_copies <= kMostCopies ? terms : 0;
     const uint64_t term_bytes = static_cast<uint64_t>(M) * b->lddz * 2;
     if (b->fold) {          // the smallest term first, each right below the one before
         b->dz_last_offset = used;

@@ -749,9 +749,10 @@ ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_l
  * D: an element of dz is off by at most half a step of itself in one term and
  * 2^-22 of itself in two, or by 2^-24 D where that is more (by 2^-49 / x_scale
  * where x_scale D is below 2^-23); dz x_scale of 2^24 and more leaves AG_F16.
- * The workspace holds x's codes as values of dtype, for such a dw one copy per
- * term unless M > 32 N.
- * Either scale may be NULL. */
+ * The workspace holds dz, its terms and x's codes as values of dtype: for a dw in
+ * AG_F32 one copy of these per term unless M / 32 (rounded down) is above N or
+ * the copies past the first would take more than 128 MiB.  Either scale may be
+ * NULL. */
 ag_status_t ag_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);
 ag_status_t ag_plan_linear_backward_q8(const ag_linear_backward_args_t* args, const float* x_scale, const float* z_scale,

@@ -163,3 +163,16 @@ def test_zero_and_nan_scales():
         b.run()
         torch.cuda.synchronize()
         assert np.isnan(b.dw.f64()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(159, 4, 264), (160, 4, 264), (8300, 300, 8200)])
+def test_both_sides_of_the_copies_limits(M, N, K, dtype):
+    """dw in fp32 with a copy of x per term, and past 32 rows for a column or 128 MiB of copies with a product per term."""
+    require_gpu()
+    for acc in (False, True) if M < 1000 else (True,):
+        what = f"linear_backward_q8 {M}x{N}x{K} {dtype} dw f32 accumulate {acc}"
+        log(what)
+        b = BackwardQ8(M, N, K, dtype, "gelu", "f32", acc, seed=M)
+        b.run()
+        b.check(what)
