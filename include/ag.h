@@ -744,7 +744,7 @@ ag_status_t ag_plan_linear_i8(const ag_linear_i8_args_t* args, int num_cus, ag_l
  * and no rounded copy of x.  (Without codes dz is rounded behind gelu,
  * gelu_tanh and silu, and exact behind none and relu.)  A dw in AG_F32 takes
  * dz in two terms of AG_F16 or three of AG_BF16, and their products.
- * In AG_BF16 the other factor lies in [1/2, 1) for every normal scale.  In
+ * In AG_BF16 the other factor lies in [1/2, 1) for scales of 2^-126 to 2^119.  In
  * AG_F16 the power is taken from the scale and the row's largest finite |dy|,
  * D: an element of dz is off by at most half a step of itself in one term and
  * 2^-22 of itself in two, or by 2^-24 D where that is more (by 2^-49 / x_scale

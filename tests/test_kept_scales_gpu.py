@@ -17,6 +17,7 @@ import numpy as np
 import pytest
 import torch
 
+from gemm_all_gather_amd import binding as ag
 from oracle.linear_oracle import linear_backward_oracle
 from tests.gpu_util import log, require_gpu
 from tests.linear_util import ACT_ERROR, HALF_STEP, U32, assert_close, rounded_bound
@@ -176,3 +177,32 @@ def test_both_sides_of_the_copies_limits(M, N, K, dtype):
         b = BackwardQ8(M, N, K, dtype, "gelu", "f32", acc, seed=M)
         b.run()
         b.check(what)
+
+
+@pytest.mark.parametrize("dw_dtype", ["f16", "f32"])
+def test_in_a_graph(dw_dtype):
+    """Captured once, replayed on gradients of other sizes, with eager calls on another workspace between: the powers are each replay's."""
+    require_gpu()
+    log(f"linear_backward_q8 f16 dw {dw_dtype} in a graph")
+    b = Small(70, 520, 264, 1.0, "gelu", dw_dtype)
+    a = b.args()
+    need = ag.plan_linear_backward_q8(**a).workspace_bytes
+    space, other = (torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ag.linear_backward_q8(**a, workspace=space, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        ag.linear_backward_q8(**a, workspace=space, stream=side)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for size in (1.0, 1e-4, 1e3, 1e-6):
+        b.dy.view.copy_(torch.randn(b.dy.view.shape, generator=g, device="cuda") * size)
+        b.dy.snapshot()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [m.buffer.clone() for m in (b.dx, b.dw, b.db)]
+        ag.linear_backward_q8(**a, workspace=other)
+        torch.cuda.synchronize()
+        same = lambda u, v: torch.equal(u.view(torch.uint8), v.view(torch.uint8))  # noqa: E731
+        assert all(same(u, m.buffer) for u, m in zip(got, (b.dx, b.dw, b.db))), f"replay at {size}"
+        b.check_weight_gradient(f"replay at {size}")
