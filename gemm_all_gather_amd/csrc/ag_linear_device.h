@@ -925,8 +925,9 @@ __global__ __launch_bounds__(C::NT, 1) void ag_linear_gemm_kernel(LinearGemmArgs
     if constexpr (FORM != kFormNT) bias_grads_after(a.db, blockIdx.x, gridDim.x, ring);
 }
 
-// y of 8-bit integers.  Bound by power where it is large: 16384 x 3584 x 8192 in 256 x 256 tiles 376 to 390 us, 2.5 POP/s; and by the loads'
-// latency where it is one round: 1024 x 3584 x 8192 in 128 x 128 tiles 38 us, 1.6 POP/s.
+// y of 8-bit integers.  Bound by power where it is large: 16384 x 3584 x 8192 in 256 x 256 tiles 376 to 403 us, 2.5 POP/s.  Where it is one
+// round, 1024 x 3584 x 8192 in 128 x 128 tiles 38 us, 1.6 POP/s, a stage takes 1024 cycles with operands in the last-level cache and 1380
+// with weights from HBM: the difference is latency; what holds the 1024 (768 of LDS, 704 of load intake, 512 of the matrix pipe) is not known.
 template <bool BF16, int ACT, class C>
 __global__ __launch_bounds__(C::NT, 1) void ag_linear_i8_gemm_kernel(LinearI8GemmArgs a)
 {

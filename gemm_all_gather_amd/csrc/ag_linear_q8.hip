@@ -228,8 +228,9 @@ __device__ __forceinline__ void fold_rows(const LinearSlopeQ8Args& a, const Dequ
 }
 
 // dz for dx and db's sums (slope_programs 0: neither), and beside them the rows for dw, which work dz out again.  Bound by memory, with dy
-// and z read twice, where a power from the scale alone needs one pass but loses small gradients: all gradients of 16384 x 3584 x 8192
-// 1621 us for 1578, of 1000 x 4100 x 4100 117 for 113, of 16384 x 512 x 1024 100 for 89.
+// and z read twice (16384 x 3584, z in codes, beside 16384 x 8192 187 to 196 us, 1000 x 4100 beside 1000 x 4100 17.6), where a power from the
+// scale alone needs one pass (135, 12) but loses small gradients: all gradients of 16384 x 3584 x 8192 1621 us for 1578, of 1000 x 4100 x
+// 4100 117 for 113, of 16384 x 512 x 1024 100 for 89.
 template <int TERMS, bool Z8, int G>
 __global__ __launch_bounds__(256) void ag_linear_fold_f16_kernel(LinearSlopeQ8Args a, DequantizeArgs x, FoldShape f, uint32_t slope_programs)
 {

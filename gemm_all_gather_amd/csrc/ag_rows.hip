@@ -278,8 +278,10 @@ __global__ __launch_bounds__(group_threads(G)) void ag_rows_kernel(RowsArgs a)
     }
 }
 
-// Longer rows: a workgroup reads its row twice, the second time from the caches, for no CU's registers hold it.  Bound by memory
-// and by those second reads, 3.6 TB/s of what has to move.
+// Longer rows: a workgroup reads its row twice, the second time from the caches.  Its registers do not hold the row beside the weight
+// and the products (1024 threads with four vectors: 4000 x 20000 185 us, read twice 164); LDS would hold 16-bit rows of up to 80000,
+// and holds none here.  Bound by memory and by those second reads: with residual and codes bf16 4000 x 20000 156 us, 2000 x 40000 149, 3.6 to
+// 3.8 TB/s of what has to move; codes alone of 2000 x 40000 bf16 64 us, fp32 108, 3.7.
 constexpr int kLongThreads = 1024;
 template <int DTYPE, bool NORM>
 __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
@@ -366,7 +368,8 @@ __global__ __launch_bounds__(kLongThreads) void ag_rows_long_kernel(RowsArgs a)
     }
 }
 
-// Bound by memory: 16384 x 8192 to bf16 60 us (403 MB, 6.7 TB/s).
+// Bound by memory: 16384 x 8192 to bf16 60 us (403 MB, 6.7 TB/s), a call 70; to fp32 165 (671 MB, 4.1 TB/s; a wave's
+// store leaves every other 16 bytes to its next one).
 template <int DTYPE>
 __global__ __launch_bounds__(256) void ag_dequantize_kernel(DequantizeArgs a)
 {
@@ -594,7 +597,8 @@ __global__ __launch_bounds__(256) void ag_norm_backward_small_kernel(NormBackwar
     else backward_weight<BF16>(a, d, p - dx_programs, part);
 }
 
-// Longer rows in two passes: mean(g n) of each row, and then columns, 8 to a thread, over `rows` rows each.
+// Longer rows in two passes: mean(g n) of each row, and then columns, 8 to a thread, over `rows` rows each.  Bound by memory, dy and h
+// read twice: bf16 with dh and dw in fp32 4000 x 20000 198 us, 2000 x 40000 201 (3.2 TB/s of what has to move, 4.9 of what does).
 template <bool BF16>
 __global__ __launch_bounds__(kLongThreads) void ag_norm_backward_mean_kernel(NormBackwardArgs a)
 {
